@@ -454,16 +454,11 @@ def _plain_beam(s, c):
     m = x.amax(1, keepdim=True)
     m = torch.where(m == NEG, 0.0, m)
     z = (x - m).exp().sum(1, keepdim=True).log()
-    kk = min(k, V)
-    top = torch.topk((_order(x) << 32) + (V - 1 - token), kk, 1)  # a row's best: by value, equal ones by token
-    tok = top.indices
-    best = x.gather(1, tok)
-    score = torch.where(best == NEG, NEG, s["score"][:, None] + ((best - m) - z))
-    score = score.view(c["batch"], n * kk)
-    at = torch.arange(n * kk, device=DEV)
-    pick = torch.topk((_order(score) << 32) + (n * kk - 1 - at), k, 1).indices
-    parent = (pick // kk + torch.arange(c["batch"], device=DEV)[:, None] * n).to(torch.int32)
-    token = tok.view(c["batch"], n * kk).gather(1, pick).to(torch.int32)
+    score = torch.where(x == NEG, NEG, s["score"][:, None] + ((x - m) - z)).view(c["batch"], n * V)
+    at = torch.arange(n * V, device=DEV)
+    pick = torch.topk((_order(score) << 32) + (n * V - 1 - at), k, 1).indices  # equal scores: by row, then token
+    parent = (pick // V + torch.arange(c["batch"], device=DEV)[:, None] * n).to(torch.int32)
+    token = (pick % V).to(torch.int32)
     done = (s["done"][parent.long()].bool() | (token == 2)).to(torch.uint8)
     return {"score": score.gather(1, pick), "parent": parent, "token": token, "done": done}
 
