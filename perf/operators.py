@@ -1,6 +1,7 @@
 """Cases of the operators around a paged key/value cache: what serves a decode round beside its matrix products.
 
-Five operators over one cache (K pages [kv head][token][dim], V pages [kv head][dim][token]):
+Five operators over one cache (K pages [kv head][token][dim], V pages
+[kv head][token / 16][dim][token % 16]):
 
 * ``append``: the rows of a qkv product get rotary positions (one to three axes); q comes back, k and v go into the cache;
 * ``attention``: each row attends to its lane's context and to the drafted tokens its mask word names;
@@ -163,7 +164,7 @@ K_SCALE, V_SCALE = 0.07, 0.055
 def _cache(g, c, layers, pages):
     """K and V pages and their scales; an 8-bit cache stands for E4M3 values times its scale."""
     k = _randn(g, layers, pages, c["kv_heads"], c["page"], c["dim"])
-    v = _randn(g, layers, pages, c["kv_heads"], c["dim"], c["page"])
+    v = _randn(g, layers, pages, c["kv_heads"], c["page"] // 16, c["dim"], 16)
     if c.get("cache") == "e4m3":
         return (k.float() / K_SCALE).to(torch.float8_e4m3fn), (v.float() / V_SCALE).to(torch.float8_e4m3fn), K_SCALE, V_SCALE
     return k, v, 1.0, 1.0
@@ -317,9 +318,9 @@ def _plain_attention(s, c):
     table = s["table"].clamp(min=0).long()
     n = table.shape[1] * P
     k = s["k"][0].view(torch.uint8)[table].view(s["k"].dtype).float() * s["ks"]  # [lanes, pages, heads, P, D]
-    v = s["v"][0].view(torch.uint8)[table].view(s["v"].dtype).float() * s["vs"]  # [lanes, pages, heads, D, P]
+    v = s["v"][0].view(torch.uint8)[table].view(s["v"].dtype).float() * s["vs"]  # [lanes, pages, heads, P / 16, D, 16]
     k = k.permute(0, 2, 1, 3, 4).reshape(lanes, Hk, n, D)
-    v = v.permute(0, 2, 1, 4, 3).reshape(lanes, Hk, n, D)
+    v = v.permute(0, 2, 1, 3, 5, 4).reshape(lanes, Hk, n, D)
     t = torch.arange(T, device=DEV)
     row = s["start"][:-1, None].long() + t  # [lanes, T]
     real = row < s["start"][1:, None]
@@ -347,11 +348,11 @@ def _rows_at(s, real, total):
     return lane * real.shape[1] + torch.arange(total, device=DEV) - s["start"][lane]
 
 
-def _store(cache, page, heads_first, value):
-    """cache[page, ...] = value by the cache's bytes (8-bit types have no indexed store)."""
+def _store(cache, at, value):
+    """cache[at] = value by the cache's bytes (8-bit types have no indexed store)."""
     b = cache.view(torch.uint8) if cache.element_size() == 1 else cache
     v = value.clamp(-448, 448).to(cache.dtype).view(torch.uint8) if cache.element_size() == 1 else value.to(cache.dtype)
-    b[page + heads_first] = v
+    b[at] = v
 
 
 def _plain_append(s, c):
@@ -372,8 +373,8 @@ def _plain_append(s, c):
     at = s["ctx"][lane] + torch.arange(total, device=DEV) - s["start"][lane]
     page, off = s["table"][lane, at // P].long()[:, None], (at % P)[:, None].long()
     head = torch.arange(Hk, device=DEV)[None]
-    _store(s["k"][0], (page, head, off), (), h[:, Hq:] / s["ks"])
-    _store(s["v"][0], (page, head, slice(None), off), (), x[:, Hq + Hk:] / s["vs"])
+    _store(s["k"][0], (page, head, off), h[:, Hq:] / s["ks"])
+    _store(s["v"][0], (page, head, off // 16, slice(None), off % 16), x[:, Hq + Hk:] / s["vs"])
     return {"q": h[:, :Hq].to(torch.bfloat16).reshape(total, Hq * D), "k": s["k"], "v": s["v"]}
 
 
@@ -432,9 +433,9 @@ def _plain_compact(s, c):
     a, b = s["table"].gather(1, (src // P).long()).long(), s["table"].gather(1, (dst // P).long()).long()
     k, v = (t.view(torch.uint8) if t.element_size() == 1 else t for t in (s["k"], s["v"]))
     so, do = (src % P).long(), (dst % P).long()
-    kk, vv = k[:, a, :, so], v[:, a, :, :, so]
+    kk, vv = k[:, a, :, so], v[:, a, :, so // 16, :, so % 16]
     k[:, b, :, do] = kk
-    v[:, b, :, :, do] = vv
+    v[:, b, :, do // 16, :, do % 16] = vv
     return {"k": s["k"], "v": s["v"]}
 
 
@@ -519,7 +520,8 @@ def exact(case, seed):
             for j in range(n):  # ascending, and path[j] >= j: a source is read before it is written
                 a, b = ctx[i] + path[i][j], ctx[i] + j
                 k[:, table[i][b // P], :, b % P] = k[:, table[i][a // P], :, a % P].clone()
-                v[:, table[i][b // P], :, :, b % P] = v[:, table[i][a // P], :, :, a % P].clone()
+                to, of = b % P, a % P
+                v[:, table[i][b // P], :, to // 16, :, to % 16] = v[:, table[i][a // P], :, of // 16, :, of % 16].clone()
         return {"k": k.to(s["k"].dtype), "v": v.to(s["v"].dtype)}
     start = s["start"].cpu().tolist()
     Hk, D = c["kv_heads"], c["dim"]
@@ -540,7 +542,7 @@ def exact(case, seed):
             for t in range(start[i + 1] - start[i]):
                 r, at = start[i] + t, ctx[i] + t
                 k[0, table[i][at // P], :, at % P] = h[r, Hq:] / s["ks"]
-                v[0, table[i][at // P], :, :, at % P] = x[r, Hq + Hk:] / s["vs"]
+                v[0, table[i][at // P], :, at % P // 16, :, at % 16] = x[r, Hq + Hk:] / s["vs"]
         return {"q": h[:, :Hq].reshape(-1, Hq * D), "k": k, "v": v}
     G = c["q_heads"] // Hk
     outs, lses = [], []
@@ -549,7 +551,7 @@ def exact(case, seed):
         n = ctx[i] + t
         pages = torch.tensor(table[i][:-(-n // P)], device=DEV)
         k = (s["k"][0].view(torch.uint8)[pages].view(s["k"].dtype).to(f64) * s["ks"]).transpose(1, 2).reshape(-1, Hk, D)[:n]
-        v = (s["v"][0].view(torch.uint8)[pages].view(s["v"].dtype).to(f64) * s["vs"]).permute(0, 3, 1, 2).reshape(-1, Hk, D)[:n]
+        v = (s["v"][0].view(torch.uint8)[pages].view(s["v"].dtype).to(f64) * s["vs"]).permute(0, 2, 4, 1, 3).reshape(-1, Hk, D)[:n]
         q = s["q"][start[i]:start[i + 1]].to(f64).view(t, Hk, G, D)
         words = s["mask"][start[i]:start[i + 1]].cpu().tolist()
         seen = torch.ones(t, n, dtype=torch.bool)
