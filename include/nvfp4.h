@@ -80,8 +80,12 @@ enum nvfp4_prefill_schedule {
                                    units is finished by the last */
 };
 
-/* Largest k of nvfp4_topk. */
+/* Largest k of nvfp4_topk and nvfp4_beam_select. */
 #define NVFP4_TOPK_MAX_K 64
+/* Largest number of drafted tokens of one lane in one call (bits of a mask word). */
+#define NVFP4_TREE_MAX_ROWS 64
+/* Largest number of beams of one request. */
+#define NVFP4_BEAM_MAX_BEAMS 64
 
 /* ---- status ----------------------------------------------------------------- */
 
@@ -355,6 +359,172 @@ int nvfp4_swiglu(const uint16_t* gate_up_dev, int M, int F, uint16_t* out_dev, v
 size_t nvfp4_topk_workspace_bytes(int M, int V, int k);
 int nvfp4_topk(const float* logits_dev, int M, int V, int ld, int k, int* idx_dev,
                float* val_dev, void* workspace_dev, size_t workspace_bytes, void* stream);
+
+/* ---- paged key/value cache ---------------------------------------------------- */
+
+/* The decode lanes of the reference engine keep their keys and values in one
+ * pool of pages with a fixed budget ("Models and artifacts", "What differs, side
+ * by side": eight lanes; "Ignis" README, "What sets it apart": prefixes are
+ * cloned on the device).  The pages' own 8-bit format is not stated; here a
+ * cache holds bf16, or E4M3 with one fp32 scale for K and one for V.
+ *
+ * A cache is the caller's memory: `layers` x `pages` pages of `page_tokens`
+ * tokens each, K and V apart.  Within a page
+ *   K: [kv_heads][page_tokens][head_dim]
+ *   V: [kv_heads][page_tokens / 16][head_dim][16]
+ * (V in blocks of 16 tokens, dim-major: the attention kernel reads both as they
+ * lie, a block of either being one run of 16 * head_dim values).  Page p of
+ * layer l starts at l * layer_stride + p * page_stride bytes.
+ *
+ * A lane's tokens are named by its row of a page table, int32 [lanes][table_ld]:
+ * token t lies in page table[lane][t / page_tokens].  An entry outside
+ * [0, pages) names no page: tokens there are seen by nobody and stored nowhere.
+ * All tables, lengths and starts are device arrays, so a call under graph
+ * capture follows the values that are there when the graph runs.
+ *
+ * Limits: head_dim 64, 128 or 256; page_tokens 16, 32, 64, 128 or 256;
+ * kv_heads up to 1024; table_ld * page_tokens up to 2^30; pointers and strides
+ * multiples of 16 bytes.  Offsets are 64 bits wide. */
+enum nvfp4_cache_dtype { NVFP4_CACHE_BF16 = 0, NVFP4_CACHE_E4M3 = 1 };
+
+typedef struct nvfp4_cache {
+    void* k_dev;
+    void* v_dev;
+    int layers, pages, kv_heads, page_tokens, head_dim;
+    int dtype;             /* nvfp4_cache_dtype */
+    float k_scale, v_scale; /* E4M3: a byte stands for scale * E4M3; unused for bf16 */
+    int64_t page_stride;   /* bytes; 0: pages are dense */
+    int64_t layer_stride;  /* bytes; 0: pages * page_stride */
+} nvfp4_cache;
+
+/* Rotary positions.  Pair i < pairs of a head, dims (i, i + pairs), or
+ * (2 i, 2 i + 1) if interleaved, of a row at position p turns by a = p * inv_freq[i]:
+ *   (x, y) -> factor * (x cos a - y sin a, x sin a + y cos a);
+ * the dims past 2 * pairs stay.  A row has one position per axis (1 for text, 3
+ * for time, height and width), and pair i turns with axis pair_axis[i].  a is
+ * formed and reduced in fp64. */
+typedef struct nvfp4_rotary {
+    const int* positions_dev;     /* [rows][axes] */
+    const float* inv_freq_dev;    /* [pairs] */
+    const uint8_t* pair_axis_dev; /* [pairs], values below axes; NULL: axis 0 */
+    int axes;                     /* 1..8 */
+    int pairs;                    /* a multiple of 4, up to head_dim / 2; 0: no rotation */
+    int interleaved;
+    float factor;                 /* on cosine and sine (1, or a long-context scaling) */
+} nvfp4_rotary;
+
+/* The step between a qkv product and the attention: rotates q and k, writes q to
+ * q_out and k, v into one layer of the cache.  qkv_dev: bf16 [rows][qkv_ld], a row
+ * holding q_heads, then kv_heads k, then kv_heads v heads of head_dim.  Rows
+ * row_start[b] .. row_start[b + 1] - 1 are lane b's (row_start: int32
+ * [lanes + 1], ascending from 0); row row_start[b] + t goes to token
+ * ctx_len[b] + t of the lane.  q_out_dev: bf16 [rows][q_ld], may be qkv_dev itself
+ * with q_ld = qkv_ld.  Values are computed in fp32 and rounded once, to
+ * nearest even: to bf16, or x / scale to E4M3 (saturating at 448).  No two lanes may share
+ * a page that is written.  qkv_ld, q_ld multiples of 4, pointers 8-byte aligned.
+ * Asynchronous on `stream`. */
+int nvfp4_cache_append(const nvfp4_cache* cache, int layer, const uint16_t* qkv_dev, int64_t qkv_ld,
+                       int rows, int q_heads, int lanes, const int* row_start_dev,
+                       const int* ctx_len_dev, const int* page_table_dev, int table_ld,
+                       const nvfp4_rotary* rotary, uint16_t* q_out_dev, int64_t q_ld, void* stream);
+
+/* Mask words of a tree of n <= 64 drafted tokens (host): parent[i] < i is the
+ * token that i continues, -1 for one that continues the context.  mask[i] has the
+ * bits of i and its ancestors; depth[i] (may be NULL) counts the ancestors, so
+ * token i's position is the context's length + depth[i]. */
+int nvfp4_tree_mask(const int* parent, int n, uint64_t* mask, int* depth);
+
+/* Attention of drafted tokens ("Ignis" README, "Speculative decoding (DFlash2)":
+ * up to seven drafts per lane are checked in the same pass).  Row t of lane b
+ * (rows as in nvfp4_cache_append, already appended) sees the lane's tokens
+ * p < ctx_len[b], and of its row_start[b + 1] - row_start[b] drafted tokens
+ * ctx_len[b] + j those whose bit j is set in mask[row].  One row per lane with
+ * mask 1 is a decode step; a chain of drafts has mask (2 << t) - 1.
+ *   out[row][head] = sum_p w_p v_p / sum_p w_p,  w_p = exp(scale * q . k_p)
+ *   lse[row][head] = log sum_p w_p   (if lse_dev is not NULL)
+ * q head i uses kv head i / (q_heads / kv_heads).  A row that sees nothing gives
+ * 0 and -inf.  q_dev: bf16 [rows][q_ld]; out_dev: bf16 [rows][out_ld]; lse_dev: fp32
+ * [rows][q_heads].  max_rows (up to 64): an upper bound of a lane's rows; rows past it
+ * are not computed.  Tokens past a lane's last row, and those in missing pages, may hold
+ * anything, NaN included; a drafted token that only some rows see must be
+ * finite.  Products of bf16 (E4M3 is exact in it) are summed in fp32; the
+ * weights enter the second product with 16 significant bits.  The split over
+ * the context depends on the lengths, not on timing: repeated calls agree to
+ * the bit.
+ *   workspace_dev: nvfp4_tree_attention_workspace_bytes bytes (16-byte aligned), any
+ *   content; owned by the call while it runs.
+ * q_ld a multiple of 8 and q 16-byte aligned; out_ld a multiple of 4 and out 8-byte
+ * aligned.  Asynchronous on `stream`. */
+size_t nvfp4_tree_attention_workspace_bytes(int q_heads, int kv_heads, int head_dim, int max_rows);
+int nvfp4_tree_attention(const nvfp4_cache* cache, int layer, const uint16_t* q_dev, int64_t q_ld,
+                         int q_heads, int lanes, int max_rows, const int* row_start_dev,
+                         const int* ctx_len_dev, const int* page_table_dev, int table_ld,
+                         const uint64_t* mask_dev, float scale, uint16_t* out_dev, int64_t out_ld,
+                         float* lse_dev, void* workspace_dev, size_t workspace_bytes, void* stream);
+
+/* After a round accepted drafts: in every layer, token ctx_len[b] + path[b][j]
+ * moves to ctx_len[b] + j for j < accepted[b] (path: int32 [lanes][path_ld], at
+ * most 64 entries of a row are used; entries outside [0, 64) and tokens in missing
+ * pages are skipped).  All sources of a lane are read before any is written.
+ * Asynchronous on `stream`. */
+int nvfp4_cache_compact(const nvfp4_cache* cache, int lanes, const int* ctx_len_dev,
+                        const int* page_table_dev, int table_ld, const int* path_dev, int path_ld,
+                        const int* accepted_dev, void* stream);
+
+/* New page tables from old ones: reordering after a beam selection, forking,
+ * truncation, freeing and making room, in one step on the device.
+ *
+ * An old row holds each page that its entries name; refs_in[p] counts the holders
+ * of page p (rows of table_in, and any others the caller knows of).
+ * New lane i continues old lane parent[i] (outside [0, lanes_in): a lane that
+ * starts empty) with its first n = min(keep[i], len_in[parent[i]]) tokens (keep NULL: all)
+ * and gets room for reserve[i] more (NULL: none):
+ *  - it inherits the entries of those n tokens;
+ *  - if n ends inside a page, that page must become the lane's own: it stays if all of
+ *    its holders are new lanes for which it is that last page and i is the lowest of
+ *    them, and is copied to a fresh page otherwise (whole pages, every layer);
+ *  - the entries up to ceil((n + reserve) / page_tokens), at most table_ld, are fresh
+ *    pages;
+ *  - the others are -1, and the lane's old reserve is given back.
+ * Fresh pages are the lowest-numbered ones that nobody holds, handed out by
+ * ascending lane, a lane's copy before its reserve; where none is left the entry
+ * is -1 (a lane that finds none for its copy loses that page's tokens).
+ * Writes table_out [lanes_out][table_ld], len_out [lanes_out] (n), refs_out
+ * [cache->pages] and short_dev[0], the number of entries that found no page.
+ * Outputs must not overlap inputs.  The answer is unique.
+ *   workspace_dev: nvfp4_cache_update_workspace_bytes bytes (16-byte aligned), any
+ *   content; owned by the call while it runs.
+ * Asynchronous on `stream`. */
+size_t nvfp4_cache_update_workspace_bytes(int pages, int lanes_out, int table_ld);
+int nvfp4_cache_update(const nvfp4_cache* cache, int lanes_in, const int* table_in_dev,
+                       const int* len_in_dev, const int* refs_in_dev, int table_ld, int lanes_out,
+                       const int* parent_dev, const int* keep_dev, const int* reserve_dev,
+                       int* table_out_dev, int* len_out_dev, int* refs_out_dev, int* short_dev,
+                       void* workspace_dev, size_t workspace_bytes, void* stream);
+
+/* ---- beam selection ---------------------------------------------------------- */
+
+/* The head's logits, fp32 or bf16 (logits_dtype: nvfp4_out_dtype) [batch * beams][ld],
+ * of `batch` requests with `beams` rows each and running scores score [batch * beams]:
+ *   s[row][v] = score[row] + ((x[row][v] - max) - log sum exp(x[row] - max))   (fp32)
+ * and of each request's beams x V candidates the k best, in descending order, equal
+ * ones by ascending row, then token:
+ *   score_out [batch][k], parent [batch][k] (global row: batch index * beams + beam,
+ *   as nvfp4_cache_update takes it), token [batch][k], and, if done_out_dev is not
+ *   NULL, done_out [batch][k] = done[parent] or token == eos.
+ * A row with done[row] != 0 (done_dev may be NULL) has one candidate, token eos at
+ * its own score; every other candidate of it, every candidate of a row with score
+ * -inf, and every logit of -inf has score -inf.  +inf and NaN logits and NaN scores are out of
+ * contract.  1 <= beams <= 64, 1 <= k <= min(V, 64), ld >= V, V * beams <= 2^31 - 1025; logits
+ * aligned to their type (16-byte aligned rows are read in vectors).
+ *   workspace_dev: nvfp4_beam_workspace_bytes bytes (16-byte aligned), any content;
+ *   owned by the call while it runs.
+ * Outputs must not overlap inputs.  Asynchronous on `stream`. */
+size_t nvfp4_beam_workspace_bytes(int batch, int beams, int V);
+int nvfp4_beam_select(const void* logits_dev, int logits_dtype, int64_t ld, int batch, int beams, int V,
+                      const float* score_dev, const uint8_t* done_dev, int eos, int k,
+                      float* score_out_dev, int* parent_dev, int* token_dev, uint8_t* done_out_dev,
+                      void* workspace_dev, size_t workspace_bytes, void* stream);
 
 /* ---- measurement ------------------------------------------------------------- */
 

@@ -35,8 +35,14 @@ EXPORTS = (
     "nvfp4_round_workspace_bytes", "nvfp4_round_create", "nvfp4_round_run",
     "nvfp4_round_graph_nodes", "nvfp4_round_destroy",
     "nvfp4_topk_workspace_bytes", "nvfp4_topk", "nvfp4_swiglu", "nvfp4_stream_read",
+    "nvfp4_cache_append", "nvfp4_cache_compact", "nvfp4_cache_update",
+    "nvfp4_cache_update_workspace_bytes", "nvfp4_tree_mask", "nvfp4_tree_attention",
+    "nvfp4_tree_attention_workspace_bytes", "nvfp4_beam_select", "nvfp4_beam_workspace_bytes",
 )
 TOPK_MAX_K = 64
+TREE_MAX_ROWS = 64
+BEAM_MAX_BEAMS = 64
+CACHE_BF16, CACHE_E4M3 = 0, 1
 
 
 class Nvfp4Error(RuntimeError):
@@ -67,6 +73,22 @@ class Layer(ctypes.Structure):
 
 
 ACT_INPUT, ACT_SWIGLU_PREV = 0, 1
+
+
+class Cache(ctypes.Structure):
+    _fields_ = [("k_dev", ctypes.c_void_p), ("v_dev", ctypes.c_void_p),
+                ("layers", ctypes.c_int), ("pages", ctypes.c_int), ("kv_heads", ctypes.c_int),
+                ("page_tokens", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("k_scale", ctypes.c_float),
+                ("v_scale", ctypes.c_float), ("page_stride", ctypes.c_int64),
+                ("layer_stride", ctypes.c_int64)]
+
+
+class Rotary(ctypes.Structure):
+    _fields_ = [("positions_dev", ctypes.c_void_p), ("inv_freq_dev", ctypes.c_void_p),
+                ("pair_axis_dev", ctypes.c_void_p), ("axes", ctypes.c_int),
+                ("pairs", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("factor", ctypes.c_float)]
 
 
 _lib = None
@@ -117,6 +139,23 @@ def lib():
         L.nvfp4_topk.argtypes = [vp, i, i, i, i, vp, vp, vp, sz, vp]
         L.nvfp4_swiglu.argtypes = [vp, i, i, vp, vp]
         L.nvfp4_stream_read.argtypes = [vp, sz, vp, vp]
+        i64, f = c.c_int64, c.c_float
+        L.nvfp4_cache_append.argtypes = [c.POINTER(Cache), i, vp, i64, i, i, i, vp, vp, vp, i,
+                                         c.POINTER(Rotary), vp, i64, vp]
+        L.nvfp4_cache_compact.argtypes = [c.POINTER(Cache), i, vp, vp, i, vp, i, vp, vp]
+        L.nvfp4_cache_update_workspace_bytes.argtypes = [i, i, i]
+        L.nvfp4_cache_update_workspace_bytes.restype = sz
+        L.nvfp4_cache_update.argtypes = [c.POINTER(Cache), i, vp, vp, vp, i, i, vp, vp, vp, vp,
+                                         vp, vp, vp, vp, sz, vp]
+        L.nvfp4_tree_mask.argtypes = [c.POINTER(i), i, c.POINTER(c.c_uint64), c.POINTER(i)]
+        L.nvfp4_tree_attention_workspace_bytes.argtypes = [i, i, i, i]
+        L.nvfp4_tree_attention_workspace_bytes.restype = sz
+        L.nvfp4_tree_attention.argtypes = [c.POINTER(Cache), i, vp, i64, i, i, i, vp, vp, vp, i,
+                                           vp, f, vp, i64, vp, vp, sz, vp]
+        L.nvfp4_beam_workspace_bytes.argtypes = [i, i, i]
+        L.nvfp4_beam_workspace_bytes.restype = sz
+        L.nvfp4_beam_select.argtypes = [vp, i, i64, i, i, i, vp, vp, i, i, vp, vp, vp, vp, vp, sz,
+                                        vp]
         for name in EXPORTS:
             getattr(L, name)
         _lib = L
@@ -220,6 +259,96 @@ def topk(logits, k, stream=None):
     ws = torch.empty(max(wsb, 16), dtype=torch.uint8, device=logits.device) if wsb else None
     nvfp4_topk(logits, M, V, logits.stride(0), k, idx, val, ws, wsb, stream)
     return idx, val
+
+
+def nvfp4_cache_append(cache, layer, qkv, qkv_ld, rows, q_heads, lanes, row_start, ctx_len,
+                       page_table, table_ld, rotary, q_out, q_ld, stream=None):
+    _check(lib().nvfp4_cache_append(ctypes.byref(cache), layer, _ptr(qkv), qkv_ld, rows, q_heads,
+                                    lanes, _ptr(row_start), _ptr(ctx_len), _ptr(page_table),
+                                    table_ld, ctypes.byref(rotary), _ptr(q_out), q_ld,
+                                    _stream(stream)))
+
+
+def nvfp4_cache_compact(cache, lanes, ctx_len, page_table, table_ld, path, path_ld, accepted,
+                        stream=None):
+    _check(lib().nvfp4_cache_compact(ctypes.byref(cache), lanes, _ptr(ctx_len), _ptr(page_table),
+                                     table_ld, _ptr(path), path_ld, _ptr(accepted),
+                                     _stream(stream)))
+
+
+def nvfp4_cache_update_workspace_bytes(pages, lanes_out, table_ld) -> int:
+    return lib().nvfp4_cache_update_workspace_bytes(pages, lanes_out, table_ld)
+
+
+def nvfp4_cache_update(cache, lanes_in, table_in, len_in, refs_in, table_ld, lanes_out, parent,
+                       keep, reserve, table_out, len_out, refs_out, short, workspace,
+                       workspace_bytes, stream=None):
+    _check(lib().nvfp4_cache_update(ctypes.byref(cache), lanes_in, _ptr(table_in), _ptr(len_in),
+                                    _ptr(refs_in), table_ld, lanes_out, _ptr(parent), _ptr(keep),
+                                    _ptr(reserve), _ptr(table_out), _ptr(len_out),
+                                    _ptr(refs_out), _ptr(short), _ptr(workspace),
+                                    workspace_bytes, _stream(stream)))
+
+
+def nvfp4_tree_mask(parent):
+    """(mask words, depths) of a tree given by each drafted token's parent (-1: the context);
+    mask words as signed 64-bit integers, the type a mask tensor has."""
+    n = len(parent)
+    p = (ctypes.c_int * max(n, 1))(*parent)
+    mask, depth = (ctypes.c_uint64 * max(n, 1))(), (ctypes.c_int * max(n, 1))()
+    _check(lib().nvfp4_tree_mask(p, n, mask, depth))
+    return [m - (1 << 64) if m >> 63 else m for m in mask], list(depth)
+
+
+def nvfp4_tree_attention_workspace_bytes(q_heads, kv_heads, head_dim, max_rows) -> int:
+    return lib().nvfp4_tree_attention_workspace_bytes(q_heads, kv_heads, head_dim, max_rows)
+
+
+def nvfp4_tree_attention(cache, layer, q, q_ld, q_heads, lanes, max_rows, row_start, ctx_len,
+                         page_table, table_ld, mask, scale, out, out_ld, lse, workspace,
+                         workspace_bytes, stream=None):
+    _check(lib().nvfp4_tree_attention(ctypes.byref(cache), layer, _ptr(q), q_ld, q_heads, lanes,
+                                      max_rows, _ptr(row_start), _ptr(ctx_len),
+                                      _ptr(page_table), table_ld, _ptr(mask), scale, _ptr(out),
+                                      out_ld, _ptr(lse), _ptr(workspace), workspace_bytes,
+                                      _stream(stream)))
+
+
+def nvfp4_beam_workspace_bytes(batch, beams, V) -> int:
+    return lib().nvfp4_beam_workspace_bytes(batch, beams, V)
+
+
+def nvfp4_beam_select(logits, logits_dtype, ld, batch, beams, V, score, done, eos, k, score_out,
+                      parent, token, done_out, workspace, workspace_bytes, stream=None):
+    _check(lib().nvfp4_beam_select(_ptr(logits), logits_dtype, ld, batch, beams, V, _ptr(score),
+                                   _ptr(done), eos, k, _ptr(score_out), _ptr(parent),
+                                   _ptr(token), _ptr(done_out), _ptr(workspace),
+                                   workspace_bytes, _stream(stream)))
+
+
+def beam_select(logits, beams, score, k, done=None, eos=-1, stream=None):
+    """The k best continuations of each request: (score fp32, parent int32, token int32, done
+    uint8), each [requests][k], of a device fp32 or bf16 logits tensor [requests * beams][V]."""
+    import torch
+    rows, V = logits.shape
+    batch = rows // beams
+    _expect(rows == batch * beams, "logits: %d rows are not a multiple of %d beams" % (rows, beams))
+    _expect(logits.dtype in (torch.float32, torch.bfloat16), "logits: not float32 or bfloat16")
+    _expect(logits.stride(1) == 1 or V == 1, "logits: rows are not contiguous")
+    _vector(score, torch.float32, rows, "score")
+    if done is not None:
+        _vector(done, torch.uint8, rows, "done")
+    dev = logits.device
+    out = torch.empty((batch, k), dtype=torch.float32, device=dev)
+    parent = torch.empty((batch, k), dtype=torch.int32, device=dev)
+    token = torch.empty((batch, k), dtype=torch.int32, device=dev)
+    ended = torch.empty((batch, k), dtype=torch.uint8, device=dev)
+    wsb = nvfp4_beam_workspace_bytes(batch, beams, V)
+    ws = torch.empty(max(wsb, 16), dtype=torch.uint8, device=dev)
+    nvfp4_beam_select(logits, OUT_F32 if logits.dtype == torch.float32 else OUT_BF16,
+                      logits.stride(0) if rows > 1 else max(logits.stride(0), V), batch, beams, V,
+                      score, done, eos, k, out, parent, token, ended, ws, wsb, stream)
+    return out, parent, token, ended
 
 
 def nvfp4_gemm_create(max_M, K, N, out_dtype, split_k=0, waves=0, chunks=0, windows=0,
@@ -339,6 +468,155 @@ class PackedWeight:
         if keep_canonical:
             pw.canonical = (codes, scales)
         return pw
+
+
+def _expect(ok, message):
+    if not ok:
+        raise Nvfp4Error(EINVAL, message)
+
+
+def _vector(x, dtype, n, name):
+    """A contiguous device vector of n values of a type."""
+    _expect(x.dtype == dtype, "%s: not %s" % (name, dtype))
+    _expect(x.numel() == n and x.is_contiguous(), "%s: not %d contiguous values" % (name, n))
+
+
+def _rows(x, dtype, width, name):
+    """Leading dimension of a matrix of rows of at least `width` contiguous values."""
+    _expect(x.dtype == dtype and x.dim() == 2, "%s: not a %s matrix" % (name, dtype))
+    _expect(x.shape[1] >= width and x.stride(1) == 1, "%s: rows are not %d contiguous values" % (name, width))
+    return x.stride(0) if x.shape[0] > 1 else max(x.stride(0), x.shape[1])
+
+
+class PagedCache:
+    """A paged key/value cache over the caller's tensors and the operators on it.
+
+    ``k``: [layers][pages][kv_heads][page_tokens][head_dim]; ``v``: [layers][pages][kv_heads]
+    [page_tokens / 16][head_dim][16]; bfloat16, or float8_e4m3fn standing for ``scale`` times its
+    value.  A page is contiguous; layers and pages may have other strides (equal ones for k and v).
+
+    ``row_start`` (int32 [lanes + 1]), ``ctx_len`` (int32 [lanes]) and ``page_table`` (int32
+    [lanes][pages of a lane]) are device tensors; include/nvfp4.h has the rules of each call.
+    Workspaces come from torch's allocator on the current stream, call by call.
+    """
+
+    def __init__(self, k, v, k_scale=1.0, v_scale=1.0):
+        import torch
+        _expect(k.dim() == 5 and v.dim() == 6, "k, v: not 5 and 6 dimensions")
+        layers, pages, heads, tokens, dim = k.shape
+        _expect(tuple(v.shape) == (layers, pages, heads, tokens // 16, dim, 16),
+                "v: shape %s does not go with k's %s" % (tuple(v.shape), tuple(k.shape)))
+        _expect(k.dtype == v.dtype and k.dtype in (torch.bfloat16, torch.float8_e4m3fn),
+                "k, v: not both bfloat16 or float8_e4m3fn")
+        dense = (tokens * dim, dim, 1), (tokens * dim, 16 * dim, 16, 1)
+        for x, want, name in ((k, dense[0], "k"), (v, dense[1], "v")):
+            _expect(all(n == 1 or a == b for n, a, b in zip(x.shape[2:], x.stride()[2:], want)),
+                    "%s: a page is not contiguous" % name)
+        es = k.element_size()
+        strides = [0 if n == 1 else s * es for n, s in zip(k.shape[:2], k.stride()[:2])]
+        _expect(strides == [0 if n == 1 else s * es for n, s in zip(v.shape[:2], v.stride()[:2])],
+                "k, v: layers or pages have different strides")
+        if pages == 1 and layers > 1 and strides[0]:
+            strides[1] = 0
+        self.k, self.v = k, v
+        self.layers, self.pages, self.kv_heads, self.page_tokens, self.head_dim = k.shape
+        self.desc = Cache(k.data_ptr(), v.data_ptr(), layers, pages, heads, tokens, dim,
+                          CACHE_BF16 if es == 2 else CACHE_E4M3, float(k_scale), float(v_scale),
+                          strides[1], strides[0])
+
+    def _lanes(self, row_start, ctx_len, page_table):
+        import torch
+        lanes = ctx_len.numel()
+        _vector(ctx_len, torch.int32, lanes, "ctx_len")
+        if row_start is not None:
+            _vector(row_start, torch.int32, lanes + 1, "row_start")
+        ld = _rows(page_table, torch.int32, 1, "page_table")
+        _expect(page_table.shape[0] == lanes, "page_table: %d rows for %d lanes"
+                % (page_table.shape[0], lanes))
+        # a view of wider rows: entries past its own width are not the lane's
+        _expect(ld == page_table.shape[1], "page_table: not contiguous")
+        return lanes, ld
+
+    def append(self, layer, qkv, q_heads, row_start, ctx_len, page_table, positions, inv_freq,
+               pair_axis=None, interleaved=False, factor=1.0, out=None, stream=None):
+        """Rotates q and k of a qkv product's rows, stores k and v, returns q [rows][q_heads * dim]."""
+        import torch
+        rows = qkv.shape[0]
+        lanes, table_ld = self._lanes(row_start, ctx_len, page_table)
+        qkv_ld = _rows(qkv, torch.bfloat16, (q_heads + 2 * self.kv_heads) * self.head_dim, "qkv")
+        pairs = inv_freq.numel()
+        _vector(inv_freq, torch.float32, pairs, "inv_freq")
+        axes = positions.shape[1] if positions.dim() == 2 else 1
+        _vector(positions, torch.int32, rows * axes, "positions")
+        if pair_axis is not None:
+            _vector(pair_axis, torch.uint8, pairs, "pair_axis")
+        if out is None:
+            out = torch.empty((rows, q_heads * self.head_dim), dtype=torch.bfloat16,
+                              device=qkv.device)
+        _expect(out.shape[0] >= rows, "out: %d rows of %d" % (out.shape[0], rows))
+        q_ld = _rows(out, torch.bfloat16, q_heads * self.head_dim, "out")
+        rot = Rotary(positions.data_ptr(), inv_freq.data_ptr(), _ptr(pair_axis), axes, pairs,
+                     int(interleaved), float(factor))
+        nvfp4_cache_append(self.desc, layer, qkv, qkv_ld, rows, q_heads, lanes, row_start, ctx_len,
+                           page_table, table_ld, rot, out, q_ld, stream)
+        return out
+
+    def attend(self, layer, q, row_start, ctx_len, page_table, mask, max_rows, scale, out=None,
+               with_lse=False, stream=None):
+        """Attention of each lane's drafted rows q [rows][q_heads * dim] over its context and the
+        drafts its mask words (int64 [rows]) name; max_rows: at least any lane's rows.  Returns
+        out, or (out, lse fp32 [rows][q_heads])."""
+        import torch
+        rows, width = q.shape
+        dim = self.head_dim
+        q_heads = width // dim
+        lanes, table_ld = self._lanes(row_start, ctx_len, page_table)
+        q_ld = _rows(q, torch.bfloat16, q_heads * dim, "q")
+        _vector(mask, torch.int64, rows, "mask")
+        if out is None:
+            out = torch.empty((rows, q_heads * dim), dtype=torch.bfloat16, device=q.device)
+        _expect(out.shape[0] >= rows, "out: %d rows of %d" % (out.shape[0], rows))
+        out_ld = _rows(out, torch.bfloat16, q_heads * dim, "out")
+        lse = torch.empty((rows, q_heads), dtype=torch.float32, device=q.device) if with_lse else None
+        wsb = nvfp4_tree_attention_workspace_bytes(q_heads, self.kv_heads, dim, max_rows)
+        ws = torch.empty(max(wsb, 16), dtype=torch.uint8, device=q.device)
+        nvfp4_tree_attention(self.desc, layer, q, q_ld, q_heads, lanes, max_rows, row_start,
+                             ctx_len, page_table, table_ld, mask, scale, out, out_ld, lse, ws, wsb,
+                             stream)
+        return (out, lse) if with_lse else out
+
+    def compact(self, ctx_len, page_table, path, accepted, stream=None):
+        """Moves each lane's accepted drafts (path int32 [lanes][n], accepted int32 [lanes]) to the
+        front of its drafted tokens, in every layer."""
+        import torch
+        lanes, table_ld = self._lanes(None, ctx_len, page_table)
+        path_ld = _rows(path, torch.int32, 1, "path")
+        _expect(path.shape[0] == lanes and path_ld == path.shape[1],
+                "path: not %d contiguous rows" % lanes)
+        _vector(accepted, torch.int32, lanes, "accepted")
+        nvfp4_cache_compact(self.desc, lanes, ctx_len, page_table, table_ld, path, path_ld,
+                            accepted, stream)
+
+    def update(self, page_table, length, refs, parent, keep=None, reserve=None, stream=None):
+        """New tables from old ones (reorder, fork, truncate, free, make room): returns
+        (page_table, length, refs, short), all int32; shared partly filled pages are copied."""
+        import torch
+        lanes_in, table_ld = self._lanes(None, length, page_table)
+        lanes_out = parent.numel()
+        _vector(refs, torch.int32, self.pages, "refs")
+        for x, name in ((parent, "parent"), (keep, "keep"), (reserve, "reserve")):
+            if x is not None:
+                _vector(x, torch.int32, lanes_out, name)
+        dev = page_table.device
+        table = torch.empty((lanes_out, table_ld), dtype=torch.int32, device=dev)
+        new_len = torch.empty(lanes_out, dtype=torch.int32, device=dev)
+        new_refs = torch.empty(self.pages, dtype=torch.int32, device=dev)
+        short = torch.empty(1, dtype=torch.int32, device=dev)
+        wsb = nvfp4_cache_update_workspace_bytes(self.pages, lanes_out, table_ld)
+        ws = torch.empty(max(wsb, 16), dtype=torch.uint8, device=dev)
+        nvfp4_cache_update(self.desc, lanes_in, page_table, length, refs, table_ld, lanes_out,
+                           parent, keep, reserve, table, new_len, new_refs, short, ws, wsb, stream)
+        return table, new_len, new_refs, short
 
 
 class Gemm:

@@ -1,0 +1,768 @@
+// Attention of drafted tokens over a paged cache.
+//
+// "Ignis" README, "Speculative decoding (DFlash2)": a lane's drafts are checked
+// in one pass.  Row t of a lane sees the lane's whole context (positions
+// p < ctx) and, of the drafted tokens at positions ctx + j, those whose bit j is
+// set in its mask word, so any tree of drafts takes one call; one row with mask
+// 1 is a plain decode step.
+//
+//     o_t = sum_p w_p v_p / sum_p w_p,   w_p = exp(scale q_t . k_p)
+//
+// One pass with a running maximum.  The q heads that share a kv head are rows
+// of the same product: a lane of T tokens and G heads per kv head has R = T G
+// rows, and each K and V byte is read once for all of them.
+//
+// Operands.  The kernel computes S^T = K Q^T and O^T = V^T P^T with
+// v_mfma_f32_16x16x32_bf16: tokens (then dims) are the M side, rows the N side.
+//  - A lane's K operand is 8 consecutive dims of one token and its V operand 8
+//    consecutive tokens of one dim: 16 bytes of a page as it lies.
+//  - Result lane (g = lane / 16, n = lane % 16) holds rows 4 g + j of row n.  With
+//    the M index 4 c + j of S tile i standing for token 16 c + 4 i + j of a
+//    64-token tile, the lane holds tokens 16 g .. 16 g + 15 of row n after four S
+//    tiles: the k slots 8 g .. 8 g + 7 of two PV steps, with no exchange between
+//    lanes.  Row statistics are one value per lane, and the rescale of O is a
+//    multiplication by it.
+//
+// Staging.  A workgroup's four waves copy a tile's K and V straight into LDS
+// (wave w the w-th 16 tokens: one run of 16 x dim values of each), the next
+// step's copies in flight while the current step is computed.  K segments of 16
+// bytes sit in slots xor-ed with their token, and V segments with their dim, so
+// that the operand reads spread over the banks.
+#include "cache.h"
+#include "decode_device.h"
+
+namespace nvfp4 {
+
+constexpr int kTile = 64;        // tokens per tile
+constexpr int kAttWaves = 4;
+constexpr int kAttThreads = 64 * kAttWaves;
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+// O and the sums are rescaled only when a row's maximum passes the one in use
+// by 2^8: weights stay below 2^8, far from fp32's and bf16's limits.
+constexpr float kRescaleAt = 8.f;
+
+struct AttArgs {
+    CacheView c;  // base pointers of the layer
+    const uint16_t* q;
+    long long q_ld;
+    int q_heads, group;  // group = q_heads / kv_heads
+    int lanes, max_rows;
+    const int* row_start;
+    const int* ctx_len;
+    const int* table;
+    int table_ld;
+    const unsigned long long* mask;
+    float scale2;  // softmax scale x log2(e) x K scale
+    uint16_t* out;
+    long long out_ld;
+    float* lse;  // [rows][q_heads] or null
+    float* part_o;   // [2 x workers][block rows][dim]
+    float2* part_ml; // [2 x workers][block rows]: maximum (log2 units), sum
+    int workers;
+};
+
+// One lane's share of the work: `units` items (kv head x row block) of `tiles`.
+struct LaneWork {
+    int row0, rows, ctx, tokens, blocks, tiles;
+};
+
+__device__ __forceinline__ LaneWork lane_work(const AttArgs& a, int b, int block_rows) {
+    LaneWork w;
+    w.row0 = a.row_start[b];
+    w.rows = min(max(a.row_start[b + 1] - w.row0, 0), a.max_rows);
+    w.ctx = max(a.ctx_len[b], 0);
+    w.tokens = (int)min((long long)w.ctx + w.rows, (long long)a.table_ld << a.c.log_page);
+    w.blocks = (w.rows * a.group + block_rows - 1) / block_rows;
+    w.tiles = w.rows > 0 ? (w.tokens + kTile - 1) / kTile : 0;
+    return w;
+}
+
+// Inclusive sum over the wave's lanes.
+__device__ __forceinline__ long long wave_scan(long long v) {
+    const int l = threadIdx.x & 63;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const long long u = __shfl_up(v, d);
+        v += l >= d ? u : 0;
+    }
+    return v;
+}
+
+// Sum of the tiles of all items of lanes [0, lanes) (or of those before `upto`).
+__device__ __forceinline__ long long total_tiles(const AttArgs& a, int block_rows, int upto) {
+    long long sum = 0;
+    for (int b0 = 0; b0 < upto; b0 += 64) {
+        const int b = b0 + (int)(threadIdx.x & 63);
+        long long v = 0;
+        if (b < upto) {
+            const LaneWork w = lane_work(a, b, block_rows);
+            v = (long long)w.blocks * a.c.kv_heads * w.tiles;
+        }
+        sum += __shfl(wave_scan(v), 63);
+    }
+    return sum;
+}
+
+// Workers that share `total` tiles: enough tiles each that every wave of a
+// workgroup has some.
+__device__ __forceinline__ int active_workers(const AttArgs& a, long long total) {
+    return (int)max(1ll, min((long long)a.workers, total / kAttWaves));
+}
+
+__device__ __forceinline__ bf16x8 bytes8(const uint4& v) {
+    bf16x8 r;
+    __builtin_memcpy(&r, &v, 16);
+    return r;
+}
+
+__device__ __forceinline__ bf16x8 e4m3x8_to_bf16(uint32_t lo, uint32_t hi) {
+    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
+    const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
+    const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
+    const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
+    return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// Keeps the first n of 16 bytes.
+__device__ __forceinline__ uint4 keep_first(uint4 v, int n) {
+    auto part = [](uint32_t w, int m) {
+        return m >= 4 ? w : m <= 0 ? 0u : (w & ((1u << (8 * m)) - 1u));
+    };
+    return make_uint4(part(v.x, n), part(v.y, n - 4), part(v.z, n - 8), part(v.w, n - 12));
+}
+
+// Copies 1024 bytes straight into LDS: lane l's 16 bytes at src + at + off to
+// dst + 16 l; reads past src + bytes give zeros.
+__device__ __forceinline__ void copy_to_lds(uint8_t* src, int bytes, int at, int off, uint8_t* dst) {
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(src, 0, bytes, 0x00020000);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)dst, 16,
+                                             off, at, 0, 0);
+}
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// How the four waves share a block: RW waves split its rows (NR row tiles of 16
+// each), TW the token halves of a tile, DW the dims of O (those repeat S).
+// SPLIT: weights enter the second product as two bf16 numbers.
+template <int D, bool FP8, int NR, int RW, int TW, int DW, bool SPLIT>
+struct AttTraits {
+    static_assert(RW * TW * DW == kAttWaves, "four waves");
+    static constexpr int ES = FP8 ? 1 : 2;
+    static constexpr int kRows = 16 * NR * RW;          // rows of a block
+    static constexpr int kRowBytes = D * ES;            // a token's K
+    static constexpr int kSegs = kRowBytes / 16;
+    static constexpr int kChunk = 16 * kRowBytes;       // 16 tokens of K, or of V
+    static constexpr int kCopies = kChunk / 1024;       // 64 lanes x 16 bytes each
+    static constexpr int kTileBytes = 8 * kChunk;       // K and V of 64 tokens
+    // Tiles per step: 32 KiB in flight per workgroup and step.
+    static constexpr int SUB = kTileBytes >= 32768 ? 1 : 32768 / kTileBytes;
+    static constexpr int kStepBytes = SUB * kTileBytes;
+};
+
+template <int D, bool FP8, int NR, int RW, int TW, int DW, bool SPLIT>
+__global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(AttArgs a) {
+    using T = AttTraits<D, FP8, NR, RW, TW, DW, SPLIT>;
+    constexpr int ES = T::ES, kRows = T::kRows, kSegs = T::kSegs, kChunk = T::kChunk, SUB = T::SUB;
+    constexpr int KS = D / 32;       // K steps of 32 dims
+    constexpr int DB = D / 16 / DW;  // this wave's dim blocks of O
+    constexpr int HH = 2 / TW;       // token halves a wave takes
+    constexpr int KA = kSegs >= 16 ? 4 : kSegs / 4;  // distinct K operand addresses
+    // Two arrays, so that the compiler can tell the copies in flight from the
+    // reads of the other one.
+    __shared__ __align__(16) uint8_t lds0[T::kStepBytes];
+    __shared__ __align__(16) uint8_t lds1[T::kStepBytes];
+    __shared__ float2 lds_ml[TW > 1 ? kRows : 1];
+    static_assert(TW == 1 || (RW <= 2 && NR * 16 * D * 4 <= T::kStepBytes), "sums of a row wave fit");
+
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int lane = threadIdx.x & 63;
+    const int g = lane >> 4, n = lane & 15;
+    const int rw = wave % RW, tw = wave / RW % TW, dw = wave / (RW * TW);
+
+    const long long total = total_tiles(a, kRows, a.lanes);
+    const int active = active_workers(a, total);
+    int worker = blockIdx.x;
+    // Consecutive ranges on one XCD (workgroup b runs on XCD b mod 8), so that
+    // the row blocks of one lane and head share their K and V in its L2.
+    if (active == a.workers) worker = (worker & 7) * (a.workers >> 3) + (worker >> 3);
+    if (worker >= active) return;
+    long long at = (long long)worker * total / active;
+    const long long end = (long long)(worker + 1) * total / active;
+    if (at >= end) return;
+
+    // The lane, item and tile that `at` falls on.
+    int b = 0;
+    long long before = 0;
+    for (int b0 = 0; b0 < a.lanes; b0 += 64) {
+        const int bb = b0 + lane;
+        long long v = 0;
+        if (bb < a.lanes) {
+            const LaneWork w = lane_work(a, bb, kRows);
+            v = (long long)w.blocks * a.c.kv_heads * w.tiles;
+        }
+        const long long upto = before + wave_scan(v);
+        const unsigned long long past = __ballot(upto > at);
+        if (past) {
+            const int first = __ffsll(past) - 1;
+            b = b0 + first;
+            before = __shfl(upto - v, first);
+            break;
+        }
+        before = __shfl(upto, 63);
+    }
+    b = __builtin_amdgcn_readfirstlane(b);
+    LaneWork w = lane_work(a, b, kRows);
+    int item = __builtin_amdgcn_readfirstlane((int)((at - before) / w.tiles));
+    int t0 = __builtin_amdgcn_readfirstlane((int)((at - before) - (long long)item * w.tiles));
+
+    const int page_mask = (1 << a.c.log_page) - 1;
+    const long long head_bytes = (long long)T::kRowBytes << a.c.log_page;
+
+    // Lane offsets of the copies.  K: slot s of the chunk's row r holds segment
+    // s ^ swz(r), swz = r mod 4 plus 4 x (chunk mod 4) where a row has as many
+    // segments; a copy covers 1024 bytes, rows in order.  V (bf16): dim d's two
+    // segments are swapped where d / 4 is odd.
+    int k_off[kSegs == 32 ? 2 : 1];
+#pragma unroll
+    for (int u = 0; u < (kSegs == 32 ? 2 : 1); ++u) {
+        const int q = u * 64 + lane, r = q / kSegs, s = q % kSegs;
+        const int swz = ((r & 3) | (wave << 2)) & (kSegs - 1) & 15;
+        k_off[u] = (r * kSegs + (s ^ swz)) * 16 - u * 1024;
+    }
+    const int v_off = FP8 ? lane * 16 : (lane >> 1) * 32 + ((lane & 1) ^ ((lane >> 3) & 1)) * 16;
+    // Lane offsets of the operand reads.
+    int k_at[KA];
+#pragma unroll
+    for (int u = 0; u < KA; ++u) {
+        const int swz = ((n & 3) | ((n >> 2) << 2)) & (kSegs - 1) & 15;
+        k_at[u] = (n >> 2) * kChunk + (n & 3) * T::kRowBytes + (((4 * u + g) ^ swz) * 16);
+    }
+    const int v_at = g * kChunk + (FP8 ? n * 16 : n * 32);
+    const int v_flip = FP8 ? 0 : ((n >> 2) & 1);
+
+    while (at < end) {
+        const int t1 = (int)min((long long)w.tiles, t0 + (end - at));
+        const int h = item / w.blocks, rb = item - h * w.blocks;
+        const int rows = w.rows * a.group;  // rows of the item's lane and head
+        const int* tab = a.table + (long long)b * a.table_ld;
+        uint8_t* kbase = a.c.k + h * head_bytes;
+        uint8_t* vbase = a.c.v + h * head_bytes;
+
+        // Page of 16-token chunk g of tile t (past the last token: its page).
+        auto load_ids = [&](int t, int (&id)[SUB]) {
+#pragma unroll
+            for (int u = 0; u < SUB; ++u) {
+                const int p = min((t + u) * kTile + 16 * g, w.tokens - 1);
+                id[u] = tab[p >> a.c.log_page];
+            }
+        };
+        auto good = [&](int id) { return (unsigned)id < (unsigned)a.c.pages; };
+        // Copies of the step at tile t.  A missing page is read as page 0 (and
+        // masked).
+        auto issue = [&](int t, const int (&id)[SUB], uint8_t* buf) {
+#pragma unroll
+            for (int u = 0; u < SUB; ++u) {
+                const int mine = __builtin_amdgcn_readlane(id[u], 16 * wave);
+                const int tok = min((t + u) * kTile + 16 * wave, (w.tokens - 1) & ~15) & page_mask;
+                const long long off = (long long)(good(mine) ? mine : 0) * a.c.page_stride + (long long)tok * T::kRowBytes;
+                uint8_t* kd = buf + u * T::kTileBytes + wave * kChunk;
+#pragma unroll
+                for (int c = 0; c < T::kCopies; ++c)
+                    copy_to_lds(kbase + off, kChunk, c * 1024, k_off[kSegs == 32 ? c & 1 : 0], kd + c * 1024);
+#pragma unroll
+                for (int c = 0; c < T::kCopies; ++c)
+                    copy_to_lds(vbase + off, kChunk, c * 1024, v_off, kd + 4 * kChunk + c * 1024);
+            }
+        };
+
+        int id0[SUB], id1[SUB];
+        load_ids(t0, id0);
+        // Q operand: row n of each row tile, 8 dims per step.
+        bf16x8 qf[NR][KS];
+        unsigned long long mask[NR];
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            const int row = rb * kRows + (rw * NR + r) * 16 + n;
+            const bool real = row < rows;
+            const int t = real ? row / a.group : 0;
+            const int head = h * a.group + (real ? row - t * a.group : 0);
+            const uint16_t* src = a.q + (long long)(w.row0 + t) * a.q_ld + (long long)head * D;
+            mask[r] = real ? a.mask[w.row0 + t] : 0ull;
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                // fp8: 16 bytes hold 16 dims of a token, two steps' slots
+                const int d = FP8 ? 64 * (s >> 1) + 16 * g + 8 * (s & 1) : 32 * s + 8 * g;
+                uint4 v = *(const uint4*)(src + d);
+                if (!real) v = make_uint4(0, 0, 0, 0);
+                qf[r][s] = bytes8(v);
+            }
+        }
+        f32x4 o[NR][DB];
+        float m[NR], mu[NR], l[NR];  // maximum, the one in use (0 for -inf), sum
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            m[r] = -__builtin_inff();
+            mu[r] = 0.f;
+            l[r] = 0.f;
+#pragma unroll
+            for (int db = 0; db < DB; ++db) o[r][db] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+
+        // One tile of a step, at byte `base` of buf.  (Operand addresses are one
+        // unsigned sum past the array: through longer chains of pointers the
+        // compiler loses which array a read is from, and makes it wait for the
+        // copies in flight into the other one.)
+        auto tile = [&](int t, int idv, const uint8_t* buf, uint32_t base) {
+            // Tiles past the context, and those with a missing page, are masked.
+            const bool masked = (t + 1) * kTile > w.ctx || __any(!good(idv));
+            const int chunk0 = t * kTile + 16 * g;  // this lane's first token
+            const int present = good(idv) ? min(max(w.tokens - chunk0, 0), 16) : 0;
+#pragma unroll
+            for (int hu = 0; hu < HH; ++hu) {
+                const int hh = TW == 2 ? tw : hu;
+                f32x4 s[NR][2];
+#pragma unroll
+                for (int r = 0; r < NR; ++r)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) s[r][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+                const uint32_t kb = base + (uint32_t)(hh * 8 * T::kRowBytes);
+                if (FP8) {
+#pragma unroll
+                    for (int ks = 0; ks < KS; ks += 2)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int u = ks / 2;
+                            const uint4 raw = *(const uint4*)(buf + (kb + (uint32_t)k_at[u % KA] + (uint32_t)((u / KA) * KA * 64 + i * 4 * T::kRowBytes)));
+                            const bf16x8 k0 = e4m3x8_to_bf16(raw.x, raw.y), k1 = e4m3x8_to_bf16(raw.z, raw.w);
+#pragma unroll
+                            for (int r = 0; r < NR; ++r) {
+                                s[r][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k0, qf[r][ks], s[r][i], 0, 0, 0);
+                                s[r][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k1, qf[r][ks + 1], s[r][i], 0, 0, 0);
+                            }
+                        }
+                } else {
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const bf16x8 kv = *(const bf16x8*)(buf + (kb + (uint32_t)k_at[ks % KA] + (uint32_t)((ks / KA) * KA * 64 + i * 4 * T::kRowBytes)));
+#pragma unroll
+                            for (int r = 0; r < NR; ++r)
+                                s[r][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kv, qf[r][ks], s[r][i], 0, 0, 0);
+                        }
+                }
+                if (masked) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int c = 8 * hh + e, p = chunk0 + c;
+                        const int j = p - w.ctx;  // place among the drafted tokens
+#pragma unroll
+                        for (int r = 0; r < NR; ++r) {
+                            const bool seen = c < present && (j < 0 || ((mask[r] >> (j & 63)) & 1));
+                            s[r][e >> 2][e & 3] = seen ? s[r][e >> 2][e & 3] : -__builtin_inff();
+                        }
+                    }
+                }
+                float top[NR];
+                bool grow = false;
+#pragma unroll
+                for (int r = 0; r < NR; ++r) {
+                    top[r] = fmaxf(fmaxf(fmaxf(s[r][0][0], s[r][0][1]), fmaxf(s[r][0][2], s[r][0][3])),
+                                   fmaxf(fmaxf(s[r][1][0], s[r][1][1]), fmaxf(s[r][1][2], s[r][1][3]))) * a.scale2;
+                    grow |= top[r] > m[r] + kRescaleAt;
+                }
+                if (__any(grow)) {
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) {
+                        float mx = fmaxf(top[r], __shfl_xor(top[r], 16));
+                        mx = fmaxf(mx, __shfl_xor(mx, 32));
+                        mx = fmaxf(mx, m[r]);
+                        const float use = mx == -__builtin_inff() ? 0.f : mx;
+                        const float f = exp2_fast(m[r] - use);  // 0 for the first maximum
+                        m[r] = mx;
+                        mu[r] = use;
+                        l[r] *= f;
+#pragma unroll
+                        for (int db = 0; db < DB; ++db)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) o[r][db][j] *= f;
+                    }
+                }
+                bf16x8 ph[NR], pl[NR];
+#pragma unroll
+                for (int r = 0; r < NR; ++r)
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2) {
+                        f32x2v p;
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            p[q] = exp2_fast(__builtin_fmaf(s[r][(e + q) >> 2][(e + q) & 3], a.scale2, -mu[r]));
+                            l[r] += p[q];
+                        }
+                        const bf16x2v hi = __builtin_convertvector(p, bf16x2v);
+                        ph[r][e] = hi[0];
+                        ph[r][e + 1] = hi[1];
+                        if (SPLIT) {
+                            const f32x2v back = __builtin_convertvector(hi, f32x2v);
+                            const f32x2v rest = {p[0] - back[0], p[1] - back[1]};
+                            const bf16x2v lo = __builtin_convertvector(rest, bf16x2v);
+                            pl[r][e] = lo[0];
+                            pl[r][e + 1] = lo[1];
+                        }
+                    }
+                const uint32_t vo = base + 4u * kChunk + (uint32_t)v_at + (uint32_t)(dw * DB * (FP8 ? 256 : 512)) +
+                                    (uint32_t)(FP8 ? 8 * hh : (hh ^ v_flip) * 16);
+#pragma unroll
+                for (int db = 0; db < DB; ++db) {
+                    bf16x8 vv;
+                    if (FP8) {
+                        const uint2 raw = *(const uint2*)(buf + (vo + db * 256u));
+                        vv = e4m3x8_to_bf16(raw.x, raw.y);
+                    } else {
+                        vv = *(const bf16x8*)(buf + (vo + db * 512u));
+                    }
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) {
+                        o[r][db] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vv, ph[r], o[r][db], 0, 0, 0);
+                        if (SPLIT) o[r][db] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vv, pl[r], o[r][db], 0, 0, 0);
+                    }
+                }
+            }
+        };
+        // Tokens past the end, and those of a missing page, may hold anything,
+        // NaN included: their values are zeroed in LDS, each wave in the chunk that
+        // it copied.
+        auto clear = [&](int t, int idv, uint8_t* buf) {
+            const int left = w.tokens - (t * kTile + 16 * wave);
+            const int keep = good(__builtin_amdgcn_readlane(idv, 16 * wave)) ? min(max(left, 0), 16) : 0;
+            if (keep == 16) return;
+            uint8_t* v = buf + (4 + wave) * kChunk;
+            for (int e = lane; e < kChunk / 16; e += 64) {
+                // bf16: first token of the segment in slot e
+                const int first = FP8 ? 0 : 8 * ((e & 1) ^ ((e >> 3) & 1));
+                uint4* p = (uint4*)(v + e * 16);
+                *p = keep_first(*p, (keep - first) * ES);
+            }
+        };
+        // One step: its copies have landed, the next step's are issued, and it
+        // is computed.  The barrier also ends every wave's reads of the other
+        // buffer, two steps back in the list of copies.
+        auto step = [&](int t, int (&ids)[SUB], int (&next)[SUB], uint8_t* buf, uint8_t* other) {
+            __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+            barrier_nofence();
+            int cur[SUB];
+#pragma unroll
+            for (int u = 0; u < SUB; ++u) cur[u] = ids[u];
+            if (t + SUB < t1) {
+                issue(t + SUB, next, other);
+                load_ids(min(t + 2 * SUB, t1 - 1), ids);
+            }
+            bool missing = (t + SUB) * kTile > w.tokens;
+#pragma unroll
+            for (int u = 0; u < SUB; ++u) missing |= __any(!good(cur[u])) != 0;
+            if (missing) {
+#pragma unroll
+                for (int u = 0; u < SUB; ++u) clear(t + u, cur[u], buf + u * T::kTileBytes);
+                __syncthreads();
+            }
+#pragma unroll
+            for (int u = 0; u < SUB; ++u)
+                if (t + u < t1) tile(t + u, cur[u], buf, u * T::kTileBytes);
+        };
+        issue(t0, id0, lds0);
+        load_ids(min(t0 + SUB, t1 - 1), id1);
+        for (int t = t0; t < t1; t += 2 * SUB) {
+            step(t, id0, id1, lds0, lds1);
+            if (t + SUB < t1) step(t + SUB, id1, id0, lds1, lds0);
+        }
+
+        // Sums over the four token groups of a row.
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            l[r] += __shfl_xor(l[r], 16);
+            l[r] += __shfl_xor(l[r], 32);
+        }
+        __syncthreads();
+        // The two waves that split the token halves meet in LDS.
+        if (TW > 1) {
+            float* sums = (float*)(rw == 0 ? lds0 : lds1);
+            if (tw > 0) {
+#pragma unroll
+                for (int r = 0; r < NR; ++r) {
+                    const int row = r * 16 + n;
+                    if (g == 0 && dw == 0) lds_ml[rw * NR * 16 + row] = make_float2(m[r], l[r]);
+#pragma unroll
+                    for (int db = 0; db < DB; ++db)
+                        *(f32x4*)(sums + row * D + ((16 * (dw * DB + db) + 4 * g) ^ (4 * (n & 7)))) = o[r][db];
+                }
+            }
+            __syncthreads();
+            if (tw == 0) {
+#pragma unroll
+                for (int r = 0; r < NR; ++r) {
+                    const int row = r * 16 + n;
+                    const float2 ml = lds_ml[rw * NR * 16 + row];
+                    const float mx = fmaxf(m[r], ml.x);
+                    const float use = mx == -__builtin_inff() ? 0.f : mx;
+                    const float f0 = exp2_fast(m[r] - use), f1 = exp2_fast(ml.x - use);
+                    m[r] = mx;
+                    l[r] = l[r] * f0 + ml.y * f1;
+#pragma unroll
+                    for (int db = 0; db < DB; ++db) {
+                        const f32x4 v = *(const f32x4*)(sums + row * D + ((16 * (dw * DB + db) + 4 * g) ^ (4 * (n & 7))));
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) o[r][db][j] = o[r][db][j] * f0 + v[j] * f1;
+                    }
+                }
+            }
+            __syncthreads();
+        }
+        if (tw == 0) {
+            const bool whole = t0 == 0 && t1 == w.tiles;
+            const int slot = 2 * worker + (t0 > 0 ? 0 : 1);
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                const int in_block = (rw * NR + r) * 16 + n;
+                const int row = rb * kRows + in_block;
+                if (row >= rows) continue;
+                if (whole) {
+                    const int tt = row / a.group, head = h * a.group + row - tt * a.group;
+                    const float inv = l[r] > 0.f ? a.c.v_scale / l[r] : 0.f;
+                    uint16_t* dst = a.out + (long long)(w.row0 + tt) * a.out_ld + (long long)head * D + 16 * dw * DB;
+#pragma unroll
+                    for (int db = 0; db < DB; ++db) {
+                        const uint32_t lo = f32_to_bf16_rne(o[r][db][0] * inv) | ((uint32_t)f32_to_bf16_rne(o[r][db][1] * inv) << 16);
+                        const uint32_t hi = f32_to_bf16_rne(o[r][db][2] * inv) | ((uint32_t)f32_to_bf16_rne(o[r][db][3] * inv) << 16);
+                        *(uint2*)(dst + 16 * db + 4 * g) = make_uint2(lo, hi);
+                    }
+                    if (a.lse && g == 0 && dw == 0)
+                        a.lse[(long long)(w.row0 + tt) * a.q_heads + head] = l[r] > 0.f ? (m[r] + log2f(l[r])) * kLn2 : -__builtin_inff();
+                } else {
+                    float* dst = a.part_o + ((long long)slot * kRows + in_block) * D + 16 * dw * DB;
+#pragma unroll
+                    for (int db = 0; db < DB; ++db) *(f32x4*)(dst + 16 * db + 4 * g) = o[r][db];
+                    if (g == 0 && dw == 0) a.part_ml[(long long)slot * kRows + in_block] = make_float2(m[r], l[r]);
+                }
+            }
+        }
+        // Next item.
+        at += t1 - t0;
+        t0 = 0;
+        if (at < end) {
+            if (++item == w.blocks * a.c.kv_heads) {
+                item = 0;
+                do {
+                    w = lane_work(a, ++b, kRows);
+                } while (w.tiles == 0);
+            }
+        }
+    }
+}
+
+// Adds the partial results of items that several workers shared: one wave per
+// row, contributors in worker order.
+template <int D>
+__global__ __launch_bounds__(256) void attend_merge_kernel(AttArgs a, int block_rows, int max_blocks) {
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), lane = threadIdx.x & 63;
+    const int per_lane = a.c.kv_heads * max_blocks;
+    const int b = blockIdx.x / per_lane, rest = blockIdx.x - b * per_lane;
+    const int h = rest / max_blocks, rb = rest - h * max_blocks;
+    const LaneWork w = lane_work(a, b, block_rows);
+    const int in_block = blockIdx.y * 4 + wave;
+    const int row = rb * block_rows + in_block;
+    if (rb >= w.blocks || row >= w.rows * a.group) return;  // whole wave
+    const int tt = row / a.group, head = h * a.group + row - tt * a.group;
+    uint16_t* dst = a.out + (long long)(w.row0 + tt) * a.out_ld + (long long)head * D;
+    float* lse = a.lse ? a.lse + (long long)(w.row0 + tt) * a.q_heads + head : nullptr;
+    constexpr int E = D / 64;
+    const long long total = total_tiles(a, block_rows, a.lanes);
+    const int active = active_workers(a, total);
+    const long long g0 = total_tiles(a, block_rows, b) + (long long)(h * w.blocks + rb) * w.tiles;
+    const int r0 = (int)(((g0 + 1) * active - 1) / total);
+    const int r1 = (int)(((g0 + w.tiles) * active - 1) / total);
+    if (r0 == r1) return;
+    auto slot = [&](int r) { return (long long)(2 * r + (r > r0 ? 0 : 1)) * block_rows + in_block; };
+    float mx = -__builtin_inff();
+    for (int r = r0 + lane; r <= r1; r += 64) mx = fmaxf(mx, a.part_ml[slot(r)].x);
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) mx = fmaxf(mx, __shfl_xor(mx, d));
+    const float use = mx == -__builtin_inff() ? 0.f : mx;
+    float sum = 0.f, acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    constexpr int U = 8;
+    for (int r = r0; r <= r1; r += U) {
+        float2 ml[U];
+        float v[U][E];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const long long s = slot(min(r + u, r1));
+            ml[u] = a.part_ml[s];
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[u][e] = a.part_o[s * D + 64 * e + lane];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const float f = r + u <= r1 ? exp2_fast(ml[u].x - use) : 0.f;
+            sum = __builtin_fmaf(ml[u].y, f, sum);
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = __builtin_fmaf(v[u][e], f, acc[e]);
+        }
+    }
+    const float inv = sum > 0.f ? a.c.v_scale / sum : 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) dst[64 * e + lane] = f32_to_bf16_rne(acc[e] * inv);
+    if (lse && lane == 0) *lse = sum > 0.f ? (mx + log2f(sum)) * kLn2 : -__builtin_inff();
+}
+
+// How a call's rows are cut.
+struct AttShape {
+    int nr, rw, tw, dw;
+    int block_rows() const { return 16 * nr * rw; }
+};
+
+AttShape att_shape(int rows, int dim) {
+    // rows: the largest lane's tokens x heads per kv head
+    const int tiles = (rows + 15) / 16;
+    if (tiles <= 1) return {1, 1, 2, 2};
+    if (tiles <= 2) return {1, 2, 2, 1};
+    if (dim == 256) return {1, 4, 1, 1};
+    if (tiles <= 4) return {2, 2, 2, 1};
+    return {2, 4, 1, 1};
+}
+
+int att_workers() {
+    const int n = 2 * device_cus();
+    return n / 8 * 8;
+}
+
+template <int D, bool FP8>
+void launch_shape(const AttShape& sh, const AttArgs& a, hipStream_t s) {
+#define NVFP4_ATT(NR_, RW_, TW_, DW_, SPLIT_)                                                     \
+    if (sh.nr == NR_ && sh.rw == RW_) {                                                           \
+        hipLaunchKernelGGL((attend_kernel<D, FP8, NR_, RW_, TW_, DW_, SPLIT_>), dim3(a.workers),  \
+                           dim3(kAttThreads), 0, s, a);                                           \
+        return;                                                                                   \
+    }
+    NVFP4_ATT(1, 1, 2, 2, true)
+    NVFP4_ATT(1, 2, 2, 1, true)
+    if constexpr (D == 256) {
+        NVFP4_ATT(1, 4, 1, 1, true)
+    } else {
+        NVFP4_ATT(2, 2, 2, 1, true)
+        NVFP4_ATT(2, 4, 1, 1, true)
+    }
+#undef NVFP4_ATT
+}
+
+template <int D>
+int launch_attend(const AttShape& sh, const AttArgs& a, int max_rows, hipStream_t s) {
+    if (a.c.fp8)
+        launch_shape<D, true>(sh, a, s);
+    else
+        launch_shape<D, false>(sh, a, s);
+    NVFP4_HIP(hipGetLastError());
+    const int rows = max_rows * a.group, br = sh.block_rows();
+    const int max_blocks = (rows + br - 1) / br;
+    const dim3 grid((unsigned)(a.lanes * a.c.kv_heads * max_blocks),
+                    (unsigned)((rows < br ? rows : br) + 3) / 4);
+    hipLaunchKernelGGL((attend_merge_kernel<D>), grid, dim3(256), 0, s, a, br, max_blocks);
+    NVFP4_HIP(hipGetLastError());
+    return NVFP4_OK;
+}
+
+size_t part_ml_bytes(const AttShape& sh) {
+    return (size_t)2 * att_workers() * sh.block_rows() * sizeof(float2);
+}
+
+}  // namespace nvfp4
+
+using namespace nvfp4;
+
+extern "C" {
+
+size_t nvfp4_tree_attention_workspace_bytes(int q_heads, int kv_heads, int head_dim, int max_rows) {
+    if (kv_heads < 1 || q_heads < kv_heads || q_heads % kv_heads || max_rows < 1 ||
+        max_rows > NVFP4_TREE_MAX_ROWS || (head_dim != 64 && head_dim != 128 && head_dim != 256) ||
+        q_heads > 65536)
+        return 0;
+    const AttShape sh = att_shape(max_rows * (q_heads / kv_heads), head_dim);
+    return part_ml_bytes(sh) + (size_t)2 * att_workers() * sh.block_rows() * head_dim * sizeof(float);
+}
+
+int nvfp4_tree_mask(const int* parent, int n, uint64_t* mask, int* depth) {
+    clear_error();
+    if (n < 1 || n > NVFP4_TREE_MAX_ROWS)
+        return set_error(NVFP4_EINVAL, "n: %d outside [1, %d]", n, NVFP4_TREE_MAX_ROWS);
+    if (!parent) return set_error(NVFP4_EINVAL, "parent: NULL");
+    if (!mask) return set_error(NVFP4_EINVAL, "mask: NULL");
+    for (int i = 0; i < n; ++i)
+        if (parent[i] < -1 || parent[i] >= i)
+            return set_error(NVFP4_EINVAL, "parent[%d]: %d outside [-1, %d]", i, parent[i], i - 1);
+    for (int i = 0; i < n; ++i) {
+        const int p = parent[i];
+        mask[i] = (p >= 0 ? mask[p] : 0ull) | (1ull << i);
+        if (depth) depth[i] = p >= 0 ? depth[p] + 1 : 0;
+    }
+    return NVFP4_OK;
+}
+
+int nvfp4_tree_attention(const nvfp4_cache* cache, int layer, const uint16_t* q_dev, int64_t q_ld,
+                         int q_heads, int lanes, int max_rows, const int* row_start_dev,
+                         const int* ctx_len_dev, const int* page_table_dev, int table_ld,
+                         const uint64_t* mask_dev, float scale, uint16_t* out_dev, int64_t out_ld,
+                         float* lse_dev, void* workspace_dev, size_t workspace_bytes, void* stream) {
+    clear_error();
+    AttArgs a;
+    int st = cache_view(cache, layer, &a.c);
+    if (st) return st;
+    if (layer < 0) return set_error(NVFP4_EINVAL, "layer: %d < 0", layer);
+    const int dim = a.c.dim, kv = a.c.kv_heads;
+    if (q_heads < kv || q_heads % kv || q_heads > 65536)
+        return set_error(NVFP4_EINVAL, "q_heads: %d is not a multiple of kv_heads %d up to 65536", q_heads, kv);
+    if (max_rows < 1 || max_rows > NVFP4_TREE_MAX_ROWS)
+        return set_error(NVFP4_EINVAL, "max_rows: %d outside [1, %d]", max_rows, NVFP4_TREE_MAX_ROWS);
+    if ((st = check_lanes(a.c, lanes, page_table_dev, table_ld))) return st;
+    const int64_t width = (int64_t)q_heads * dim;
+    if (q_ld < width || q_ld % 8) return set_error(NVFP4_EINVAL, "q_ld: %lld below %lld or not a multiple of 8", (long long)q_ld, (long long)width);
+    if (out_ld < width || out_ld % 4) return set_error(NVFP4_EINVAL, "out_ld: %lld below %lld or not a multiple of 4", (long long)out_ld, (long long)width);
+    if (!q_dev || ((uintptr_t)q_dev & 15)) return set_error(NVFP4_EINVAL, "q: NULL or not 16-byte aligned");
+    if (!out_dev || ((uintptr_t)out_dev & 7)) return set_error(NVFP4_EINVAL, "out: NULL or not 8-byte aligned");
+    if (!row_start_dev || ((uintptr_t)row_start_dev & 3)) return set_error(NVFP4_EINVAL, "row_start: NULL or not 4-byte aligned");
+    if (!ctx_len_dev || ((uintptr_t)ctx_len_dev & 3)) return set_error(NVFP4_EINVAL, "ctx_len: NULL or not 4-byte aligned");
+    if (!mask_dev || ((uintptr_t)mask_dev & 7)) return set_error(NVFP4_EINVAL, "mask: NULL or not 8-byte aligned");
+    if ((uintptr_t)lse_dev & 3) return set_error(NVFP4_EINVAL, "lse: not 4-byte aligned");
+    if (!(scale > 0.f) || scale > 1e30f) return set_error(NVFP4_EINVAL, "scale: not a positive number");
+    const size_t need = nvfp4_tree_attention_workspace_bytes(q_heads, kv, dim, max_rows);
+    if (workspace_bytes < need) return set_error(NVFP4_EINVAL, "workspace_bytes: %zu < %zu needed", workspace_bytes, need);
+    if (!workspace_dev || ((uintptr_t)workspace_dev & 15)) return set_error(NVFP4_EINVAL, "workspace: NULL or not 16-byte aligned");
+    const AttShape sh = att_shape(max_rows * (q_heads / kv), dim);
+    const int blocks = (max_rows * (q_heads / kv) + sh.block_rows() - 1) / sh.block_rows();
+    if ((long long)lanes * kv * blocks > 0x7FFFFFFFll)
+        return set_error(NVFP4_EUNSUPPORTED, "lanes: %d lanes of %d kv heads and %d row blocks exceed 2^31", lanes, kv, blocks);
+    a.q = q_dev;
+    a.q_ld = q_ld;
+    a.q_heads = q_heads;
+    a.group = q_heads / kv;
+    a.lanes = lanes;
+    a.max_rows = max_rows;
+    a.row_start = row_start_dev;
+    a.ctx_len = ctx_len_dev;
+    a.table = page_table_dev;
+    a.table_ld = table_ld;
+    a.mask = (const unsigned long long*)mask_dev;
+    a.scale2 = scale * kLog2e * a.c.k_scale;
+    a.out = out_dev;
+    a.out_ld = out_ld;
+    a.lse = lse_dev;
+    a.workers = att_workers();
+    a.part_ml = (float2*)workspace_dev;
+    a.part_o = (float*)((char*)workspace_dev + part_ml_bytes(sh));
+    hipStream_t s = (hipStream_t)stream;
+    if (dim == 64) return launch_attend<64>(sh, a, max_rows, s);
+    if (dim == 128) return launch_attend<128>(sh, a, max_rows, s);
+    return launch_attend<256>(sh, a, max_rows, s);
+}
+
+}  // extern "C"
