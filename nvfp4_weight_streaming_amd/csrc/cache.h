@@ -27,7 +27,7 @@ int cache_view(const nvfp4_cache* c, int layer, CacheView* out);
 // Checks a lane count and a page table.
 int check_lanes(const CacheView& c, int lanes, const int* table, int table_ld);
 
-constexpr int kMaxLanes = 65536;
+constexpr int kMaxLanes = 65535;  // a grid dimension
 
 // The lane that owns row r: the number of lanes whose rows end at or before r.
 // Every lane of the wave calls it with the same r (wave-parallel: one load per

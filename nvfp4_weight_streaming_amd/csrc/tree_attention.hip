@@ -28,6 +28,8 @@
 // step's copies in flight while the current step is computed.  K segments of 16
 // bytes sit in slots xor-ed with their token, and V segments with their dim, so
 // that the operand reads spread over the banks.
+#include <type_traits>
+
 #include "cache.h"
 #include "decode_device.h"
 
@@ -41,6 +43,9 @@ constexpr float kLn2 = 0.69314718055994530942f;
 // O and the sums are rescaled only when a row's maximum passes the one in use
 // by 2^8: weights stay below 2^8, far from fp32's and bf16's limits.
 constexpr float kRescaleAt = 8.f;
+// Fewest tiles a worker takes: below, joining partial results costs more than
+// the shorter walk saves.
+constexpr int kMinTiles = 4;
 
 struct AttArgs {
     CacheView c;  // base pointers of the layer
@@ -57,8 +62,8 @@ struct AttArgs {
     uint16_t* out;
     long long out_ld;
     float* lse;  // [rows][q_heads] or null
-    float* part_o;   // [2 x workers][block rows][dim]
-    float2* part_ml; // [2 x workers][block rows]: maximum (log2 units), sum
+    float2* part_ml;  // [2 x workers][block rows]: maximum (log2 units), sum
+    float* part_o;    // [2 x workers][block rows][dim]
     int workers;
 };
 
@@ -79,35 +84,48 @@ __device__ __forceinline__ LaneWork lane_work(const AttArgs& a, int b, int block
 }
 
 // Inclusive sum over the wave's lanes.
-__device__ __forceinline__ long long wave_scan(long long v) {
+__device__ __forceinline__ int wave_scan(int v) {
     const int l = threadIdx.x & 63;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-        const long long u = __shfl_up(v, d);
+        const int u = __shfl_up(v, d);
         v += l >= d ? u : 0;
     }
     return v;
 }
 
-// Sum of the tiles of all items of lanes [0, lanes) (or of those before `upto`).
-__device__ __forceinline__ long long total_tiles(const AttArgs& a, int block_rows, int upto) {
-    long long sum = 0;
-    for (int b0 = 0; b0 < upto; b0 += 64) {
-        const int b = b0 + (int)(threadIdx.x & 63);
-        long long v = 0;
-        if (b < upto) {
-            const LaneWork w = lane_work(a, b, block_rows);
-            v = (long long)w.blocks * a.c.kv_heads * w.tiles;
-        }
-        sum += __shfl(wave_scan(v), 63);
-    }
-    return sum;
+// Tiles of all items of a lane's work.
+__device__ __forceinline__ int lane_tiles(const AttArgs& a, const LaneWork& w) {
+    return w.blocks * a.c.kv_heads * w.tiles;
 }
 
-// Workers that share `total` tiles: enough tiles each that every wave of a
-// workgroup has some.
-__device__ __forceinline__ int active_workers(const AttArgs& a, long long total) {
-    return (int)max(1ll, min((long long)a.workers, total / kAttWaves));
+// Equal shares: worker r < active takes tiles [begin(r), begin(r + 1)).
+struct Shares {
+    int active, each, rem;
+    __device__ __forceinline__ int begin(int r) const { return r * each + min(r, rem); }
+    __device__ __forceinline__ int owner(int tile) const {
+        const int wide = rem * (each + 1);
+        return tile < wide ? (int)((unsigned)tile / (unsigned)(each + 1))
+                           : rem + (int)((unsigned)(tile - wide) / (unsigned)each);
+    }
+};
+
+// The shares, worked out by a wave: its lane l looks at lanes l, l + 64, ... of
+// the call.  first, upto: lane l's own work (none past the last) and the sum of
+// tiles of lanes 0 .. l, for the first 64.
+__device__ __forceinline__ Shares shares_of(const AttArgs& a, int block_rows, LaneWork& first, int& upto) {
+    const int l = threadIdx.x & 63;
+    first = LaneWork{0, 0, 0, 0, 0, 0};
+    if (l < a.lanes) first = lane_work(a, l, block_rows);
+    upto = wave_scan(lane_tiles(a, first));
+    int total = __builtin_amdgcn_readlane(upto, 63);
+    for (int b0 = 64; b0 < a.lanes; b0 += 64) {
+        const int v = b0 + l < a.lanes ? lane_tiles(a, lane_work(a, b0 + l, block_rows)) : 0;
+        total += __builtin_amdgcn_readlane(wave_scan(v), 63);
+    }
+    // Enough tiles each to outweigh the joining of their results.
+    const int active = max(1, min(a.workers, total / kMinTiles));
+    return {active, (int)((unsigned)total / (unsigned)active), (int)((unsigned)total % (unsigned)active)};
 }
 
 __device__ __forceinline__ bf16x8 bytes8(const uint4& v) {
@@ -142,6 +160,11 @@ __device__ __forceinline__ void copy_to_lds(uint8_t* src, int bytes, int at, int
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
+__device__ __forceinline__ uint2 bf16x4(float a, float b, float c, float d) {
+    return make_uint2(f32_to_bf16_rne(a) | ((uint32_t)f32_to_bf16_rne(b) << 16),
+                      f32_to_bf16_rne(c) | ((uint32_t)f32_to_bf16_rne(d) << 16));
+}
+
 // How the four waves share a block: RW waves split its rows (NR row tiles of 16
 // each), TW the token halves of a tile, DW the dims of O (those repeat S).
 // SPLIT: weights enter the second product as two bf16 numbers.
@@ -167,6 +190,8 @@ __global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(AttArgs a) {
     constexpr int KS = D / 32;       // K steps of 32 dims
     constexpr int DB = D / 16 / DW;  // this wave's dim blocks of O
     constexpr int HH = 2 / TW;       // token halves a wave takes
+    constexpr int KL = FP8 ? KS / 2 : KS;  // 16-byte reads of a token's K
+    using VRaw = typename std::conditional<FP8, uint2, uint4>::type;  // 8 tokens of V
     constexpr int KA = kSegs >= 16 ? 4 : kSegs / 4;  // distinct K operand addresses
     // Two arrays, so that the compiler can tell the copies in flight from the
     // reads of the other one.
@@ -180,41 +205,44 @@ __global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(AttArgs a) {
     const int g = lane >> 4, n = lane & 15;
     const int rw = wave % RW, tw = wave / RW % TW, dw = wave / (RW * TW);
 
-    const long long total = total_tiles(a, kRows, a.lanes);
-    const int active = active_workers(a, total);
+    // Every workgroup works its share out of the lanes' lengths by itself.
+    LaneWork w;
+    int first_upto;
+    const Shares share = shares_of(a, kRows, w, first_upto);
     int worker = blockIdx.x;
     // Consecutive ranges on one XCD (workgroup b runs on XCD b mod 8), so that
     // the row blocks of one lane and head share their K and V in its L2.
-    if (active == a.workers) worker = (worker & 7) * (a.workers >> 3) + (worker >> 3);
-    if (worker >= active) return;
-    long long at = (long long)worker * total / active;
-    const long long end = (long long)(worker + 1) * total / active;
+    if (share.active == a.workers && a.workers % 8 == 0) worker = (worker & 7) * (a.workers >> 3) + (worker >> 3);
+    if (worker >= share.active) return;
+    int at = share.begin(worker);
+    const int end = share.begin(worker + 1);
     if (at >= end) return;
 
     // The lane, item and tile that `at` falls on.
-    int b = 0;
-    long long before = 0;
-    for (int b0 = 0; b0 < a.lanes; b0 += 64) {
-        const int bb = b0 + lane;
-        long long v = 0;
-        if (bb < a.lanes) {
-            const LaneWork w = lane_work(a, bb, kRows);
-            v = (long long)w.blocks * a.c.kv_heads * w.tiles;
+    int b, before;
+    {
+        int b0 = 0, upto = first_upto, base = 0;
+        unsigned long long past = __ballot(upto > at);
+        while (!past) {
+            base += __builtin_amdgcn_readlane(upto, 63);
+            b0 += 64;
+            w = LaneWork{0, 0, 0, 0, 0, 0};
+            if (b0 + lane < a.lanes) w = lane_work(a, b0 + lane, kRows);
+            upto = wave_scan(lane_tiles(a, w));
+            past = __ballot(base + upto > at);
         }
-        const long long upto = before + wave_scan(v);
-        const unsigned long long past = __ballot(upto > at);
-        if (past) {
-            const int first = __ffsll(past) - 1;
-            b = b0 + first;
-            before = __shfl(upto - v, first);
-            break;
-        }
-        before = __shfl(upto, 63);
+        const int first = __ffsll(past) - 1;
+        w.row0 = __builtin_amdgcn_readlane(w.row0, first);
+        w.rows = __builtin_amdgcn_readlane(w.rows, first);
+        w.ctx = __builtin_amdgcn_readlane(w.ctx, first);
+        w.tokens = __builtin_amdgcn_readlane(w.tokens, first);
+        w.blocks = __builtin_amdgcn_readlane(w.blocks, first);
+        w.tiles = __builtin_amdgcn_readlane(w.tiles, first);
+        b = b0 + first;
+        before = base + __builtin_amdgcn_readlane(upto, first) - lane_tiles(a, w);
     }
-    b = __builtin_amdgcn_readfirstlane(b);
-    LaneWork w = lane_work(a, b, kRows);
-    int item = __builtin_amdgcn_readfirstlane((int)((at - before) / w.tiles));
-    int t0 = __builtin_amdgcn_readfirstlane((int)((at - before) - (long long)item * w.tiles));
+    int item = (int)((unsigned)(at - before) / (unsigned)w.tiles);
+    int t0 = at - before - item * w.tiles;
 
     const int page_mask = (1 << a.c.log_page) - 1;
     const long long head_bytes = (long long)T::kRowBytes << a.c.log_page;
@@ -242,8 +270,8 @@ __global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(AttArgs a) {
     const int v_flip = FP8 ? 0 : ((n >> 2) & 1);
 
     while (at < end) {
-        const int t1 = (int)min((long long)w.tiles, t0 + (end - at));
-        const int h = item / w.blocks, rb = item - h * w.blocks;
+        const int t1 = min(w.tiles, t0 + (end - at));
+        const int h = (int)((unsigned)item / (unsigned)w.blocks), rb = item - h * w.blocks;
         const int rows = w.rows * a.group;  // rows of the item's lane and head
         const int* tab = a.table + (long long)b * a.table_ld;
         uint8_t* kbase = a.c.k + h * head_bytes;
@@ -285,7 +313,7 @@ __global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(AttArgs a) {
         for (int r = 0; r < NR; ++r) {
             const int row = rb * kRows + (rw * NR + r) * 16 + n;
             const bool real = row < rows;
-            const int t = real ? row / a.group : 0;
+            const int t = real ? (int)((unsigned)row / (unsigned)a.group) : 0;
             const int head = h * a.group + (real ? row - t * a.group : 0);
             const uint16_t* src = a.q + (long long)(w.row0 + t) * a.q_ld + (long long)head * D;
             mask[r] = real ? a.mask[w.row0 + t] : 0ull;
@@ -327,31 +355,35 @@ __global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(AttArgs a) {
 #pragma unroll
                     for (int i = 0; i < 2; ++i) s[r][i] = f32x4{0.f, 0.f, 0.f, 0.f};
                 const uint32_t kb = base + (uint32_t)(hh * 8 * T::kRowBytes);
-                if (FP8) {
+                // All operand reads of a product go out before its first
+                // instruction (left alone, the compiler waits for each read).
+                uint4 kr[KL][2];
 #pragma unroll
-                    for (int ks = 0; ks < KS; ks += 2)
+                for (int u = 0; u < KL; ++u)
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int u = ks / 2;
-                            const uint4 raw = *(const uint4*)(buf + (kb + (uint32_t)k_at[u % KA] + (uint32_t)((u / KA) * KA * 64 + i * 4 * T::kRowBytes)));
-                            const bf16x8 k0 = e4m3x8_to_bf16(raw.x, raw.y), k1 = e4m3x8_to_bf16(raw.z, raw.w);
+                    for (int i = 0; i < 2; ++i)
+                        kr[u][i] = *(const uint4*)(buf + (kb + (uint32_t)k_at[u % KA] + (uint32_t)((u / KA) * KA * 64 + i * 4 * T::kRowBytes)));
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                            for (int r = 0; r < NR; ++r) {
-                                s[r][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k0, qf[r][ks], s[r][i], 0, 0, 0);
-                                s[r][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k1, qf[r][ks + 1], s[r][i], 0, 0, 0);
-                            }
-                        }
-                } else {
+                for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-                    for (int ks = 0; ks < KS; ++ks)
+                    for (int i = 0; i < 2; ++i) {
+                        bf16x8 kv;
+                        if (FP8)
+                            kv = (ks & 1) ? e4m3x8_to_bf16(kr[ks / 2][i].z, kr[ks / 2][i].w) : e4m3x8_to_bf16(kr[ks / 2][i].x, kr[ks / 2][i].y);
+                        else
+                            kv = bytes8(kr[FP8 ? 0 : ks][i]);
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const bf16x8 kv = *(const bf16x8*)(buf + (kb + (uint32_t)k_at[ks % KA] + (uint32_t)((ks / KA) * KA * 64 + i * 4 * T::kRowBytes)));
+                        for (int r = 0; r < NR; ++r)
+                            s[r][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kv, qf[r][ks], s[r][i], 0, 0, 0);
+                    }
+                // V is on its way during the softmax.
+                const uint32_t vo = base + 4u * kChunk + (uint32_t)v_at + (uint32_t)(dw * DB * (FP8 ? 256 : 512)) +
+                                    (uint32_t)(FP8 ? 8 * hh : (hh ^ v_flip) * 16);
+                VRaw vr[DB];
 #pragma unroll
-                            for (int r = 0; r < NR; ++r)
-                                s[r][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kv, qf[r][ks], s[r][i], 0, 0, 0);
-                        }
-                }
+                for (int db = 0; db < DB; ++db) vr[db] = *(const VRaw*)(buf + (vo + db * (FP8 ? 256u : 512u)));
+                __builtin_amdgcn_sched_barrier(0);
                 if (masked) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
@@ -411,23 +443,27 @@ __global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(AttArgs a) {
                             pl[r][e + 1] = lo[1];
                         }
                     }
-                const uint32_t vo = base + 4u * kChunk + (uint32_t)v_at + (uint32_t)(dw * DB * (FP8 ? 256 : 512)) +
-                                    (uint32_t)(FP8 ? 8 * hh : (hh ^ v_flip) * 16);
+                bf16x8 vv[DB];
 #pragma unroll
                 for (int db = 0; db < DB; ++db) {
-                    bf16x8 vv;
-                    if (FP8) {
-                        const uint2 raw = *(const uint2*)(buf + (vo + db * 256u));
-                        vv = e4m3x8_to_bf16(raw.x, raw.y);
-                    } else {
-                        vv = *(const bf16x8*)(buf + (vo + db * 512u));
-                    }
-#pragma unroll
-                    for (int r = 0; r < NR; ++r) {
-                        o[r][db] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vv, ph[r], o[r][db], 0, 0, 0);
-                        if (SPLIT) o[r][db] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vv, pl[r], o[r][db], 0, 0, 0);
-                    }
+                    if constexpr (FP8)
+                        vv[db] = e4m3x8_to_bf16(vr[db].x, vr[db].y);
+                    else
+                        vv[db] = bytes8(vr[db]);
                 }
+                // The two products of an accumulator stand apart: the second
+                // waits for the first.
+#pragma unroll
+                for (int db = 0; db < DB; ++db)
+#pragma unroll
+                    for (int r = 0; r < NR; ++r)
+                        o[r][db] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vv[db], ph[r], o[r][db], 0, 0, 0);
+                if (SPLIT)
+#pragma unroll
+                    for (int db = 0; db < DB; ++db)
+#pragma unroll
+                        for (int r = 0; r < NR; ++r)
+                            o[r][db] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vv[db], pl[r], o[r][db], 0, 0, 0);
             }
         };
         // Tokens past the end, and those of a missing page, may hold anything,
@@ -518,8 +554,8 @@ __global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(AttArgs a) {
             }
             __syncthreads();
         }
+        const bool whole = t0 == 0 && t1 == w.tiles;
         if (tw == 0) {
-            const bool whole = t0 == 0 && t1 == w.tiles;
             const int slot = 2 * worker + (t0 > 0 ? 0 : 1);
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
@@ -527,15 +563,12 @@ __global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(AttArgs a) {
                 const int row = rb * kRows + in_block;
                 if (row >= rows) continue;
                 if (whole) {
-                    const int tt = row / a.group, head = h * a.group + row - tt * a.group;
+                    const int tt = (int)((unsigned)row / (unsigned)a.group), head = h * a.group + row - tt * a.group;
                     const float inv = l[r] > 0.f ? a.c.v_scale / l[r] : 0.f;
                     uint16_t* dst = a.out + (long long)(w.row0 + tt) * a.out_ld + (long long)head * D + 16 * dw * DB;
 #pragma unroll
-                    for (int db = 0; db < DB; ++db) {
-                        const uint32_t lo = f32_to_bf16_rne(o[r][db][0] * inv) | ((uint32_t)f32_to_bf16_rne(o[r][db][1] * inv) << 16);
-                        const uint32_t hi = f32_to_bf16_rne(o[r][db][2] * inv) | ((uint32_t)f32_to_bf16_rne(o[r][db][3] * inv) << 16);
-                        *(uint2*)(dst + 16 * db + 4 * g) = make_uint2(lo, hi);
-                    }
+                    for (int db = 0; db < DB; ++db)
+                        *(uint2*)(dst + 16 * db + 4 * g) = bf16x4(o[r][db][0] * inv, o[r][db][1] * inv, o[r][db][2] * inv, o[r][db][3] * inv);
                     if (a.lse && g == 0 && dw == 0)
                         a.lse[(long long)(w.row0 + tt) * a.q_heads + head] = l[r] > 0.f ? (m[r] + log2f(l[r])) * kLn2 : -__builtin_inff();
                 } else {
@@ -560,60 +593,80 @@ __global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(AttArgs a) {
     }
 }
 
-// Adds the partial results of items that several workers shared: one wave per
-// row, contributors in worker order.
+// Joins the partial results of items that several workers shared: one wave per
+// row, contributors in worker order, kFan of them loaded at once.
+constexpr int kFan = 16;
 template <int D>
-__global__ __launch_bounds__(256) void attend_merge_kernel(AttArgs a, int block_rows, int max_blocks) {
+__global__ __launch_bounds__(256) void attend_join_kernel(AttArgs a, int block_rows, int max_blocks) {
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), lane = threadIdx.x & 63;
-    const int per_lane = a.c.kv_heads * max_blocks;
-    const int b = blockIdx.x / per_lane, rest = blockIdx.x - b * per_lane;
-    const int h = rest / max_blocks, rb = rest - h * max_blocks;
-    const LaneWork w = lane_work(a, b, block_rows);
-    const int in_block = blockIdx.y * 4 + wave;
-    const int row = rb * block_rows + in_block;
-    if (rb >= w.blocks || row >= w.rows * a.group) return;  // whole wave
-    const int tt = row / a.group, head = h * a.group + row - tt * a.group;
-    uint16_t* dst = a.out + (long long)(w.row0 + tt) * a.out_ld + (long long)head * D;
-    float* lse = a.lse ? a.lse + (long long)(w.row0 + tt) * a.q_heads + head : nullptr;
-    constexpr int E = D / 64;
-    const long long total = total_tiles(a, block_rows, a.lanes);
-    const int active = active_workers(a, total);
-    const long long g0 = total_tiles(a, block_rows, b) + (long long)(h * w.blocks + rb) * w.tiles;
-    const int r0 = (int)(((g0 + 1) * active - 1) / total);
-    const int r1 = (int)(((g0 + w.tiles) * active - 1) / total);
+    const int b = blockIdx.z, h = (int)(blockIdx.y / (unsigned)max_blocks), rb = blockIdx.y - h * max_blocks;
+    const int in_block = blockIdx.x * 4 + wave, row = rb * block_rows + in_block;
+    LaneWork w;
+    int upto;
+    const Shares share = shares_of(a, block_rows, w, upto);
+    int before = 0;  // tiles of the lanes before b
+    if (b < 64) {
+        before = __builtin_amdgcn_readlane(upto, b) - __builtin_amdgcn_readlane(lane_tiles(a, w), b);
+        w.row0 = __builtin_amdgcn_readlane(w.row0, b);
+        w.rows = __builtin_amdgcn_readlane(w.rows, b);
+        w.blocks = __builtin_amdgcn_readlane(w.blocks, b);
+        w.tiles = __builtin_amdgcn_readlane(w.tiles, b);
+    } else {
+        for (int b0 = 0; b0 < b; b0 += 64) {
+            const int v = b0 + lane < b ? lane_tiles(a, lane_work(a, b0 + lane, block_rows)) : 0;
+            before += __builtin_amdgcn_readlane(wave_scan(v), 63);
+        }
+        w = lane_work(a, b, block_rows);
+    }
+    if (rb >= w.blocks || row >= w.rows * a.group || in_block >= block_rows || w.tiles == 0) return;  // whole wave
+    const int start = before + (h * w.blocks + rb) * w.tiles;  // the item's first tile
+    const int r0 = share.owner(start), r1 = share.owner(start + w.tiles - 1);
     if (r0 == r1) return;
+    const int tt = (int)((unsigned)row / (unsigned)a.group), head = h * a.group + row - tt * a.group;
+    constexpr int E = D / 64;
+    typedef float vec __attribute__((ext_vector_type(E)));
     auto slot = [&](int r) { return (long long)(2 * r + (r > r0 ? 0 : 1)) * block_rows + in_block; };
-    float mx = -__builtin_inff();
-    for (int r = r0 + lane; r <= r1; r += 64) mx = fmaxf(mx, a.part_ml[slot(r)].x);
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) mx = fmaxf(mx, __shfl_xor(mx, d));
-    const float use = mx == -__builtin_inff() ? 0.f : mx;
-    float sum = 0.f, acc[E];
+    float mx = -__builtin_inff(), sum = 0.f;
+    float acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    constexpr int U = 8;
-    for (int r = r0; r <= r1; r += U) {
-        float2 ml[U];
-        float v[U][E];
+    for (int r = r0; r <= r1; r += kFan) {
+        float2 ml[kFan];
+        vec v[kFan];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
+        for (int u = 0; u < kFan; ++u) {
             const long long s = slot(min(r + u, r1));
             ml[u] = a.part_ml[s];
-#pragma unroll
-            for (int e = 0; e < E; ++e) v[u][e] = a.part_o[s * D + 64 * e + lane];
+            v[u] = *(const vec*)(a.part_o + s * D + E * lane);
         }
+        float top = mx;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
+        for (int u = 0; u < kFan; ++u) top = fmaxf(top, ml[u].x);
+        const float use = top == -__builtin_inff() ? 0.f : top;
+        const float old = exp2_fast(mx - use);
+        mx = top;
+        sum *= old;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] *= old;
+#pragma unroll
+        for (int u = 0; u < kFan; ++u) {
             const float f = r + u <= r1 ? exp2_fast(ml[u].x - use) : 0.f;
             sum = __builtin_fmaf(ml[u].y, f, sum);
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = __builtin_fmaf(v[u][e], f, acc[e]);
+            for (int e = 0; e < E; ++e) acc[e] = __builtin_fmaf(E == 1 ? v[u][0] : v[u][e], f, acc[e]);
         }
     }
     const float inv = sum > 0.f ? a.c.v_scale / sum : 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) dst[64 * e + lane] = f32_to_bf16_rne(acc[e] * inv);
-    if (lse && lane == 0) *lse = sum > 0.f ? (mx + log2f(sum)) * kLn2 : -__builtin_inff();
+    uint16_t* dst = a.out + (long long)(w.row0 + tt) * a.out_ld + (long long)head * D + E * lane;
+    if constexpr (E == 1) {
+        dst[0] = f32_to_bf16_rne(acc[0] * inv);
+    } else if constexpr (E == 2) {
+        *(uint32_t*)dst = f32_to_bf16_rne(acc[0] * inv) | ((uint32_t)f32_to_bf16_rne(acc[1] * inv) << 16);
+    } else {
+        *(uint2*)dst = bf16x4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
+    }
+    if (a.lse && lane == 0)
+        a.lse[(long long)(w.row0 + tt) * a.q_heads + head] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : -__builtin_inff();
 }
 
 // How a call's rows are cut.
@@ -657,17 +710,17 @@ void launch_shape(const AttShape& sh, const AttArgs& a, hipStream_t s) {
 }
 
 template <int D>
-int launch_attend(const AttShape& sh, const AttArgs& a, int max_rows, hipStream_t s) {
+int launch_attend(const AttShape& sh, const AttArgs& a, bool joins, hipStream_t s) {
     if (a.c.fp8)
         launch_shape<D, true>(sh, a, s);
     else
         launch_shape<D, false>(sh, a, s);
     NVFP4_HIP(hipGetLastError());
-    const int rows = max_rows * a.group, br = sh.block_rows();
+    if (!joins) return NVFP4_OK;
+    const int rows = a.max_rows * a.group, br = sh.block_rows();
     const int max_blocks = (rows + br - 1) / br;
-    const dim3 grid((unsigned)(a.lanes * a.c.kv_heads * max_blocks),
-                    (unsigned)((rows < br ? rows : br) + 3) / 4);
-    hipLaunchKernelGGL((attend_merge_kernel<D>), grid, dim3(256), 0, s, a, br, max_blocks);
+    const dim3 grid((unsigned)((rows < br ? rows : br) + 3) / 4, (unsigned)(a.c.kv_heads * max_blocks), (unsigned)a.lanes);
+    hipLaunchKernelGGL((attend_join_kernel<D>), grid, dim3(256), 0, s, a, br, max_blocks);
     NVFP4_HIP(hipGetLastError());
     return NVFP4_OK;
 }
@@ -739,8 +792,11 @@ int nvfp4_tree_attention(const nvfp4_cache* cache, int layer, const uint16_t* q_
     if (!workspace_dev || ((uintptr_t)workspace_dev & 15)) return set_error(NVFP4_EINVAL, "workspace: NULL or not 16-byte aligned");
     const AttShape sh = att_shape(max_rows * (q_heads / kv), dim);
     const int blocks = (max_rows * (q_heads / kv) + sh.block_rows() - 1) / sh.block_rows();
-    if ((long long)lanes * kv * blocks > 0x7FFFFFFFll)
-        return set_error(NVFP4_EUNSUPPORTED, "lanes: %d lanes of %d kv heads and %d row blocks exceed 2^31", lanes, kv, blocks);
+    const long long tiles = (long long)lanes * kv * blocks * ((((int64_t)table_ld << a.c.log_page) + kTile - 1) / kTile);
+    if (tiles > 0x7FFFFFFFll)
+        return set_error(NVFP4_EUNSUPPORTED, "lanes: %d lanes of %d kv heads, %d row blocks and %d pages exceed 2^31 tiles", lanes, kv, blocks, table_ld);
+    if ((long long)kv * blocks > 65535)
+        return set_error(NVFP4_EUNSUPPORTED, "q_heads: %d kv heads of %d row blocks exceed 65535", kv, blocks);
     a.q = q_dev;
     a.q_ld = q_ld;
     a.q_heads = q_heads;
@@ -756,13 +812,17 @@ int nvfp4_tree_attention(const nvfp4_cache* cache, int layer, const uint16_t* q_
     a.out = out_dev;
     a.out_ld = out_ld;
     a.lse = lse_dev;
-    a.workers = att_workers();
+    // No more workgroups than the tables could ever feed.
+    const long long most = (tiles + kMinTiles - 1) / kMinTiles;
+    a.workers = most < att_workers() ? (int)most : att_workers();
     a.part_ml = (float2*)workspace_dev;
     a.part_o = (float*)((char*)workspace_dev + part_ml_bytes(sh));
+    // One worker never shares an item.
+    const bool joins = a.workers > 1;
     hipStream_t s = (hipStream_t)stream;
-    if (dim == 64) return launch_attend<64>(sh, a, max_rows, s);
-    if (dim == 128) return launch_attend<128>(sh, a, max_rows, s);
-    return launch_attend<256>(sh, a, max_rows, s);
+    if (dim == 64) return launch_attend<64>(sh, a, joins, s);
+    if (dim == 128) return launch_attend<128>(sh, a, joins, s);
+    return launch_attend<256>(sh, a, joins, s);
 }
 
 }  // extern "C"
