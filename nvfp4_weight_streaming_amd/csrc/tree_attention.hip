@@ -346,14 +346,14 @@ __global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(AttArgs a) {
             const bool masked = (t + 1) * kTile > w.ctx || __any(!good(idv));
             const int chunk0 = t * kTile + 16 * g;  // this lane's first token
             const int present = good(idv) ? min(max(w.tokens - chunk0, 0), 16) : 0;
+            f32x4 s[HH][NR][2];
 #pragma unroll
             for (int hu = 0; hu < HH; ++hu) {
                 const int hh = TW == 2 ? tw : hu;
-                f32x4 s[NR][2];
 #pragma unroll
                 for (int r = 0; r < NR; ++r)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) s[r][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+                    for (int i = 0; i < 2; ++i) s[hu][r][i] = f32x4{0.f, 0.f, 0.f, 0.f};
                 const uint32_t kb = base + (uint32_t)(hh * 8 * T::kRowBytes);
                 // All operand reads of a product go out before its first
                 // instruction (left alone, the compiler waits for each read).
@@ -375,75 +375,90 @@ __global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(AttArgs a) {
                             kv = bytes8(kr[FP8 ? 0 : ks][i]);
 #pragma unroll
                         for (int r = 0; r < NR; ++r)
-                            s[r][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kv, qf[r][ks], s[r][i], 0, 0, 0);
+                            s[hu][r][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kv, qf[r][ks], s[hu][r][i], 0, 0, 0);
                     }
-                // V is on its way during the softmax.
+            }
+            // V is on its way during the softmax.
+            VRaw vr[DB];
+            auto read_v = [&](int hu) {
+                const int hh = TW == 2 ? tw : hu;
                 const uint32_t vo = base + 4u * kChunk + (uint32_t)v_at + (uint32_t)(dw * DB * (FP8 ? 256 : 512)) +
                                     (uint32_t)(FP8 ? 8 * hh : (hh ^ v_flip) * 16);
-                VRaw vr[DB];
 #pragma unroll
                 for (int db = 0; db < DB; ++db) vr[db] = *(const VRaw*)(buf + (vo + db * (FP8 ? 256u : 512u)));
-                __builtin_amdgcn_sched_barrier(0);
-                if (masked) {
+            };
+            read_v(0);
+            __builtin_amdgcn_sched_barrier(0);
+            if (masked) {
+#pragma unroll
+                for (int hu = 0; hu < HH; ++hu)
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const int c = 8 * hh + e, p = chunk0 + c;
+                        const int c = 8 * (TW == 2 ? tw : hu) + e, p = chunk0 + c;
                         const int j = p - w.ctx;  // place among the drafted tokens
 #pragma unroll
                         for (int r = 0; r < NR; ++r) {
                             const bool seen = c < present && (j < 0 || ((mask[r] >> (j & 63)) & 1));
-                            s[r][e >> 2][e & 3] = seen ? s[r][e >> 2][e & 3] : -__builtin_inff();
+                            s[hu][r][e >> 2][e & 3] = seen ? s[hu][r][e >> 2][e & 3] : -__builtin_inff();
                         }
                     }
-                }
-                float top[NR];
-                bool grow = false;
+            }
+            float top[NR];
+            bool grow = false;
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                float x = -__builtin_inff();
+#pragma unroll
+                for (int hu = 0; hu < HH; ++hu)
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2)
+                        x = fmaxf(x, fmaxf(s[hu][r][e >> 2][e & 3], s[hu][r][e >> 2][(e & 3) + 1]));
+                top[r] = x * a.scale2;
+                grow |= top[r] > m[r] + kRescaleAt;
+            }
+            if (__any(grow)) {
 #pragma unroll
                 for (int r = 0; r < NR; ++r) {
-                    top[r] = fmaxf(fmaxf(fmaxf(s[r][0][0], s[r][0][1]), fmaxf(s[r][0][2], s[r][0][3])),
-                                   fmaxf(fmaxf(s[r][1][0], s[r][1][1]), fmaxf(s[r][1][2], s[r][1][3]))) * a.scale2;
-                    grow |= top[r] > m[r] + kRescaleAt;
+                    float mx = fmaxf(top[r], __shfl_xor(top[r], 16));
+                    mx = fmaxf(mx, __shfl_xor(mx, 32));
+                    mx = fmaxf(mx, m[r]);
+                    const float use = mx == -__builtin_inff() ? 0.f : mx;
+                    const float f = exp2_fast(m[r] - use);  // 0 for the first maximum
+                    m[r] = mx;
+                    mu[r] = use;
+                    l[r] *= f;
+#pragma unroll
+                    for (int db = 0; db < DB; ++db)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) o[r][db][j] *= f;
                 }
-                if (__any(grow)) {
+            }
+            // Weights of a half, as one or two bf16 operands: piece e of row tile
+            // r is a pair.
+            bf16x8 ph[HH][NR], pl[HH][NR];
+            auto weights = [&](int hu, int r, int e) {
+                f32x2v p;
 #pragma unroll
-                    for (int r = 0; r < NR; ++r) {
-                        float mx = fmaxf(top[r], __shfl_xor(top[r], 16));
-                        mx = fmaxf(mx, __shfl_xor(mx, 32));
-                        mx = fmaxf(mx, m[r]);
-                        const float use = mx == -__builtin_inff() ? 0.f : mx;
-                        const float f = exp2_fast(m[r] - use);  // 0 for the first maximum
-                        m[r] = mx;
-                        mu[r] = use;
-                        l[r] *= f;
-#pragma unroll
-                        for (int db = 0; db < DB; ++db)
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) o[r][db][j] *= f;
-                    }
+                for (int q = 0; q < 2; ++q) {
+                    p[q] = exp2_fast(__builtin_fmaf(s[hu][r][(e + q) >> 2][(e + q) & 3], a.scale2, -mu[r]));
+                    l[r] += p[q];
                 }
-                bf16x8 ph[NR], pl[NR];
-#pragma unroll
-                for (int r = 0; r < NR; ++r)
-#pragma unroll
-                    for (int e = 0; e < 8; e += 2) {
-                        f32x2v p;
-#pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            p[q] = exp2_fast(__builtin_fmaf(s[r][(e + q) >> 2][(e + q) & 3], a.scale2, -mu[r]));
-                            l[r] += p[q];
-                        }
-                        const bf16x2v hi = __builtin_convertvector(p, bf16x2v);
-                        ph[r][e] = hi[0];
-                        ph[r][e + 1] = hi[1];
-                        if (SPLIT) {
-                            const f32x2v back = __builtin_convertvector(hi, f32x2v);
-                            const f32x2v rest = {p[0] - back[0], p[1] - back[1]};
-                            const bf16x2v lo = __builtin_convertvector(rest, bf16x2v);
-                            pl[r][e] = lo[0];
-                            pl[r][e + 1] = lo[1];
-                        }
-                    }
-                bf16x8 vv[DB];
+                const bf16x2v hi = __builtin_convertvector(p, bf16x2v);
+                ph[hu][r][e] = hi[0];
+                ph[hu][r][e + 1] = hi[1];
+                if (SPLIT) {
+                    const f32x2v back = __builtin_convertvector(hi, f32x2v);
+                    const f32x2v rest = {p[0] - back[0], p[1] - back[1]};
+                    const bf16x2v lo = __builtin_convertvector(rest, bf16x2v);
+                    pl[hu][r][e] = lo[0];
+                    pl[hu][r][e + 1] = lo[1];
+                }
+            };
+            // The product of a half, instruction i of kSteps.  The two of an
+            // accumulator stand apart: the second waits for the first.
+            constexpr int kSteps = NR * DB * (SPLIT ? 2 : 1);
+            bf16x8 vv[DB];
+            auto convert = [&]() {
 #pragma unroll
                 for (int db = 0; db < DB; ++db) {
                     if constexpr (FP8)
@@ -451,19 +466,35 @@ __global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(AttArgs a) {
                     else
                         vv[db] = bytes8(vr[db]);
                 }
-                // The two products of an accumulator stand apart: the second
-                // waits for the first.
+            };
+            auto product = [&](int hu, int i) {
+                const int db = i % (NR * DB) / NR, r = i % NR;
+                o[r][db] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vv[db], i < NR * DB ? ph[hu][r] : pl[hu][r], o[r][db], 0, 0, 0);
+            };
 #pragma unroll
-                for (int db = 0; db < DB; ++db)
+            for (int r = 0; r < NR; ++r)
 #pragma unroll
-                    for (int r = 0; r < NR; ++r)
-                        o[r][db] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vv[db], ph[r], o[r][db], 0, 0, 0);
-                if (SPLIT)
+                for (int e = 0; e < 8; e += 2) weights(0, r, e);
+            convert();
+            if (HH == 1) {
 #pragma unroll
-                    for (int db = 0; db < DB; ++db)
+                for (int i = 0; i < kSteps; ++i) product(0, i);
+            } else {
+                // The second half's weights are formed while the matrix cores
+                // are busy with the first half's product, piece by piece.
+                constexpr int kPieces = 4 * NR;
 #pragma unroll
-                        for (int r = 0; r < NR; ++r)
-                            o[r][db] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vv[db], pl[r], o[r][db], 0, 0, 0);
+                for (int u = 0; u < kPieces; ++u) {
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int i = u * kSteps / kPieces; i < (u + 1) * kSteps / kPieces; ++i) product(0, i);
+                    weights(HH - 1, u / 4, u % 4 * 2);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                read_v(HH - 1);
+                convert();
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i) product(HH - 1, i);
             }
         };
         // Tokens past the end, and those of a missing page, may hold anything,
