@@ -331,23 +331,36 @@ def beam_select(logits, beams, score, k, done=None, eos=-1, stream=None):
     uint8), each [requests][k], of a device fp32 or bf16 logits tensor [requests * beams][V]."""
     import torch
     rows, V = logits.shape
-    batch = rows // beams
-    _expect(rows == batch * beams, "logits: %d rows are not a multiple of %d beams" % (rows, beams))
-    _expect(logits.dtype in (torch.float32, torch.bfloat16), "logits: not float32 or bfloat16")
-    _expect(logits.stride(1) == 1 or V == 1, "logits: rows are not contiguous")
-    _vector(score, torch.float32, rows, "score")
-    if done is not None:
-        _vector(done, torch.uint8, rows, "done")
-    dev = logits.device
-    out = torch.empty((batch, k), dtype=torch.float32, device=dev)
-    parent = torch.empty((batch, k), dtype=torch.int32, device=dev)
-    token = torch.empty((batch, k), dtype=torch.int32, device=dev)
-    ended = torch.empty((batch, k), dtype=torch.uint8, device=dev)
-    wsb = nvfp4_beam_workspace_bytes(batch, beams, V)
-    ws = torch.empty(max(wsb, 16), dtype=torch.uint8, device=dev)
-    nvfp4_beam_select(logits, OUT_F32 if logits.dtype == torch.float32 else OUT_BF16,
-                      logits.stride(0) if rows > 1 else max(logits.stride(0), V), batch, beams, V,
-                      score, done, eos, k, out, parent, token, ended, ws, wsb, stream)
+    batch = rows // beams if beams > 0 else 0
+    if rows != batch * beams:
+        _refuse("logits: %d rows are not a multiple of %d beams" % (rows, beams))
+    ld, inner = logits.stride()
+    if inner != 1 and V > 1:
+        _refuse("logits: rows are not contiguous")
+    if logits.dtype is torch.float32:
+        dtype = OUT_F32
+    elif logits.dtype is torch.bfloat16:
+        dtype = OUT_BF16
+    else:
+        _refuse("logits: not float32 or bfloat16")
+    if not (score.dtype is torch.float32 and score.numel() == rows and score.is_contiguous()):
+        _refuse("score: not %d contiguous float32 values" % rows)
+    if done is not None and not (done.dtype is torch.uint8 and done.numel() == rows and done.is_contiguous()):
+        _refuse("done: not %d contiguous uint8 values" % rows)
+    L, dev = _lib or lib(), logits.device
+    shape = (batch, k)
+    out = torch.empty(shape, dtype=torch.float32, device=dev)
+    parent = torch.empty(shape, dtype=torch.int32, device=dev)
+    token = torch.empty(shape, dtype=torch.int32, device=dev)
+    ended = torch.empty(shape, dtype=torch.uint8, device=dev)
+    wsb = L.nvfp4_beam_workspace_bytes(batch, beams, V)
+    ws = torch.empty(wsb or 16, dtype=torch.uint8, device=dev)
+    st = L.nvfp4_beam_select(logits.data_ptr(), dtype, ld if rows > 1 else max(ld, V), batch, beams, V,
+                             score.data_ptr(), None if done is None else done.data_ptr(), eos, k,
+                             out.data_ptr(), parent.data_ptr(), token.data_ptr(), ended.data_ptr(),
+                             ws.data_ptr(), wsb, _current(dev) if stream is None else _stream(stream))
+    if st:
+        _check(st)
     return out, parent, token, ended
 
 
@@ -470,22 +483,16 @@ class PackedWeight:
         return pw
 
 
-def _expect(ok, message):
-    if not ok:
-        raise Nvfp4Error(EINVAL, message)
+def _refuse(message):
+    raise Nvfp4Error(EINVAL, message)
 
 
-def _vector(x, dtype, n, name):
-    """A contiguous device vector of n values of a type."""
-    _expect(x.dtype == dtype, "%s: not %s" % (name, dtype))
-    _expect(x.numel() == n and x.is_contiguous(), "%s: not %d contiguous values" % (name, n))
-
-
-def _rows(x, dtype, width, name):
-    """Leading dimension of a matrix of rows of at least `width` contiguous values."""
-    _expect(x.dtype == dtype and x.dim() == 2, "%s: not a %s matrix" % (name, dtype))
-    _expect(x.shape[1] >= width and x.stride(1) == 1, "%s: rows are not %d contiguous values" % (name, width))
-    return x.stride(0) if x.shape[0] > 1 else max(x.stride(0), x.shape[1])
+def _current(device):
+    """torch's current stream on a device, as a handle."""
+    import torch
+    if device.type != "cuda":
+        return 0
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 class PagedCache:
@@ -496,70 +503,93 @@ class PagedCache:
     value.  A page is contiguous; layers and pages may have other strides (equal ones for k and v).
 
     ``row_start`` (int32 [lanes + 1]), ``ctx_len`` (int32 [lanes]) and ``page_table`` (int32
-    [lanes][pages of a lane]) are device tensors; include/nvfp4.h has the rules of each call.
-    Workspaces come from torch's allocator on the current stream, call by call.
+    [lanes][pages of a lane], contiguous) are device tensors; include/nvfp4.h has the rules of
+    each call.  Workspaces come from torch's allocator on the current stream, call by call.
+    (The checks are written out in each method: they run once per layer and round.)
     """
 
     def __init__(self, k, v, k_scale=1.0, v_scale=1.0):
         import torch
-        _expect(k.dim() == 5 and v.dim() == 6, "k, v: not 5 and 6 dimensions")
+        if k.dim() != 5 or v.dim() != 6:
+            _refuse("k, v: not 5 and 6 dimensions")
         layers, pages, heads, tokens, dim = k.shape
-        _expect(tuple(v.shape) == (layers, pages, heads, tokens // 16, dim, 16),
-                "v: shape %s does not go with k's %s" % (tuple(v.shape), tuple(k.shape)))
-        _expect(k.dtype == v.dtype and k.dtype in (torch.bfloat16, torch.float8_e4m3fn),
-                "k, v: not both bfloat16 or float8_e4m3fn")
-        dense = (tokens * dim, dim, 1), (tokens * dim, 16 * dim, 16, 1)
-        for x, want, name in ((k, dense[0], "k"), (v, dense[1], "v")):
-            _expect(all(n == 1 or a == b for n, a, b in zip(x.shape[2:], x.stride()[2:], want)),
-                    "%s: a page is not contiguous" % name)
+        if tuple(v.shape) != (layers, pages, heads, tokens // 16, dim, 16):
+            _refuse("v: shape %s does not go with k's %s" % (tuple(v.shape), tuple(k.shape)))
+        if k.dtype != v.dtype or k.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+            _refuse("k, v: not both bfloat16 or float8_e4m3fn")
+        for x, want, name in ((k, (tokens * dim, dim, 1), "k"),
+                              (v, (tokens * dim, 16 * dim, 16, 1), "v")):
+            if any(n != 1 and a != b for n, a, b in zip(x.shape[2:], x.stride()[2:], want)):
+                _refuse("%s: a page is not contiguous" % name)
         es = k.element_size()
-        strides = [0 if n == 1 else s * es for n, s in zip(k.shape[:2], k.stride()[:2])]
-        _expect(strides == [0 if n == 1 else s * es for n, s in zip(v.shape[:2], v.stride()[:2])],
-                "k, v: layers or pages have different strides")
-        if pages == 1 and layers > 1 and strides[0]:
-            strides[1] = 0
+        strides = [[0 if n == 1 else s * es for n, s in zip(x.shape[:2], x.stride()[:2])]
+                   for x in (k, v)]
+        if strides[0] != strides[1]:
+            _refuse("k, v: layers or pages have different strides")
         self.k, self.v = k, v
         self.layers, self.pages, self.kv_heads, self.page_tokens, self.head_dim = k.shape
+        self.device = k.device
         self.desc = Cache(k.data_ptr(), v.data_ptr(), layers, pages, heads, tokens, dim,
                           CACHE_BF16 if es == 2 else CACHE_E4M3, float(k_scale), float(v_scale),
-                          strides[1], strides[0])
+                          strides[0][1], strides[0][0])
+        self._ref = ctypes.byref(self.desc)
 
-    def _lanes(self, row_start, ctx_len, page_table):
+    def _bad_lanes(self, row_start, ctx_len, page_table, lanes):
+        """Names what is wrong with a call's lanes."""
         import torch
-        lanes = ctx_len.numel()
-        _vector(ctx_len, torch.int32, lanes, "ctx_len")
-        if row_start is not None:
-            _vector(row_start, torch.int32, lanes + 1, "row_start")
-        ld = _rows(page_table, torch.int32, 1, "page_table")
-        _expect(page_table.shape[0] == lanes, "page_table: %d rows for %d lanes"
-                % (page_table.shape[0], lanes))
-        # a view of wider rows: entries past its own width are not the lane's
-        _expect(ld == page_table.shape[1], "page_table: not contiguous")
-        return lanes, ld
+        for x, n, name in ((row_start, lanes + 1, "row_start"), (ctx_len, lanes, "ctx_len")):
+            if x is not None and not (x.dtype is torch.int32 and x.numel() == n and x.is_contiguous()):
+                _refuse("%s: not %d contiguous int32 values" % (name, n))
+        _refuse("page_table: not a contiguous int32 matrix of %d rows" % lanes)
 
     def append(self, layer, qkv, q_heads, row_start, ctx_len, page_table, positions, inv_freq,
                pair_axis=None, interleaved=False, factor=1.0, out=None, stream=None):
         """Rotates q and k of a qkv product's rows, stores k and v, returns q [rows][q_heads * dim]."""
         import torch
-        rows = qkv.shape[0]
-        lanes, table_ld = self._lanes(row_start, ctx_len, page_table)
-        qkv_ld = _rows(qkv, torch.bfloat16, (q_heads + 2 * self.kv_heads) * self.head_dim, "qkv")
-        pairs = inv_freq.numel()
-        _vector(inv_freq, torch.float32, pairs, "inv_freq")
-        axes = positions.shape[1] if positions.dim() == 2 else 1
-        _vector(positions, torch.int32, rows * axes, "positions")
-        if pair_axis is not None:
-            _vector(pair_axis, torch.uint8, pairs, "pair_axis")
+        i32, bf16 = torch.int32, torch.bfloat16
+        lanes, dim, L, dev = ctx_len.numel(), self.head_dim, _lib or lib(), self.device
+        if not (ctx_len.dtype is i32 and ctx_len.is_contiguous() and row_start.dtype is i32
+                and row_start.is_contiguous() and row_start.numel() == lanes + 1
+                and page_table.dtype is i32 and page_table.is_contiguous()
+                and page_table.dim() == 2 and page_table.shape[0] == lanes):
+            self._bad_lanes(row_start, ctx_len, page_table, lanes)
+        width = q_heads * dim
+        if qkv.dtype is not bf16 or qkv.dim() != 2:
+            _refuse("qkv: not a bfloat16 matrix")
+        rows, cols = qkv.shape
+        ld, inner = qkv.stride()
+        if cols < width + 2 * self.kv_heads * dim or inner != 1:
+            _refuse("qkv: rows are not %d contiguous values" % (width + 2 * self.kv_heads * dim))
+        pairs, axes = inv_freq.numel(), positions.shape[1] if positions.dim() == 2 else 1
+        if not (inv_freq.dtype is torch.float32 and inv_freq.is_contiguous()):
+            _refuse("inv_freq: not contiguous float32 values")
+        if not (positions.dtype is i32 and positions.is_contiguous() and positions.numel() == rows * axes):
+            _refuse("positions: not %d contiguous int32 values" % (rows * axes))
+        if pair_axis is not None and not (pair_axis.dtype is torch.uint8 and pair_axis.is_contiguous()
+                                          and pair_axis.numel() == pairs):
+            _refuse("pair_axis: not %d contiguous uint8 values" % pairs)
         if out is None:
-            out = torch.empty((rows, q_heads * self.head_dim), dtype=torch.bfloat16,
-                              device=qkv.device)
-        _expect(out.shape[0] >= rows, "out: %d rows of %d" % (out.shape[0], rows))
-        q_ld = _rows(out, torch.bfloat16, q_heads * self.head_dim, "out")
-        rot = Rotary(positions.data_ptr(), inv_freq.data_ptr(), _ptr(pair_axis), axes, pairs,
-                     int(interleaved), float(factor))
-        nvfp4_cache_append(self.desc, layer, qkv, qkv_ld, rows, q_heads, lanes, row_start, ctx_len,
-                           page_table, table_ld, rot, out, q_ld, stream)
+            out, q_ld = torch.empty((rows, width), dtype=bf16, device=dev), width
+        else:
+            q_ld = self._out_ld(out, rows, width)
+        rot = Rotary(positions.data_ptr(), inv_freq.data_ptr(),
+                     None if pair_axis is None else pair_axis.data_ptr(), axes, pairs, interleaved, factor)
+        st = L.nvfp4_cache_append(self._ref, layer, qkv.data_ptr(), ld if rows > 1 else max(ld, cols), rows,
+                                  q_heads, lanes, row_start.data_ptr(), ctx_len.data_ptr(),
+                                  page_table.data_ptr(), page_table.shape[1], ctypes.byref(rot), out.data_ptr(),
+                                  q_ld, _current(dev) if stream is None else _stream(stream))
+        if st:
+            _check(st)
         return out
+
+    def _out_ld(self, out, rows, width):
+        """Leading dimension of a caller's output of at least `rows` rows."""
+        import torch
+        if out.dtype is not torch.bfloat16 or out.dim() != 2 or out.shape[0] < rows:
+            _refuse("out: not a bfloat16 matrix of %d rows" % rows)
+        if out.shape[1] < width or out.stride(1) != 1:
+            _refuse("out: rows are not %d contiguous values" % width)
+        return out.stride(0) if out.shape[0] > 1 else max(out.stride(0), out.shape[1])
 
     def attend(self, layer, q, row_start, ctx_len, page_table, mask, max_rows, scale, out=None,
                with_lse=False, stream=None):
@@ -567,55 +597,84 @@ class PagedCache:
         drafts its mask words (int64 [rows]) name; max_rows: at least any lane's rows.  Returns
         out, or (out, lse fp32 [rows][q_heads])."""
         import torch
-        rows, width = q.shape
-        dim = self.head_dim
-        q_heads = width // dim
-        lanes, table_ld = self._lanes(row_start, ctx_len, page_table)
-        q_ld = _rows(q, torch.bfloat16, q_heads * dim, "q")
-        _vector(mask, torch.int64, rows, "mask")
+        i32, bf16 = torch.int32, torch.bfloat16
+        lanes, dim, L, dev = ctx_len.numel(), self.head_dim, _lib or lib(), self.device
+        if not (ctx_len.dtype is i32 and ctx_len.is_contiguous() and row_start.dtype is i32
+                and row_start.is_contiguous() and row_start.numel() == lanes + 1
+                and page_table.dtype is i32 and page_table.is_contiguous()
+                and page_table.dim() == 2 and page_table.shape[0] == lanes):
+            self._bad_lanes(row_start, ctx_len, page_table, lanes)
+        if q.dtype is not bf16 or q.dim() != 2:
+            _refuse("q: not a bfloat16 matrix")
+        rows, cols = q.shape
+        ld, inner = q.stride()
+        q_heads = cols // dim
+        width = q_heads * dim
+        if inner != 1:
+            _refuse("q: rows are not contiguous")
+        if not (mask.dtype is torch.int64 and mask.numel() == rows and mask.is_contiguous()):
+            _refuse("mask: not %d contiguous int64 values" % rows)
         if out is None:
-            out = torch.empty((rows, q_heads * dim), dtype=torch.bfloat16, device=q.device)
-        _expect(out.shape[0] >= rows, "out: %d rows of %d" % (out.shape[0], rows))
-        out_ld = _rows(out, torch.bfloat16, q_heads * dim, "out")
-        lse = torch.empty((rows, q_heads), dtype=torch.float32, device=q.device) if with_lse else None
-        wsb = nvfp4_tree_attention_workspace_bytes(q_heads, self.kv_heads, dim, max_rows)
-        ws = torch.empty(max(wsb, 16), dtype=torch.uint8, device=q.device)
-        nvfp4_tree_attention(self.desc, layer, q, q_ld, q_heads, lanes, max_rows, row_start,
-                             ctx_len, page_table, table_ld, mask, scale, out, out_ld, lse, ws, wsb,
-                             stream)
+            out, out_ld = torch.empty((rows, width), dtype=bf16, device=dev), width
+        else:
+            out_ld = self._out_ld(out, rows, width)
+        lse = torch.empty((rows, q_heads), dtype=torch.float32, device=dev) if with_lse else None
+        wsb = L.nvfp4_tree_attention_workspace_bytes(q_heads, self.kv_heads, dim, max_rows)
+        ws = torch.empty(wsb or 16, dtype=torch.uint8, device=dev)
+        st = L.nvfp4_tree_attention(self._ref, layer, q.data_ptr(), ld if rows > 1 else max(ld, width), q_heads,
+                                    lanes, max_rows, row_start.data_ptr(), ctx_len.data_ptr(),
+                                    page_table.data_ptr(), page_table.shape[1], mask.data_ptr(), scale,
+                                    out.data_ptr(), out_ld, lse.data_ptr() if with_lse else None,
+                                    ws.data_ptr(), wsb, _current(dev) if stream is None else _stream(stream))
+        if st:
+            _check(st)
         return (out, lse) if with_lse else out
 
     def compact(self, ctx_len, page_table, path, accepted, stream=None):
         """Moves each lane's accepted drafts (path int32 [lanes][n], accepted int32 [lanes]) to the
         front of its drafted tokens, in every layer."""
         import torch
-        lanes, table_ld = self._lanes(None, ctx_len, page_table)
-        path_ld = _rows(path, torch.int32, 1, "path")
-        _expect(path.shape[0] == lanes and path_ld == path.shape[1],
-                "path: not %d contiguous rows" % lanes)
-        _vector(accepted, torch.int32, lanes, "accepted")
-        nvfp4_cache_compact(self.desc, lanes, ctx_len, page_table, table_ld, path, path_ld,
-                            accepted, stream)
+        i32, lanes, L = torch.int32, ctx_len.numel(), _lib or lib()
+        if not (ctx_len.dtype is i32 and ctx_len.is_contiguous() and page_table.dtype is i32
+                and page_table.is_contiguous() and page_table.dim() == 2 and page_table.shape[0] == lanes):
+            self._bad_lanes(None, ctx_len, page_table, lanes)
+        if not (path.dtype is i32 and path.is_contiguous() and path.dim() == 2 and path.shape[0] == lanes):
+            _refuse("path: not a contiguous int32 matrix of %d rows" % lanes)
+        if not (accepted.dtype is i32 and accepted.is_contiguous() and accepted.numel() == lanes):
+            _refuse("accepted: not %d contiguous int32 values" % lanes)
+        st = L.nvfp4_cache_compact(self._ref, lanes, ctx_len.data_ptr(), page_table.data_ptr(),
+                                   page_table.shape[1], path.data_ptr(), path.shape[1], accepted.data_ptr(),
+                                   _current(self.device) if stream is None else _stream(stream))
+        if st:
+            _check(st)
 
     def update(self, page_table, length, refs, parent, keep=None, reserve=None, stream=None):
         """New tables from old ones (reorder, fork, truncate, free, make room): returns
         (page_table, length, refs, short), all int32; shared partly filled pages are copied."""
         import torch
-        lanes_in, table_ld = self._lanes(None, length, page_table)
-        lanes_out = parent.numel()
-        _vector(refs, torch.int32, self.pages, "refs")
+        i32, lanes, L, dev = torch.int32, length.numel(), _lib or lib(), self.device
+        if not (length.dtype is i32 and length.is_contiguous() and page_table.dtype is i32
+                and page_table.is_contiguous() and page_table.dim() == 2 and page_table.shape[0] == lanes):
+            self._bad_lanes(None, length, page_table, lanes)
+        if not (refs.dtype is i32 and refs.is_contiguous() and refs.numel() == self.pages):
+            _refuse("refs: not %d contiguous int32 values" % self.pages)
+        n, width = parent.numel(), page_table.shape[1]
         for x, name in ((parent, "parent"), (keep, "keep"), (reserve, "reserve")):
-            if x is not None:
-                _vector(x, torch.int32, lanes_out, name)
-        dev = page_table.device
-        table = torch.empty((lanes_out, table_ld), dtype=torch.int32, device=dev)
-        new_len = torch.empty(lanes_out, dtype=torch.int32, device=dev)
-        new_refs = torch.empty(self.pages, dtype=torch.int32, device=dev)
-        short = torch.empty(1, dtype=torch.int32, device=dev)
-        wsb = nvfp4_cache_update_workspace_bytes(self.pages, lanes_out, table_ld)
-        ws = torch.empty(max(wsb, 16), dtype=torch.uint8, device=dev)
-        nvfp4_cache_update(self.desc, lanes_in, page_table, length, refs, table_ld, lanes_out,
-                           parent, keep, reserve, table, new_len, new_refs, short, ws, wsb, stream)
+            if x is not None and not (x.dtype is i32 and x.is_contiguous() and x.numel() == n):
+                _refuse("%s: not %d contiguous int32 values" % (name, n))
+        table = torch.empty((n, width), dtype=i32, device=dev)
+        new_len = torch.empty(n, dtype=i32, device=dev)
+        new_refs = torch.empty(self.pages, dtype=i32, device=dev)
+        short = torch.empty(1, dtype=i32, device=dev)
+        wsb = L.nvfp4_cache_update_workspace_bytes(self.pages, n, width)
+        ws = torch.empty(wsb or 16, dtype=torch.uint8, device=dev)
+        st = L.nvfp4_cache_update(self._ref, lanes, page_table.data_ptr(), length.data_ptr(), refs.data_ptr(),
+                                  width, n, parent.data_ptr(), None if keep is None else keep.data_ptr(),
+                                  None if reserve is None else reserve.data_ptr(), table.data_ptr(),
+                                  new_len.data_ptr(), new_refs.data_ptr(), short.data_ptr(), ws.data_ptr(), wsb,
+                                  _current(dev) if stream is None else _stream(stream))
+        if st:
+            _check(st)
         return table, new_len, new_refs, short
 
 
