@@ -21,7 +21,9 @@ namespace nvfp4 {
 
 constexpr int kBeamGroup = 1024;
 constexpr int kBeamThreads = 256;      // scan: 4 waves, one group each
+constexpr int kBeamRun = 2;            // groups per wave
 constexpr int kBeamPickThreads = 512;  // pick: 8 waves
+constexpr int kBeamList = 1024;        // keys the pick kernel ranks at once
 
 struct BeamArgs {
     const void* logits;
@@ -125,34 +127,58 @@ __device__ __forceinline__ void load_group(const BeamArgs& a, int row, int group
     }
 }
 
+// The wave's maximum and sum, uniform: as wave_max64, within rows of 16 lanes by
+// DPP, then over the four rows.
+template <int CTRL>
+__device__ __forceinline__ float dppf(float v) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(v), __float_as_int(v), CTRL, 0xF, 0xF, false));
+}
+__device__ __forceinline__ float lanef(float v, int lane) {
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
+}
 __device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) v = fmaxf(v, __shfl_xor(v, d));
-    return v;
+    v = fmaxf(v, dppf<0xB1>(v));
+    v = fmaxf(v, dppf<0x4E>(v));
+    v = fmaxf(v, dppf<0x141>(v));
+    v = fmaxf(v, dppf<0x140>(v));
+    return fmaxf(fmaxf(lanef(v, 0), lanef(v, 16)), fmaxf(lanef(v, 32), lanef(v, 48)));
 }
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
-    return v;
+    v += dppf<0xB1>(v);
+    v += dppf<0x4E>(v);
+    v += dppf<0x141>(v);
+    v += dppf<0x140>(v);
+    return (lanef(v, 0) + lanef(v, 16)) + (lanef(v, 32) + lanef(v, 48));
+}
+// exp(x - m): the difference is rounded before it is scaled, so that terms near
+// the maximum, which make up the sum, are off by 2^-22 or less.
+__device__ __forceinline__ float exp_diff(float x, float m) {
+    return __builtin_amdgcn_exp2f((x - m) * 1.44269504088896340736f);
 }
 
+// A wave takes kBeamRun groups, all of their loads in flight at once.
 template <bool BF16, bool VEC>
 __global__ __launch_bounds__(kBeamThreads) void beam_scan_kernel(BeamArgs a) {
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), lane = threadIdx.x & 63;
-    const int group = blockIdx.x * (kBeamThreads / 64) + wave, row = blockIdx.y;
-    if (group >= a.groups) return;  // whole wave
-    float x[16];
-    load_group<BF16, VEC>(a, row, group, lane, row_state(a, row), x);
-    float m = x[0];
+    const int group0 = (blockIdx.x * (kBeamThreads / 64) + wave) * kBeamRun, row = blockIdx.y;
+    if (group0 >= a.groups) return;  // whole wave
+    const int state = row_state(a, row);
+    float x[kBeamRun][16];
 #pragma unroll
-    for (int e = 1; e < 16; ++e) m = fmaxf(m, x[e]);
-    m = wave_max(m);
-    const float use = m == -__builtin_inff() ? 0.f : m;
-    float s = 0.f;
+    for (int u = 0; u < kBeamRun; ++u) load_group<BF16, VEC>(a, row, group0 + u, lane, state, x[u]);
 #pragma unroll
-    for (int e = 0; e < 16; ++e) s += expf(x[e] - use);
-    s = wave_sum(s);
-    if (lane == 0) a.part[(long long)row * a.groups + group] = make_float2(m, s);
+    for (int u = 0; u < kBeamRun; ++u) {
+        float m = x[u][0];
+#pragma unroll
+        for (int e = 1; e < 16; ++e) m = fmaxf(m, x[u][e]);
+        m = wave_max(m);
+        const float use = m == -__builtin_inff() ? 0.f : m;
+        float s = 0.f;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s += exp_diff(x[u][e], use);
+        s = wave_sum(s);
+        if (lane == 0 && group0 + u < a.groups) a.part[(long long)row * a.groups + group0 + u] = make_float2(m, s);
+    }
 }
 
 // Merges the lane's N keys into the wave's sorted list (lane r: the r-th
@@ -160,7 +186,6 @@ __global__ __launch_bounds__(kBeamThreads) void beam_scan_kernel(BeamArgs a) {
 template <int N>
 __device__ __forceinline__ u64 wave_keep(u64 kept, u64 (&x)[N], int k, int lane) {
     u64 out = 0;
-    unsigned int used = 0;
     for (int r = 0; r < k; ++r) {
         u64 head = kept;
 #pragma unroll
@@ -172,7 +197,6 @@ __device__ __forceinline__ u64 wave_keep(u64 kept, u64 (&x)[N], int k, int lane)
 #pragma unroll
         for (int j = 0; j < N; ++j) x[j] = x[j] == top ? 0 : x[j];
     }
-    (void)used;
     return out;
 }
 
@@ -180,104 +204,193 @@ __device__ __forceinline__ float beam_score(float c, float x, float m, float z) 
     return x == -__builtin_inff() ? x : c + ((x - m) - z);
 }
 
+// Appends the wave's keys that are at least `bar` to a list in LDS (in no
+// particular order); *count goes on past the list's end.
+__device__ __forceinline__ void append_keys(u64 key, bool take, u64* list, int* count, int lane) {
+    const unsigned long long mine = __ballot(take);
+    if (!mine) return;
+    int at = 0;
+    if (lane == 0) at = atomicAdd(count, __popcll(mine));
+    at = __builtin_amdgcn_readfirstlane(at) + __popcll(mine & ((1ull << lane) - 1ull));
+    if (take && at < kBeamList) list[at] = key;
+}
+
+// The k largest of n distinct keys, in order: a key's place is the number of
+// larger ones.  best[] past n is 0.
+__device__ __forceinline__ void rank_keys(const u64* list, int n, int k, u64* best) {
+    for (int i = threadIdx.x; i < n; i += kBeamPickThreads) {
+        const u64 x = list[i];
+        int place = 0;
+#pragma unroll 8
+        for (int j = 0; j < n; ++j) place += list[j] > x ? 1 : 0;
+        if (place < k) best[place] = x;
+    }
+    if ((int)threadIdx.x >= n && (int)threadIdx.x < k) best[threadIdx.x] = 0;
+}
+
+// The k-th largest of the wave's 64 keys, one a lane (the smallest nonzero one
+// if there are fewer than k; keys are distinct but for zeros).
+__device__ __forceinline__ u64 wave_kth(u64 head, int k) {
+    u64 lo = 1, hi = ~0ull;  // at least k keys >= lo (or lo = 1), fewer than k > hi
+    while (lo < hi) {
+        const u64 mid = lo + (hi - lo) / 2 + ((hi - lo) & 1);
+        const int n = __popcll(__ballot(head >= mid));
+        if (n == k) return mid;
+        if (n > k)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
+}
+
 template <bool BF16, bool VEC>
 __global__ __launch_bounds__(kBeamPickThreads) void beam_pick_kernel(BeamArgs a) {
     constexpr int kWaves = kBeamPickThreads / 64;
     __shared__ float row_m[NVFP4_BEAM_MAX_BEAMS], row_z[NVFP4_BEAM_MAX_BEAMS], row_c[NVFP4_BEAM_MAX_BEAMS];
     __shared__ int row_s[NVFP4_BEAM_MAX_BEAMS];
-    __shared__ u64 lists[kWaves][64];
+    __shared__ u64 list[kBeamList];
     __shared__ u64 best[64];
+    __shared__ int counts[2];
+    static_assert(kBeamList >= kWaves * 64, "the waves' lists fit");
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), lane = threadIdx.x & 63;
     const int row0 = blockIdx.x * a.beams;
+    if (threadIdx.x < 2) counts[threadIdx.x] = 0;
 
+    // Each row's maximum and log-sum.
     for (int r = wave; r < a.beams; r += kWaves) {
         const float2* part = a.part + (long long)(row0 + r) * a.groups;
+        const float c = a.score[row0 + r];
+        const int state = row_state(a, row0 + r);
         float m = -__builtin_inff(), s = 0.f;
-        for (int i = lane; i < a.groups; i += 64) {
-            const float2 p = part[i];
-            const float mx = fmaxf(m, p.x), use = mx == -__builtin_inff() ? 0.f : mx;
-            s = s * expf(m - use) + p.y * expf(p.x - use);
+        for (int i0 = 0; i0 < a.groups; i0 += 64 * 4) {
+            float2 p[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int i = i0 + 64 * j + lane;
+                p[j] = part[min(i, a.groups - 1)];
+                if (i >= a.groups) p[j] = make_float2(-__builtin_inff(), 0.f);
+            }
+            const float mx = fmaxf(fmaxf(fmaxf(p[0].x, p[1].x), fmaxf(p[2].x, p[3].x)), m);
+            const float use = mx == -__builtin_inff() ? 0.f : mx;
+            s *= exp_diff(m, use);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s = __builtin_fmaf(p[j].y, exp_diff(p[j].x, use), s);
             m = mx;
         }
         const float mx = wave_max(m), use = mx == -__builtin_inff() ? 0.f : mx;
-        s = wave_sum(s * expf(m - use));
+        s = wave_sum(s * exp_diff(m, use));
         if (lane == 0) {
             row_m[r] = use;
             row_z[r] = logf(s);
-            row_c[r] = a.score[row0 + r];
-            row_s[r] = row_state(a, row0 + r);
+            row_c[r] = c;
+            row_s[r] = state;
         }
     }
     __syncthreads();
 
-    // The k best groups.
-    const long long n = (long long)a.beams * a.groups;
-    u64 kept = 0;
-    for (long long i0 = wave * 64 * 4; i0 < n; i0 += kBeamPickThreads * 4) {
-        u64 x[4];
+    // The k best groups.  The k-th best of the lanes' best groups bounds them
+    // from below; what passes it is ranked.
+    const int n = a.beams * a.groups;
+    auto group_key = [&](int i) -> u64 {
+        if (i >= n) return 0;
+        const int r = (int)((unsigned)i / (unsigned)a.groups), g = i - r * a.groups;
+        const float m = a.part[(long long)(row0 + r) * a.groups + g].x;
+        return topk_key(beam_score(row_c[r], m, row_m[r], row_z[r]), r * a.V + g * kBeamGroup);
+    };
+    u64 head = 0;
+    for (int i = threadIdx.x; i < n; i += kBeamPickThreads) head = max64(head, group_key(i));
+    const u64 bar = wave_kth(head, a.k);
+    for (int i0 = wave * 64; i0 < n; i0 += kBeamPickThreads) {
+        const u64 key = group_key(i0 + lane);
+        append_keys(key, key >= bar, list, &counts[0], lane);
+    }
+    __syncthreads();
+    if (counts[0] <= kBeamList) {
+        rank_keys(list, counts[0], a.k, best);
+        __syncthreads();
+    } else {
+        // Too many pass (a large k over many beams): every wave keeps the k
+        // best of what it looks at, and the first joins them.
+        __syncthreads();
+        u64 kept = 0;
+        for (int i0 = wave * 64 * 4; i0 < n; i0 += kBeamPickThreads * 4) {
+            u64 x[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const long long i = i0 + 64 * j + lane;
-            x[j] = 0;
-            if (i < n) {
-                const int r = (int)(i / a.groups), g = (int)(i - (long long)r * a.groups);
-                const float m = a.part[(long long)(row0 + r) * a.groups + g].x;
-                x[j] = topk_key(beam_score(row_c[r], m, row_m[r], row_z[r]), r * a.V + g * kBeamGroup);
-            }
+            for (int j = 0; j < 4; ++j) x[j] = group_key(i0 + 64 * j + lane);
+            kept = wave_keep<4>(kept, x, a.k, lane);
         }
-        kept = wave_keep<4>(kept, x, a.k, lane);
-    }
-    lists[wave][lane] = lane < a.k ? kept : 0;
-    __syncthreads();
-    if (wave == 0) {
-        u64 x[kWaves];
+        list[wave * 64 + lane] = lane < a.k ? kept : 0;
+        __syncthreads();
+        if (wave == 0) {
+            u64 x[kWaves];
 #pragma unroll
-        for (int j = 0; j < kWaves; ++j) x[j] = lists[j][lane];
-        best[lane] = wave_keep<kWaves>(0, x, a.k, lane);
+            for (int j = 0; j < kWaves; ++j) x[j] = list[j * 64 + lane];
+            best[lane] = wave_keep<kWaves>(0, x, a.k, lane);
+        }
+        __syncthreads();
     }
-    __syncthreads();
 
     // Their candidates: none below the last group's best one can be listed.
     const u64 last = best[a.k - 1];
     const u64 floor = last ? ((last >> 32) << 32) | (unsigned int)((unsigned int)last - (kBeamGroup - 1)) : 1;
-    kept = 0;
-    for (int q = wave; q < a.k && best[q]; q += kWaves) {
-        const int flat = (int)~(unsigned int)best[q];
-        const int r = flat / a.V, g = (flat - r * a.V) / kBeamGroup;
-        float x[16];
-        load_group<BF16, VEC>(a, row0 + r, g, lane, row_s[r], x);
+    auto for_candidates = [&](auto&& f) {
+        for (int q = wave; q < a.k && best[q]; q += kWaves) {
+            const int flat = (int)~(unsigned int)best[q];
+            const int r = (int)((unsigned)flat / (unsigned)a.V), g = (flat - r * a.V) / kBeamGroup;
+            float x[16];
+            load_group<BF16, VEC>(a, row0 + r, g, lane, row_s[r], x);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            const int t = token_of<BF16, VEC>(g, lane, e);
-            const u64 key = t < a.V ? topk_key(beam_score(row_c[r], x[e], row_m[r], row_z[r]), r * a.V + t) : 0;
-            unsigned long long todo = __ballot(key >= floor);
+            for (int e = 0; e < 16; ++e) {
+                const int t = token_of<BF16, VEC>(g, lane, e);
+                f(t < a.V ? topk_key(beam_score(row_c[r], x[e], row_m[r], row_z[r]), r * a.V + t) : 0);
+            }
+        }
+    };
+    for_candidates([&](u64 key) { append_keys(key, key >= floor, list, &counts[1], lane); });
+    __syncthreads();
+    if (counts[1] <= kBeamList) {
+        const int found = counts[1];
+        __shared__ u64 winners[64];
+        rank_keys(list, found, a.k, winners);
+        __syncthreads();
+        if (threadIdx.x < 64) best[threadIdx.x] = winners[threadIdx.x];
+    } else {
+        // Many equal scores: the waves insert their candidates one by one into
+        // sorted lists of their own.
+        __syncthreads();
+        u64 kept = 0;
+        for_candidates([&](u64 key) {
+            unsigned long long todo = __ballot(key >= floor && key > lane64(kept, a.k - 1));
             while (todo) {
-                // Insert one key into the wave's sorted list.
                 const u64 v = lane64(key, __ffsll(todo) - 1);
                 todo &= todo - 1;
                 u64 prev = ((u64)(unsigned int)__shfl_up((int)(kept >> 32), 1) << 32) | (unsigned int)__shfl_up((int)kept, 1);
                 if (lane == 0) prev = ~0ull;
                 kept = kept > v ? kept : prev > v ? v : prev;
             }
+        });
+        list[wave * 64 + lane] = lane < a.k ? kept : 0;
+        __syncthreads();
+        if (wave == 0) {
+            u64 x[kWaves];
+#pragma unroll
+            for (int j = 0; j < kWaves; ++j) x[j] = list[j * 64 + lane];
+            best[lane] = wave_keep<kWaves>(0, x, a.k, lane);
         }
     }
-    lists[wave][lane] = lane < a.k ? kept : 0;
     __syncthreads();
-    if (wave == 0) {
-        u64 x[kWaves];
-#pragma unroll
-        for (int j = 0; j < kWaves; ++j) x[j] = lists[j][lane];
-        const u64 key = wave_keep<kWaves>(0, x, a.k, lane);
-        if (lane < a.k) {
-            const int flat = (int)~(unsigned int)key;
-            const int r = flat / a.V, t = flat - r * a.V;
-            const unsigned int o = (unsigned int)(key >> 32);
-            const long long at = (long long)blockIdx.x * a.k + lane;
-            a.score_out[at] = __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
-            a.parent_out[at] = row0 + r;
-            a.token_out[at] = t;
-            if (a.done_out) a.done_out[at] = (row_s[r] == kRowDone || (a.done && a.done[row0 + r]) || t == a.eos) ? 1 : 0;
-        }
+    if ((int)threadIdx.x < a.k) {
+        const u64 key = best[threadIdx.x];
+        const int flat = (int)~(unsigned int)key;
+        // (a NaN among the logits can leave a place empty: token -1, in bounds)
+        const int r = key ? (int)((unsigned)flat / (unsigned)a.V) : 0, t = key ? flat - r * a.V : -1;
+        const unsigned int o = (unsigned int)(key >> 32);
+        const long long at = (long long)blockIdx.x * a.k + threadIdx.x;
+        a.score_out[at] = __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
+        a.parent_out[at] = row0 + r;
+        a.token_out[at] = t;
+        if (a.done_out) a.done_out[at] = (a.done && a.done[row0 + r]) || t == a.eos ? 1 : 0;
     }
 }
 
@@ -336,7 +449,8 @@ int nvfp4_beam_select(const void* logits_dev, int logits_dtype, int64_t ld, int 
     a.done_out = done_out_dev;
     const bool vec = ((uintptr_t)logits_dev & 15) == 0 && ld % (bf16 ? 8 : 4) == 0;
     hipStream_t s = (hipStream_t)stream;
-    const dim3 scan((unsigned)(a.groups + kBeamThreads / 64 - 1) / (kBeamThreads / 64), (unsigned)(batch * beams));
+    const int per_block = kBeamThreads / 64 * kBeamRun;
+    const dim3 scan((unsigned)(a.groups + per_block - 1) / per_block, (unsigned)(batch * beams));
     const dim3 pick((unsigned)batch);
 #define NVFP4_BEAM(B, W)                                                                          \
     if (bf16 == B && vec == W) {                                                                  \

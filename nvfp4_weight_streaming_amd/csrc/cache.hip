@@ -106,6 +106,7 @@ struct AppendArgs {
 };
 
 constexpr int kAppendThreads = 256;
+constexpr int kAppendBatch = 4;
 
 __device__ __forceinline__ float bf16_f32(uint16_t h) { return __uint_as_float((uint32_t)h << 16); }
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
@@ -196,46 +197,56 @@ __global__ __launch_bounds__(kAppendThreads) void append_kernel(AppendArgs a) {
     const uint16_t* row = a.qkv + (long long)r * a.ld;
     uint8_t* page = a.c.k + (long long)(stored ? id : 0) * a.c.page_stride;
     const int off = (int)p & (page_tokens - 1);
-    for (int u = share * kAppendThreads + threadIdx.x; u < units; u += a.shares * kAppendThreads) {
-        const int head = u / per_head, k = u - head * per_head;
-        const uint16_t* src = row + (long long)head * dim;
-        const bool is_q = head < a.q_heads;
-        if (!is_q && !stored) continue;
-        const bool fp8 = !is_q && a.c.fp8;
-        uint8_t* dst = is_q ? (uint8_t*)(a.q_out + (long long)r * a.q_ld + (long long)head * dim)
-                            : page + ((((long long)(head - a.q_heads) << a.c.log_page) + off) * dim) * es;
-        const int de = fp8 ? 1 : 2;
-        const float scale = a.c.k_scale;
-        float x[4], y[4];
-        if (k < rot) {
-            const int i0 = 4 * k;
-            const int dx = a.interleaved ? 2 * i0 : i0, dy = a.interleaved ? 2 * i0 + 4 : i0 + a.pairs;
-            get4(src + dx, x);
-            get4(src + dy, y);
-            float o1[4], o2[4];
+    // kAppendBatch units of a thread are read before the first is written.
+    const int step = a.shares * kAppendThreads;
+    for (int u0 = share * kAppendThreads + threadIdx.x; u0 < units; u0 += kAppendBatch * step) {
+        float x[kAppendBatch][4], y[kAppendBatch][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                // interleaved: pair i is (x[2 i], x[2 i + 1]), the later two in y
-                const float u0 = a.interleaved ? (i < 2 ? x[2 * (i & 1)] : y[2 * (i & 1)]) : x[i];
-                const float u1 = a.interleaved ? (i < 2 ? x[2 * (i & 1) + 1] : y[2 * (i & 1) + 1]) : y[i];
-                const float c = cs[i0 + i], s = sn[i0 + i];
-                o1[i] = u0 * c - u1 * s;
-                o2[i] = u0 * s + u1 * c;
+        for (int j = 0; j < kAppendBatch; ++j) {
+            const int u = min(u0 + j * step, units - 1);
+            const int head = (int)((unsigned)u / (unsigned)per_head), k = u - head * per_head;
+            const uint16_t* src = row + (long long)head * dim;
+            const int dx = k >= rot ? 2 * a.pairs + 8 * (k - rot) : a.interleaved ? 8 * k : 4 * k;
+            const int dy = k >= rot || a.interleaved ? dx + 4 : dx + a.pairs;
+            get4(src + dx, x[j]);
+            get4(src + dy, y[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < kAppendBatch; ++j) {
+            const int u = u0 + j * step;
+            if (u >= units) break;
+            const int head = (int)((unsigned)u / (unsigned)per_head), k = u - head * per_head;
+            const int dx = k >= rot ? 2 * a.pairs + 8 * (k - rot) : a.interleaved ? 8 * k : 4 * k;
+            const int dy = k >= rot || a.interleaved ? dx + 4 : dx + a.pairs;
+            const bool is_q = head < a.q_heads;
+            if (!is_q && !stored) continue;
+            const bool fp8 = !is_q && a.c.fp8;
+            uint8_t* dst = is_q ? (uint8_t*)(a.q_out + (long long)r * a.q_ld + (long long)head * dim)
+                                : page + ((((long long)(head - a.q_heads) << a.c.log_page) + off) * dim) * es;
+            const int de = fp8 ? 1 : 2;
+            if (k < rot) {
+                float u0v[4], u1v[4];
+                // interleaved: the eight values are four pairs in a row
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    u0v[i] = a.interleaved ? (i < 2 ? x[j][2 * (i & 1)] : y[j][2 * (i & 1)]) : x[j][i];
+                    u1v[i] = a.interleaved ? (i < 2 ? x[j][2 * (i & 1) + 1] : y[j][2 * (i & 1) + 1]) : y[j][i];
+                }
+                float o1[4], o2[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float c = cs[4 * k + i], s = sn[4 * k + i];
+                    o1[i] = u0v[i] * c - u1v[i] * s;
+                    o2[i] = u0v[i] * s + u1v[i] * c;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[j][i] = a.interleaved ? (i & 1 ? o2[i >> 1] : o1[i >> 1]) : o1[i];
+                    y[j][i] = a.interleaved ? (i & 1 ? o2[2 + (i >> 1)] : o1[2 + (i >> 1)]) : o2[i];
+                }
             }
-            if (a.interleaved) {
-                const float w1[4] = {o1[0], o2[0], o1[1], o2[1]}, w2[4] = {o1[2], o2[2], o1[3], o2[3]};
-                put4(dst + dx * de, fp8, scale, w1);
-                put4(dst + dy * de, fp8, scale, w2);
-            } else {
-                put4(dst + dx * de, fp8, scale, o1);
-                put4(dst + dy * de, fp8, scale, o2);
-            }
-        } else {
-            const int d = 2 * a.pairs + 8 * (k - rot);
-            get4(src + d, x);
-            get4(src + d + 4, y);
-            put4(dst + d * de, fp8, scale, x);
-            put4(dst + (d + 4) * de, fp8, scale, y);
+            put4(dst + dx * de, fp8, a.c.k_scale, x[j]);
+            put4(dst + dy * de, fp8, a.c.k_scale, y[j]);
         }
     }
 }
@@ -244,8 +255,16 @@ __global__ __launch_bounds__(kAppendThreads) void append_kernel(AppendArgs a) {
 //
 // Token ctx + path[j] of a lane moves to ctx + j, j < accepted.  A block takes
 // one lane, layer, kv head and side (K or V), reads every source into LDS, and
-// writes after a barrier, so a path in any order is right.  Latency-bound: a few
-// KiB per block, all of a lane's layers and heads at once.
+// writes after a barrier, so a path in any order is right.
+//
+// Tokens are numbered in slots from the start of the 16-token block that ctx lies
+// in; the 64 drafted ones take at most five blocks, each of which lies in one page.
+// K moves whole rows.  V blocks are dim-major: the blocks with a source or a
+// destination are read whole (runs of 16 x dim values) and the destinations'
+// vectors put together in LDS, so memory sees only 16-byte accesses.
+//
+// Bound by latency for few lanes (lengths, then table, then data) and by bytes
+// for many.
 
 struct CompactArgs {
     CacheView c;
@@ -259,68 +278,91 @@ struct CompactArgs {
 };
 
 constexpr int kCompactThreads = 128;
+constexpr int kCompactBlocks = NVFP4_TREE_MAX_ROWS / 16 + 1;
 
 template <typename T>
 __global__ __launch_bounds__(kCompactThreads) void compact_kernel(CompactArgs a) {
-    // one block's tokens: 64 of at most 256 dims
     extern __shared__ __align__(16) uint8_t lds[];
-    __shared__ long long from[64], to[64];  // byte offsets of the page; -1: not moved
-    __shared__ int at_from[64], at_to[64];  // token in the page
-    const int b = blockIdx.x / a.c.kv_heads, h = blockIdx.x - b * a.c.kv_heads;
-    const int layer = blockIdx.y;
+    __shared__ long long block_at[kCompactBlocks];       // byte offset of the slots' 16 tokens; -1: no page
+    __shared__ uint8_t source[16 * kCompactBlocks];      // slot that a slot's content comes from
+    __shared__ int ends[2];                              // blocks with a source or destination; rows to read
+    const int b = (int)(blockIdx.x / (unsigned)a.c.kv_heads), h = blockIdx.x - b * a.c.kv_heads;
     const bool is_v = blockIdx.z != 0;
-    const int count = min(max(a.accepted[b], 0), min(a.path_ld, NVFP4_TREE_MAX_ROWS));
     const int dim = a.c.dim, page_mask = (1 << a.c.log_page) - 1;
-    if (threadIdx.x < 64) {
+    const int count = min(max(a.accepted[b], 0), min(a.path_ld, NVFP4_TREE_MAX_ROWS));
+    if (count == 0) return;
+    const int ctx = a.ctx_len[b], first = ctx & 15;
+    if (ctx < 0) return;
+    const int token_bytes = dim * (int)sizeof(T);  // of K; V's 16 tokens take as much as 16 of K
+    if (threadIdx.x < 64) {  // the first wave works the moves out
         const int j = threadIdx.x;
-        long long f = -1, w = -1;
-        if (j < count) {
-            const int s = a.path[(long long)b * a.path_ld + j];
-            const long long ps = (long long)a.ctx_len[b] + s, pd = (long long)a.ctx_len[b] + j;
-            if (s >= 0 && s < NVFP4_TREE_MAX_ROWS && s != j && pd >= 0 &&
-                (max(ps, pd) >> a.c.log_page) < a.table_ld) {
-                const int* tab = a.table + (long long)b * a.table_ld;
-                const int is = tab[ps >> a.c.log_page], id = tab[pd >> a.c.log_page];
-                if ((unsigned)is < (unsigned)a.c.pages && (unsigned)id < (unsigned)a.c.pages) {
-                    f = (long long)is * a.c.page_stride;
-                    w = (long long)id * a.c.page_stride;
-                    at_from[j] = (int)ps & page_mask;
-                    at_to[j] = (int)pd & page_mask;
-                }
+        const int s = j < count ? a.path[(long long)b * a.path_ld + j] : -1;
+        long long at = -1;
+        if (j < kCompactBlocks) {
+            const long long p = (long long)(ctx >> 4) * 16 + 16 * j;
+            if ((p >> a.c.log_page) < a.table_ld) {
+                const int id = a.table[(long long)b * a.table_ld + (p >> a.c.log_page)];
+                if ((unsigned)id < (unsigned)a.c.pages)
+                    at = (long long)id * a.c.page_stride + (long long)((int)p & page_mask) * token_bytes;
             }
+            block_at[j] = at;
         }
-        from[j] = f;
-        to[j] = w;
+        const int from = first + s, to = first + j;
+        // (every lane takes part in the exchange)
+        const int has = at >= 0 ? 1 : 0, has_from = __shfl(has, (from & 127) >> 4), has_to = __shfl(has, (to & 127) >> 4);
+        const bool moves = j < count && s >= 0 && s < NVFP4_TREE_MAX_ROWS && s != j && has_from && has_to;
+        for (int i = j; i < 16 * kCompactBlocks; i += 64) source[i] = (uint8_t)i;
+        __builtin_amdgcn_wave_barrier();
+        if (moves) source[to] = (uint8_t)from;
+        int last = moves ? max(from, to) : -1;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) last = max(last, __shfl_xor(last, d));
+        if (j == 0) ends[0] = (last + 16) >> 4;  // 0: nothing moves
     }
     __syncthreads();
-    if (count == 0) return;
-    const long long head = ((long long)h * dim << a.c.log_page) * sizeof(T);
-    uint8_t* base = (is_v ? a.c.v : a.c.k) + layer * a.c.layer_stride + head;
+    const int blocks = ends[0];
+    if (blocks == 0) return;
+    const long long head = ((long long)h * token_bytes) << a.c.log_page;
+    uint8_t* base = (is_v ? a.c.v : a.c.k) + (long long)blockIdx.y * a.c.layer_stride + head;
+    uint4* buf = (uint4*)lds;
+    const int log_vecs = 31 - __clz(token_bytes / 16), vecs = 1 << log_vecs;  // 16-byte vectors of a token
     if (!is_v) {
-        // 16-byte vectors of a token's row
-        const int vecs = dim * (int)sizeof(T) / 16;
-        uint4* buf = (uint4*)lds;
-        for (int e = threadIdx.x; e < count * vecs; e += kCompactThreads) {
-            const int j = e / vecs, k = e - j * vecs;
-            if (from[j] >= 0) buf[e] = *(const uint4*)(base + from[j] + ((long long)at_from[j] * vecs + k) * 16);
+        for (int e = threadIdx.x; e < count << log_vecs; e += kCompactThreads) {
+            const int to = first + (e >> log_vecs), k = e & (vecs - 1), from = source[to];
+            if (from != to) buf[e] = *(const uint4*)(base + block_at[from >> 4] + (from & 15) * token_bytes + 16 * k);
         }
         __syncthreads();
-        for (int e = threadIdx.x; e < count * vecs; e += kCompactThreads) {
-            const int j = e / vecs, k = e - j * vecs;
-            if (from[j] >= 0) *(uint4*)(base + to[j] + ((long long)at_to[j] * vecs + k) * 16) = buf[e];
+        for (int e = threadIdx.x; e < count << log_vecs; e += kCompactThreads) {
+            const int to = first + (e >> log_vecs), k = e & (vecs - 1);
+            if (source[to] != to) *(uint4*)(base + block_at[to >> 4] + (to & 15) * token_bytes + 16 * k) = buf[e];
         }
-    } else {
-        // single values: consecutive threads take consecutive tokens of a dim
-        T* buf = (T*)lds;
-        for (int e = threadIdx.x; e < count * dim; e += kCompactThreads) {
-            const int d = e / count, j = e - d * count;
-            if (from[j] >= 0) buf[e] = *(const T*)(base + from[j] + v_element(a.c, d, at_from[j]) * sizeof(T));
+        return;
+    }
+    const int log_block = log_vecs + 4;  // vectors of a V block
+    for (int e = threadIdx.x; e < blocks << log_block; e += kCompactThreads) {
+        const long long at = block_at[e >> log_block];
+        if (at >= 0) buf[e] = *(const uint4*)(base + at + 16 * (e & ((1 << log_block) - 1)));
+    }
+    __syncthreads();
+    // A vector is 16 / sizeof(T) tokens of one dim.
+    constexpr int kPer = 16 / (int)sizeof(T);
+    const T* in = (const T*)lds;
+    const int out_blocks = (first + count + 15) >> 4;
+    for (int e = threadIdx.x; e < out_blocks << log_block; e += kCompactThreads) {
+        const int blk = e >> log_block, v = e & ((1 << log_block) - 1);
+        const int d = v / (16 / kPer), slot0 = 16 * blk + v % (16 / kPer) * kPer;
+        union {
+            uint4 vec;
+            T x[kPer];
+        } o;
+        bool changed = false;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int from = source[slot0 + i];
+            changed |= from != slot0 + i;
+            o.x[i] = in[((from >> 4) * dim + d) * 16 + (from & 15)];
         }
-        __syncthreads();
-        for (int e = threadIdx.x; e < count * dim; e += kCompactThreads) {
-            const int d = e / count, j = e - d * count;
-            if (from[j] >= 0) *(T*)(base + to[j] + v_element(a.c, d, at_to[j]) * sizeof(T)) = buf[e];
-        }
+        if (changed) *(uint4*)(base + block_at[blk] + 16 * v) = o.vec;
     }
 }
 
@@ -502,6 +544,105 @@ __global__ __launch_bounds__(kAssignThreads) void update_assign_kernel(UpdateArg
     }
 }
 
+// Phases 1 to 3 in one workgroup, counts in LDS, where the pool and the lanes fit
+// it: one launch instead of three.  Lanes' partly filled last pages are compared
+// with each other directly.
+constexpr int kFusedPages = 32768, kFusedLanes = kAssignThreads, kFusedEntries = 65536;
+__global__ __launch_bounds__(kAssignThreads) void update_fused_kernel(UpdateArgs a, int* slots) {
+    extern __shared__ int refs[];  // [pages]
+    __shared__ int lasts[kFusedLanes];
+    __shared__ int lds[kAssignThreads / 64];
+    constexpr int kBatch = 8;
+    const int tid = threadIdx.x, i = tid;
+    const bool lane = i < a.lanes_out;
+    NewLane n = {-1, 0, 0, 0};
+    if (lane) n = new_lane(a, i);
+    for (int p0 = 0; p0 < a.c.pages; p0 += kBatch * kAssignThreads) {
+        int v[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) v[j] = a.refs_in[min(p0 + j * kAssignThreads + tid, a.c.pages - 1)];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+            if (p0 + j * kAssignThreads + tid < a.c.pages) refs[p0 + j * kAssignThreads + tid] = v[j];
+    }
+    __syncthreads();
+    const int old = a.lanes_in * a.table_ld;
+    for (int e0 = 0; e0 < old; e0 += kBatch * kAssignThreads) {
+        int v[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) v[j] = a.table_in[min(e0 + j * kAssignThreads + tid, old - 1)];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+            if (e0 + j * kAssignThreads + tid < old && is_page(a, v[j])) atomicSub(&refs[v[j]], 1);
+    }
+    // New rows, a wave each in turn.
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
+    for (int r = wave; r < a.lanes_out; r += kAssignThreads / 64) {
+        const NewLane m = new_lane(a, r);
+        const int* row = a.table_in + (long long)max(m.parent, 0) * a.table_ld;
+        int* out = a.table_out + (long long)r * a.table_ld;
+        int last = -1;
+        for (int j0 = 0; j0 < a.table_ld; j0 += kBatch * 64) {
+            int v[kBatch];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) v[j] = row[min(j0 + 64 * j + l, a.table_ld - 1)];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                const int e = j0 + 64 * j + l;
+                if (e >= a.table_ld) continue;
+                const int id = e < m.held && is_page(a, v[j]) ? v[j] : -1;
+                out[e] = id;
+                if (id >= 0) atomicAdd(&refs[id], 1);
+                if (e == m.held - 1 && (m.len & ((1 << a.c.log_page) - 1))) last = id;
+            }
+        }
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) last = max(last, __shfl_xor(last, d));
+        if (l == 0) {
+            lasts[r] = last;
+            a.len_out[r] = m.len;
+        }
+    }
+    __syncthreads();
+    int last = -1, same = 0, lowest = i;
+    if (lane) last = lasts[i];
+    for (int j = 0; j < a.lanes_out; ++j) {
+        const bool hit = lasts[j] == last;
+        same += hit ? 1 : 0;
+        lowest = hit ? min(lowest, j) : lowest;
+    }
+    const bool copy = last >= 0 && !(same == refs[max(last, 0)] && lowest == i);
+    const int need = lane ? (copy ? 1 : 0) + max(n.upto - n.held, 0) : 0;
+    int requests;
+    const int first = block_scan(need, lds, &requests);
+    const int entry0 = n.held - (copy ? 1 : 0);
+    for (int j = 0; j < need; ++j) {
+        slots[2 * (size_t)(first + j)] = i;
+        slots[2 * (size_t)(first + j) + 1] = entry0 + j;
+    }
+    __syncthreads();
+    int given = 0;
+    for (int p0 = 0; p0 < a.c.pages && given < requests; p0 += kAssignThreads) {
+        const int p = p0 + tid;
+        const int free = p < a.c.pages && refs[p] == 0 ? 1 : 0;
+        int all;
+        const int r = given + block_scan(free, lds, &all);
+        if (free && r < requests) {
+            a.table_out[(long long)slots[2 * (size_t)r] * a.table_ld + slots[2 * (size_t)r + 1]] = p;
+            refs[p] = 1;
+        }
+        given += all;
+    }
+    if (tid == 0) *a.short_out = max(requests - given, 0);
+    for (int r = min(given, requests) + tid; r < requests; r += kAssignThreads)
+        a.table_out[(long long)slots[2 * (size_t)r] * a.table_ld + slots[2 * (size_t)r + 1]] = -1;
+    __syncthreads();
+    if (copy) atomicSub(&refs[last], 1);
+    if (lane) a.copies[i] = make_int2(copy ? last : -1, copy ? a.table_out[(long long)i * a.table_ld + n.held - 1] : -1);
+    __syncthreads();
+    for (int p = tid; p < a.c.pages; p += kAssignThreads) a.refs_out[p] = refs[p];
+}
+
 // Copies K and V of the pages that became a lane's own: block (lane, layer, part).
 __global__ __launch_bounds__(256) void update_copy_kernel(UpdateArgs a, long long page_bytes) {
     const int2 c = a.copies[blockIdx.x];
@@ -605,8 +746,7 @@ int nvfp4_cache_compact(const nvfp4_cache* cache, int lanes, const int* ctx_len_
     a.path_ld = path_ld;
     a.accepted = accepted_dev;
     const dim3 grid((unsigned)lanes * a.c.kv_heads, (unsigned)a.c.layers, 2);
-    const int tokens = path_ld < NVFP4_TREE_MAX_ROWS ? path_ld : NVFP4_TREE_MAX_ROWS;
-    const size_t bytes = (size_t)tokens * a.c.dim * (a.c.fp8 ? 1 : 2);
+    const size_t bytes = (size_t)kCompactBlocks * 16 * a.c.dim * (a.c.fp8 ? 1 : 2);
     if (a.c.fp8)
         hipLaunchKernelGGL((compact_kernel<uint8_t>), grid, dim3(kCompactThreads), bytes, (hipStream_t)stream, a);
     else
@@ -668,12 +808,18 @@ int nvfp4_cache_update(const nvfp4_cache* cache, int lanes_in, const int* table_
     ws += round16((size_t)lanes_out * sizeof(int2));
     int* slots = (int*)ws;
     hipStream_t s = (hipStream_t)stream;
-    hipLaunchKernelGGL(update_init_kernel, dim3((unsigned)(a.c.pages + 255) / 256), dim3(256), 0, s, a);
-    NVFP4_HIP(hipGetLastError());
-    hipLaunchKernelGGL(update_count_kernel, dim3((unsigned)(lanes_in + lanes_out)), dim3(256), 0, s, a);
-    NVFP4_HIP(hipGetLastError());
-    hipLaunchKernelGGL(update_assign_kernel, dim3(1), dim3(kAssignThreads), 0, s, a, slots);
-    NVFP4_HIP(hipGetLastError());
+    if (a.c.pages <= kFusedPages && lanes_out <= kFusedLanes &&
+        ((long long)lanes_in + lanes_out) * table_ld <= kFusedEntries) {
+        hipLaunchKernelGGL(update_fused_kernel, dim3(1), dim3(kAssignThreads), (size_t)a.c.pages * sizeof(int), s, a, slots);
+        NVFP4_HIP(hipGetLastError());
+    } else {
+        hipLaunchKernelGGL(update_init_kernel, dim3((unsigned)(a.c.pages + 255) / 256), dim3(256), 0, s, a);
+        NVFP4_HIP(hipGetLastError());
+        hipLaunchKernelGGL(update_count_kernel, dim3((unsigned)(lanes_in + lanes_out)), dim3(256), 0, s, a);
+        NVFP4_HIP(hipGetLastError());
+        hipLaunchKernelGGL(update_assign_kernel, dim3(1), dim3(kAssignThreads), 0, s, a, slots);
+        NVFP4_HIP(hipGetLastError());
+    }
     const long long page_bytes = ((long long)a.c.kv_heads * a.c.dim << a.c.log_page) * (a.c.fp8 ? 1 : 2);
     hipLaunchKernelGGL(update_copy_kernel, dim3((unsigned)lanes_out, (unsigned)a.c.layers, 8), dim3(256), 0, s, a, page_bytes);
     NVFP4_HIP(hipGetLastError());
