@@ -82,8 +82,8 @@ int check_lanes(const CacheView& c, int lanes, const int* table, int table_ld) {
 // Bound by the bytes of the rows (read once, q and the cache written once) and,
 // for a few rows, by latency: blocks of 256 threads take one row and a share of
 // its heads, the cosines of the row once per block in LDS.  K rows are written
-// 4 or 8 bytes at a time.  V blocks are dim-major: the first row of each aligned
-// group of 8 tokens writes the group's 8 tokens of a dim in one store.
+// 4 or 8 bytes at a time.  V blocks are dim-major: a block
+// takes an aligned group of 8 tokens and stores a dim's 8 tokens at once.
 
 struct AppendArgs {
     CacheView c;
@@ -103,6 +103,7 @@ struct AppendArgs {
     uint16_t* q_out;
     long long q_ld;
     int shares;  // blocks per row for the rotated heads
+    int wide;    // rows of qkv and q are 16-byte aligned
 };
 
 constexpr int kAppendThreads = 256;
@@ -114,52 +115,78 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 }
 
 // Four values to four consecutive dims of a K row (or q row).
-__device__ __forceinline__ void put4(uint8_t* dst, bool fp8, float scale, const float (&x)[4]) {
+__device__ __forceinline__ void put4(uint8_t* dst, bool fp8, float scale, const float* x) {
     if (fp8)
         *(uint32_t*)dst = e4m3x2(x[0] / scale, x[1] / scale) | (e4m3x2(x[2] / scale, x[3] / scale) << 16);
     else
         *(uint2*)dst = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
 }
 
-__device__ __forceinline__ void get4(const uint16_t* src, float (&x)[4]) {
-    const uint2 v = *(const uint2*)src;
+__device__ __forceinline__ void unpack4(const uint2& v, float* x) {
     x[0] = __uint_as_float(v.x << 16);
     x[1] = __uint_as_float(v.x & 0xFFFF0000u);
     x[2] = __uint_as_float(v.y << 16);
     x[3] = __uint_as_float(v.y & 0xFFFF0000u);
 }
 
-__global__ __launch_bounds__(kAppendThreads) void append_kernel(AppendArgs a) {
-    const int r = blockIdx.x, share = blockIdx.y;
-    const int b = __builtin_amdgcn_readfirstlane(lane_of_row(a.row_start, a.lanes, r));
-    if (b >= a.lanes) return;  // a row past the last lane's
-    const int row0 = a.row_start[b], t = r - row0;
-    if (t < 0) return;
-    const long long p = (long long)a.ctx_len[b] + t;  // this row's place in the lane
-    const int page_tokens = 1 << a.c.log_page;
-    const int* tab = a.table + (long long)b * a.table_ld;
-    const int dim = a.c.dim, es = a.c.fp8 ? 1 : 2;
-    const bool placed = p >= 0 && (p >> a.c.log_page) < a.table_ld;
-    const int id = placed ? tab[p >> a.c.log_page] : -1;
-    const bool stored = (unsigned)id < (unsigned)a.c.pages;
-
-    if (share == a.shares) {  // V
-        const int slot = (int)p & 7;
-        if (!stored || (t > 0 && slot != 0)) return;  // the group's first row writes it
-        const int left = a.row_start[b + 1] - r;
-        const int count = min(8 - slot, left);
-        const uint16_t* src = a.qkv + (long long)r * a.ld + (long long)(a.q_heads + a.c.kv_heads) * dim;
-        uint8_t* page = a.c.v + (long long)id * a.c.page_stride;
-        const int off = (int)p & (page_tokens - 1);
-        for (int e = threadIdx.x; e < a.c.kv_heads * dim; e += kAppendThreads) {
-            float x[8];
+// V of one aligned group of 8 tokens of a lane: group number `g` over all lanes'
+// groups.  A thread takes two dims, and stores a dim's tokens of the group in one go.
+__device__ __forceinline__ void append_v(const AppendArgs& a, int g) {
+    const int lane = threadIdx.x & 63;
+    int b = -1, before = 0, row0 = 0, rows = 0, ctx = 0;
+    for (int b0 = 0; b0 < a.lanes && b < 0; b0 += 64) {
+        int r0 = 0, n = 0, c = 0;
+        if (b0 + lane < a.lanes) {
+            r0 = a.row_start[b0 + lane];
+            n = min(max(a.row_start[b0 + lane + 1] - r0, 0), a.rows - min(r0, a.rows));
+            c = a.ctx_len[b0 + lane];
+            if (r0 < 0 || c < 0) n = 0;
+        }
+        const int mine = n > 0 ? (int)((((long long)c + n - 1) >> 3) - (c >> 3)) + 1 : 0;
+        int upto = mine;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = bf16_f32(src[(long long)min(i, count - 1) * a.ld + e]);
-            uint8_t* dst = page + v_element(a.c, e, off) * es;
+        for (int d = 1; d < 64; d <<= 1) {
+            const int u = __shfl_up(upto, d);
+            upto += lane >= d ? u : 0;
+        }
+        const unsigned long long past = __ballot(before + upto > g);
+        if (past) {
+            const int first = __ffsll(past) - 1;
+            b = b0 + first;
+            before += __builtin_amdgcn_readlane(upto, first) - __builtin_amdgcn_readlane(mine, first);
+            row0 = __builtin_amdgcn_readlane(r0, first);
+            rows = __builtin_amdgcn_readlane(n, first);
+            ctx = __builtin_amdgcn_readlane(c, first);
+        } else {
+            before += __builtin_amdgcn_readlane(upto, 63);
+        }
+    }
+    if (b < 0) return;
+    // tokens [p, p + count) of the lane, rows from r on
+    const long long p = max(((long long)(ctx >> 3) + (g - before)) * 8, (long long)ctx);
+    const int r = row0 + (int)(p - ctx), count = (int)min((p & ~7ll) + 8, (long long)ctx + rows) - (int)p;
+    if ((p >> a.c.log_page) >= a.table_ld) return;
+    const int id = a.table[(long long)b * a.table_ld + (p >> a.c.log_page)];
+    if ((unsigned)id >= (unsigned)a.c.pages) return;
+    const int dim = a.c.dim, es = a.c.fp8 ? 1 : 2;
+    const uint16_t* src = a.qkv + (long long)r * a.ld + (long long)(a.q_heads + a.c.kv_heads) * dim;
+    uint8_t* page = a.c.v + (long long)id * a.c.page_stride;
+    const int off = (int)p & ((1 << a.c.log_page) - 1);
+    for (int e = 2 * threadIdx.x; e < a.c.kv_heads * dim; e += 2 * kAppendThreads) {
+        uint32_t in[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) in[i] = *(const uint32_t*)(src + (long long)min(i, count - 1) * a.ld + e);
+        uint8_t* dst = page + v_element(a.c, e, off) * es;
+#pragma unroll
+        for (int half = 0; half < 2; ++half, dst += 16 * es) {  // the next dim is 16 tokens on
+            uint32_t h[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) h[i] = half ? in[i] >> 16 : in[i] & 0xFFFFu;
             if (a.c.fp8) {
                 uint32_t w[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = e4m3x2(x[2 * i] / a.c.v_scale, x[2 * i + 1] / a.c.v_scale);
+                for (int i = 0; i < 4; ++i)
+                    w[i] = e4m3x2(bf16_f32((uint16_t)h[2 * i]) / a.c.v_scale, bf16_f32((uint16_t)h[2 * i + 1]) / a.c.v_scale);
                 if (count == 8)
                     *(uint2*)dst = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
                 else
@@ -167,16 +194,62 @@ __global__ __launch_bounds__(kAppendThreads) void append_kernel(AppendArgs a) {
                     for (int i = 0; i < 8; ++i)
                         if (i < count) dst[i] = (uint8_t)(w[i >> 1] >> (8 * (i & 1)));
             } else if (count == 8) {
-                *(uint4*)dst = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
-                                          pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+                *(uint4*)dst = make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16));
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    if (i < count) ((uint16_t*)dst)[i] = f32_to_bf16_rne(x[i]);
+                    if (i < count) ((uint16_t*)dst)[i] = (uint16_t)h[i];
             }
         }
+    }
+}
+
+__global__ __launch_bounds__(kAppendThreads) void append_kernel(AppendArgs a) {
+    if ((int)blockIdx.x >= a.rows * a.shares) {
+        append_v(a, blockIdx.x - a.rows * a.shares);
         return;
     }
+    const int r = (int)(blockIdx.x / (unsigned)a.shares), share = blockIdx.x - r * a.shares;
+    // A head is dim / 8 units of eight values: pairs / 4 of four pairs, then
+    // copied vectors.  A thread keeps one unit, its cosines in registers, and
+    // goes through the heads.
+    const int dim = a.c.dim, log_units = dim == 64 ? 3 : dim == 128 ? 4 : 5;
+    const int rot = a.pairs >> 2, unit = threadIdx.x & ((1 << log_units) - 1);
+    const bool turns = unit < rot;
+    const int dx = !turns ? 2 * a.pairs + 8 * (unit - rot) : a.interleaved ? 8 * unit : 4 * unit;
+    const int dy = !turns || a.interleaved ? dx + 4 : dx + a.pairs;
+    const int heads = a.q_heads + a.c.kv_heads, pass = kAppendThreads >> log_units;
+    const int head0 = share * pass + (threadIdx.x >> log_units), step = a.shares * pass;
+    const uint16_t* row = a.qkv + (long long)r * a.ld;
+    const bool wide = a.wide && dy == dx + 4;  // eight values in a row, 16-byte aligned
+    uint2 in[kAppendBatch][2];
+    auto read = [&](int h0) {
+#pragma unroll
+        for (int j = 0; j < kAppendBatch; ++j) {
+            const uint16_t* src = row + (long long)min(h0 + j * step, heads - 1) * dim;
+            if (wide) {
+                const uint4 v = *(const uint4*)(src + dx);
+                in[j][0] = make_uint2(v.x, v.y);
+                in[j][1] = make_uint2(v.z, v.w);
+            } else {
+                in[j][0] = *(const uint2*)(src + dx);
+                in[j][1] = *(const uint2*)(src + dy);
+            }
+        }
+    };
+    // The row is on its way while its lane, page and cosines are worked out.
+    read(head0);
+    const int b = __builtin_amdgcn_readfirstlane(lane_of_row(a.row_start, a.lanes, r));
+    if (b >= a.lanes) return;  // a row past the last lane's
+    const int row0 = a.row_start[b], t = r - row0;
+    if (t < 0) return;
+    const long long p = (long long)a.ctx_len[b] + t;  // this row's place in the lane
+    const int page_tokens = 1 << a.c.log_page;
+    const int* tab = a.table + (long long)b * a.table_ld;
+    const int es = a.c.fp8 ? 1 : 2;
+    const bool placed = p >= 0 && (p >> a.c.log_page) < a.table_ld;
+    const int id = placed ? tab[p >> a.c.log_page] : -1;
+    const bool stored = (unsigned)id < (unsigned)a.c.pages;
 
     __shared__ float cs[128], sn[128];
     for (int i = threadIdx.x; i < a.pairs; i += kAppendThreads) {
@@ -189,64 +262,50 @@ __global__ __launch_bounds__(kAppendThreads) void append_kernel(AppendArgs a) {
     }
     __syncthreads();
 
-    // Units of a head: pairs / 4 of four pairs, then (dim - 2 pairs) / 8 copied
-    // vectors of 8.
-    const int rot = a.pairs >> 2, per_head = rot + ((dim - 2 * a.pairs) >> 3);
-    const int heads = a.q_heads + a.c.kv_heads;
-    const int units = heads * per_head;
-    const uint16_t* row = a.qkv + (long long)r * a.ld;
+    float c[4], s[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        c[i] = turns ? cs[4 * unit + i] : 1.f;
+        s[i] = turns ? sn[4 * unit + i] : 0.f;
+    }
+    const bool flat = a.interleaved && turns;  // pairs lie next to each other
     uint8_t* page = a.c.k + (long long)(stored ? id : 0) * a.c.page_stride;
     const int off = (int)p & (page_tokens - 1);
-    // kAppendBatch units of a thread are read before the first is written.
-    const int step = a.shares * kAppendThreads;
-    for (int u0 = share * kAppendThreads + threadIdx.x; u0 < units; u0 += kAppendBatch * step) {
-        float x[kAppendBatch][4], y[kAppendBatch][4];
+    for (int h0 = head0; h0 < heads; h0 += kAppendBatch * step) {
+        if (h0 != head0) read(h0);
 #pragma unroll
         for (int j = 0; j < kAppendBatch; ++j) {
-            const int u = min(u0 + j * step, units - 1);
-            const int head = (int)((unsigned)u / (unsigned)per_head), k = u - head * per_head;
-            const uint16_t* src = row + (long long)head * dim;
-            const int dx = k >= rot ? 2 * a.pairs + 8 * (k - rot) : a.interleaved ? 8 * k : 4 * k;
-            const int dy = k >= rot || a.interleaved ? dx + 4 : dx + a.pairs;
-            get4(src + dx, x[j]);
-            get4(src + dy, y[j]);
-        }
-#pragma unroll
-        for (int j = 0; j < kAppendBatch; ++j) {
-            const int u = u0 + j * step;
-            if (u >= units) break;
-            const int head = (int)((unsigned)u / (unsigned)per_head), k = u - head * per_head;
-            const int dx = k >= rot ? 2 * a.pairs + 8 * (k - rot) : a.interleaved ? 8 * k : 4 * k;
-            const int dy = k >= rot || a.interleaved ? dx + 4 : dx + a.pairs;
+            const int head = h0 + j * step;
+            if (head >= heads) break;
             const bool is_q = head < a.q_heads;
             if (!is_q && !stored) continue;
             const bool fp8 = !is_q && a.c.fp8;
             uint8_t* dst = is_q ? (uint8_t*)(a.q_out + (long long)r * a.q_ld + (long long)head * dim)
                                 : page + ((((long long)(head - a.q_heads) << a.c.log_page) + off) * dim) * es;
             const int de = fp8 ? 1 : 2;
-            if (k < rot) {
-                float u0v[4], u1v[4];
-                // interleaved: the eight values are four pairs in a row
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    u0v[i] = a.interleaved ? (i < 2 ? x[j][2 * (i & 1)] : y[j][2 * (i & 1)]) : x[j][i];
-                    u1v[i] = a.interleaved ? (i < 2 ? x[j][2 * (i & 1) + 1] : y[j][2 * (i & 1) + 1]) : y[j][i];
-                }
+            float v[8];
+            unpack4(in[j][0], v);
+            unpack4(in[j][1], v + 4);
+            if (turns) {
                 float o1[4], o2[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float c = cs[4 * k + i], s = sn[4 * k + i];
-                    o1[i] = u0v[i] * c - u1v[i] * s;
-                    o2[i] = u0v[i] * s + u1v[i] * c;
+                    const float x = flat ? v[2 * i] : v[i], y = flat ? v[2 * i + 1] : v[4 + i];
+                    o1[i] = x * c[i] - y * s[i];
+                    o2[i] = x * s[i] + y * c[i];
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    x[j][i] = a.interleaved ? (i & 1 ? o2[i >> 1] : o1[i >> 1]) : o1[i];
-                    y[j][i] = a.interleaved ? (i & 1 ? o2[2 + (i >> 1)] : o1[2 + (i >> 1)]) : o2[i];
+                    v[i] = flat ? (i & 1 ? o2[i >> 1] : o1[i >> 1]) : o1[i];
+                    v[4 + i] = flat ? (i & 1 ? o2[2 + (i >> 1)] : o1[2 + (i >> 1)]) : o2[i];
                 }
             }
-            put4(dst + dx * de, fp8, a.c.k_scale, x[j]);
-            put4(dst + dy * de, fp8, a.c.k_scale, y[j]);
+            if (wide && !fp8) {
+                *(uint4*)(dst + dx * 2) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+            } else {
+                put4(dst + dx * de, fp8, a.c.k_scale, v);
+                put4(dst + dy * de, fp8, a.c.k_scale, v + 4);
+            }
         }
     }
 }
@@ -713,14 +772,15 @@ int nvfp4_cache_append(const nvfp4_cache* cache, int layer, const uint16_t* qkv_
     a.factor = rotary->factor;
     a.q_out = q_out_dev;
     a.q_ld = q_ld;
-    const int per_head = rotary->pairs / 4 + (dim - 2 * rotary->pairs) / 8;
-    const int units = (q_heads + a.c.kv_heads) * per_head;
-    // One unit per thread while the rows alone do not fill the card.
-    const int most = (units + kAppendThreads - 1) / kAppendThreads;
+    // One head per thread while the rows alone do not fill the card.
+    const int pass = kAppendThreads / (dim / 8);
+    const int most = (q_heads + a.c.kv_heads + pass - 1) / pass;
     int shares = (8 * device_cus() + rows - 1) / rows;
     a.shares = shares < 1 ? 1 : shares > most ? most : shares;
-    hipLaunchKernelGGL(append_kernel, dim3((unsigned)rows, (unsigned)a.shares + 1), dim3(kAppendThreads),
-                       0, (hipStream_t)stream, a);
+    a.wide = (((uintptr_t)qkv_dev | (uintptr_t)q_out_dev) & 15) == 0 && qkv_ld % 8 == 0 && q_ld % 8 == 0;
+    // V: a lane's rows cover at most rows / 8 + 2 groups of 8 tokens.
+    const long long blocks = (long long)rows * a.shares + rows / 8 + 2ll * (lanes < rows ? lanes : rows);
+    hipLaunchKernelGGL(append_kernel, dim3((unsigned)blocks), dim3(kAppendThreads), 0, (hipStream_t)stream, a);
     NVFP4_HIP(hipGetLastError());
     return NVFP4_OK;
 }
