@@ -43,9 +43,12 @@ constexpr float kLn2 = 0.69314718055994530942f;
 // O and the sums are rescaled only when a row's maximum passes the one in use
 // by 2^8: weights stay below 2^8, far from fp32's and bf16's limits.
 constexpr float kRescaleAt = 8.f;
-// Fewest tiles a worker takes: below, joining partial results costs more than
-// the shorter walk saves.
-constexpr int kMinTiles = 4;
+// Fewest tiles a worker takes where there are more workers than items: below,
+// storing and joining partial results costs more than the shorter walk saves
+// (8 lanes of 4096 tokens and 12 rows: 21.3 us with 2 or 4 tiles, 19.5 with 8).
+constexpr int kMinTiles = 8;
+// Items of at most so many tiles are never shared, and no joining kernel runs.
+constexpr int kWholeTiles = 8;
 
 struct AttArgs {
     CacheView c;  // base pointers of the layer
@@ -65,11 +68,14 @@ struct AttArgs {
     float2* part_ml;  // [2 x workers][block rows]: maximum (log2 units), sum
     float* part_o;    // [2 x workers][block rows][dim]
     int workers;
+    int whole;   // items are not shared: a worker's range is in items
+    int stream;  // K and V are read with the streaming hint
 };
 
 // One lane's share of the work: `units` items (kv head x row block) of `tiles`.
 struct LaneWork {
     int row0, rows, ctx, tokens, blocks, tiles;
+    int parts;  // tiles that can be shared out apart: all, or 1
 };
 
 __device__ __forceinline__ LaneWork lane_work(const AttArgs& a, int b, int block_rows) {
@@ -80,26 +86,32 @@ __device__ __forceinline__ LaneWork lane_work(const AttArgs& a, int b, int block
     w.tokens = (int)min((long long)w.ctx + w.rows, (long long)a.table_ld << a.c.log_page);
     w.blocks = (w.rows * a.group + block_rows - 1) / block_rows;
     w.tiles = w.rows > 0 ? (w.tokens + kTile - 1) / kTile : 0;
+    w.parts = a.whole ? min(w.tiles, 1) : w.tiles;
     return w;
 }
 
-// Inclusive sum over the wave's lanes.
+// Inclusive sum over the wave's lanes: within rows of 16 by shifts, then the rows'
+// totals carried on.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_add(int v) {
+    return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, true);
+}
 __device__ __forceinline__ int wave_scan(int v) {
-    const int l = threadIdx.x & 63;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int u = __shfl_up(v, d);
-        v += l >= d ? u : 0;
-    }
-    return v;
+    v = dpp_add<0x111, 0xF>(v);  // row_shr 1, 2, 4, 8
+    v = dpp_add<0x112, 0xF>(v);
+    v = dpp_add<0x114, 0xF>(v);
+    v = dpp_add<0x118, 0xF>(v);
+    v = dpp_add<0x142, 0xA>(v);  // row_bcast 15 into rows 1 and 3
+    return dpp_add<0x143, 0xC>(v);  // row_bcast 31 into rows 2 and 3
 }
 
-// Tiles of all items of a lane's work.
-__device__ __forceinline__ int lane_tiles(const AttArgs& a, const LaneWork& w) {
-    return w.blocks * a.c.kv_heads * w.tiles;
+// Items of a lane's work, and all of their parts.
+__device__ __forceinline__ int lane_items(const AttArgs& a, const LaneWork& w) {
+    return w.tiles > 0 ? w.blocks * a.c.kv_heads : 0;
 }
+__device__ __forceinline__ int lane_parts(const AttArgs& a, const LaneWork& w) { return lane_items(a, w) * w.parts; }
 
-// Equal shares: worker r < active takes tiles [begin(r), begin(r + 1)).
+// Equal shares: worker r < active takes parts [begin(r), begin(r + 1)).
 struct Shares {
     int active, each, rem;
     __device__ __forceinline__ int begin(int r) const { return r * each + min(r, rem); }
@@ -112,19 +124,21 @@ struct Shares {
 
 // The shares, worked out by a wave: its lane l looks at lanes l, l + 64, ... of
 // the call.  first, upto: lane l's own work (none past the last) and the sum of
-// tiles of lanes 0 .. l, for the first 64.
+// parts of lanes 0 .. l, for the first 64.
 __device__ __forceinline__ Shares shares_of(const AttArgs& a, int block_rows, LaneWork& first, int& upto) {
     const int l = threadIdx.x & 63;
-    first = LaneWork{0, 0, 0, 0, 0, 0};
+    first = LaneWork{0, 0, 0, 0, 0, 0, 0};
     if (l < a.lanes) first = lane_work(a, l, block_rows);
-    upto = wave_scan(lane_tiles(a, first));
+    upto = wave_scan(lane_parts(a, first));
     int total = __builtin_amdgcn_readlane(upto, 63);
+    int items = __builtin_amdgcn_readlane(wave_scan(lane_items(a, first)), 63);
     for (int b0 = 64; b0 < a.lanes; b0 += 64) {
-        const int v = b0 + l < a.lanes ? lane_tiles(a, lane_work(a, b0 + l, block_rows)) : 0;
-        total += __builtin_amdgcn_readlane(wave_scan(v), 63);
+        LaneWork w = {0, 0, 0, 0, 0, 0, 0};
+        if (b0 + l < a.lanes) w = lane_work(a, b0 + l, block_rows);
+        total += __builtin_amdgcn_readlane(wave_scan(lane_parts(a, w)), 63);
+        items += __builtin_amdgcn_readlane(wave_scan(lane_items(a, w)), 63);
     }
-    // Enough tiles each to outweigh the joining of their results.
-    const int active = max(1, min(a.workers, total / kMinTiles));
+    const int active = max(1, min(a.workers, max(items, total / kMinTiles)));
     return {active, (int)((unsigned)total / (unsigned)active), (int)((unsigned)total % (unsigned)active)};
 }
 
@@ -157,6 +171,12 @@ __device__ __forceinline__ void copy_to_lds(uint8_t* src, int bytes, int at, int
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)dst, 16,
                                              off, at, 0, 0);
 }
+// The same with the streaming hint.
+__device__ __forceinline__ void stream_to_lds(uint8_t* src, int bytes, int at, int off, uint8_t* dst) {
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(src, 0, bytes, 0x00020000);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)dst, 16,
+                                             off, at, 0, 2);
+}
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -164,6 +184,9 @@ __device__ __forceinline__ uint2 bf16x4(float a, float b, float c, float d) {
     return make_uint2(f32_to_bf16_rne(a) | ((uint32_t)f32_to_bf16_rne(b) << 16),
                       f32_to_bf16_rne(c) | ((uint32_t)f32_to_bf16_rne(d) << 16));
 }
+
+// Largest block of rows that is taken to be bound by memory.
+constexpr int kFewRows = 32;
 
 // How the four waves share a block: RW waves split its rows (NR row tiles of 16
 // each), TW the token halves of a tile, DW the dims of O (those repeat S).
@@ -181,10 +204,15 @@ struct AttTraits {
     // Tiles per step: 32 KiB in flight per workgroup and step.
     static constexpr int SUB = kTileBytes >= 32768 ? 1 : 32768 / kTileBytes;
     static constexpr int kStepBytes = SUB * kTileBytes;
+    // Workgroups per compute unit: two, whose phases overlap, but one for few
+    // rows, where memory is the bound and twice the partial results cost more (8
+    // lanes of 16384 tokens of dim 256: 47 us against 55), or where LDS has room
+    // for no more.
+    static constexpr int kPerUnit = kRows <= kFewRows || kStepBytes > 32768 ? 1 : 2;
 };
 
 template <int D, bool FP8, int NR, int RW, int TW, int DW, bool SPLIT>
-__global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(AttArgs a) {
+__global__ __launch_bounds__(kAttThreads, (AttTraits<D, FP8, NR, RW, TW, DW, SPLIT>::kPerUnit)) void attend_kernel(AttArgs a) {
     using T = AttTraits<D, FP8, NR, RW, TW, DW, SPLIT>;
     constexpr int ES = T::ES, kRows = T::kRows, kSegs = T::kSegs, kChunk = T::kChunk, SUB = T::SUB;
     constexpr int KS = D / 32;       // K steps of 32 dims
@@ -197,6 +225,7 @@ __global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(AttArgs a) {
     // reads of the other one.
     __shared__ __align__(16) uint8_t lds0[T::kStepBytes];
     __shared__ __align__(16) uint8_t lds1[T::kStepBytes];
+    __shared__ int lds_page[2][SUB][4];  // page of each 16-token chunk of a step, -1: none
     __shared__ float2 lds_ml[TW > 1 ? kRows : 1];
     static_assert(TW == 1 || (RW <= 2 && NR * 16 * D * 4 <= T::kStepBytes), "sums of a row wave fit");
 
@@ -226,9 +255,9 @@ __global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(AttArgs a) {
         while (!past) {
             base += __builtin_amdgcn_readlane(upto, 63);
             b0 += 64;
-            w = LaneWork{0, 0, 0, 0, 0, 0};
+            w = LaneWork{0, 0, 0, 0, 0, 0, 0};
             if (b0 + lane < a.lanes) w = lane_work(a, b0 + lane, kRows);
-            upto = wave_scan(lane_tiles(a, w));
+            upto = wave_scan(lane_parts(a, w));
             past = __ballot(base + upto > at);
         }
         const int first = __ffsll(past) - 1;
@@ -238,11 +267,12 @@ __global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(AttArgs a) {
         w.tokens = __builtin_amdgcn_readlane(w.tokens, first);
         w.blocks = __builtin_amdgcn_readlane(w.blocks, first);
         w.tiles = __builtin_amdgcn_readlane(w.tiles, first);
+        w.parts = a.whole ? 1 : w.tiles;
         b = b0 + first;
-        before = base + __builtin_amdgcn_readlane(upto, first) - lane_tiles(a, w);
+        before = base + __builtin_amdgcn_readlane(upto, first) - lane_parts(a, w);
     }
-    int item = (int)((unsigned)(at - before) / (unsigned)w.tiles);
-    int t0 = at - before - item * w.tiles;
+    int item = (int)((unsigned)(at - before) / (unsigned)w.parts);
+    int t0 = at - before - item * w.parts;
 
     const int page_mask = (1 << a.c.log_page) - 1;
     const long long head_bytes = (long long)T::kRowBytes << a.c.log_page;
@@ -270,42 +300,55 @@ __global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(AttArgs a) {
     const int v_flip = FP8 ? 0 : ((n >> 2) & 1);
 
     while (at < end) {
-        const int t1 = min(w.tiles, t0 + (end - at));
+        const int t1 = a.whole ? w.tiles : min(w.tiles, t0 + (end - at));
         const int h = (int)((unsigned)item / (unsigned)w.blocks), rb = item - h * w.blocks;
         const int rows = w.rows * a.group;  // rows of the item's lane and head
-        const int* tab = a.table + (long long)b * a.table_ld;
+        // (constant address space: scalar loads, which wait apart from the copies)
+        const auto* tab = (const __attribute__((address_space(4))) int*)(uintptr_t)(a.table + (long long)b * a.table_ld);
         uint8_t* kbase = a.c.k + h * head_bytes;
         uint8_t* vbase = a.c.v + h * head_bytes;
 
-        // Page of 16-token chunk g of tile t (past the last token: its page).
+        auto good = [&](int id) { return (unsigned)id < (unsigned)a.c.pages; };
+        // Page of this wave's 16 tokens in the tiles of the step at t (past the
+        // last token: its page).
         auto load_ids = [&](int t, int (&id)[SUB]) {
 #pragma unroll
-            for (int u = 0; u < SUB; ++u) {
-                const int p = min((t + u) * kTile + 16 * g, w.tokens - 1);
-                id[u] = tab[p >> a.c.log_page];
-            }
+            for (int u = 0; u < SUB; ++u)
+                id[u] = tab[min((t + u) * kTile + 16 * wave, w.tokens - 1) >> a.c.log_page];
         };
-        auto good = [&](int id) { return (unsigned)id < (unsigned)a.c.pages; };
         // Copies of the step at tile t.  A missing page is read as page 0 (and
-        // masked).
-        auto issue = [&](int t, const int (&id)[SUB], uint8_t* buf) {
+        // masked); past the range the copies read nothing (zero records).
+        auto issue = [&](int t, const int (&id)[SUB], uint8_t* buf, int (*pages)[4]) {
+            const int records = t < t1 ? kChunk : 0;
 #pragma unroll
             for (int u = 0; u < SUB; ++u) {
-                const int mine = __builtin_amdgcn_readlane(id[u], 16 * wave);
+                const int mine = id[u];
+                if (lane == 0) pages[u][wave] = good(mine) ? mine : -1;
                 const int tok = min((t + u) * kTile + 16 * wave, (w.tokens - 1) & ~15) & page_mask;
                 const long long off = (long long)(good(mine) ? mine : 0) * a.c.page_stride + (long long)tok * T::kRowBytes;
                 uint8_t* kd = buf + u * T::kTileBytes + wave * kChunk;
+                if (a.stream) {
 #pragma unroll
-                for (int c = 0; c < T::kCopies; ++c)
-                    copy_to_lds(kbase + off, kChunk, c * 1024, k_off[kSegs == 32 ? c & 1 : 0], kd + c * 1024);
+                    for (int c = 0; c < T::kCopies; ++c)
+                        stream_to_lds(kbase + off, records, c * 1024, k_off[kSegs == 32 ? c & 1 : 0], kd + c * 1024);
 #pragma unroll
-                for (int c = 0; c < T::kCopies; ++c)
-                    copy_to_lds(vbase + off, kChunk, c * 1024, v_off, kd + 4 * kChunk + c * 1024);
+                    for (int c = 0; c < T::kCopies; ++c)
+                        stream_to_lds(vbase + off, records, c * 1024, v_off, kd + 4 * kChunk + c * 1024);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < T::kCopies; ++c)
+                        copy_to_lds(kbase + off, records, c * 1024, k_off[kSegs == 32 ? c & 1 : 0], kd + c * 1024);
+#pragma unroll
+                    for (int c = 0; c < T::kCopies; ++c)
+                        copy_to_lds(vbase + off, records, c * 1024, v_off, kd + 4 * kChunk + c * 1024);
+                }
             }
         };
 
-        int id0[SUB], id1[SUB];
-        load_ids(t0, id0);
+        int ids[SUB], next_ids[SUB];
+        load_ids(t0, ids);
+        load_ids(t0 + SUB, next_ids);
+        issue(t0, ids, lds0, lds_page[0]);
         // Q operand: row n of each row tile, 8 dims per step.
         bf16x8 qf[NR][KS];
         unsigned long long mask[NR];
@@ -341,11 +384,11 @@ __global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(AttArgs a) {
         // unsigned sum past the array: through longer chains of pointers the
         // compiler loses which array a read is from, and makes it wait for the
         // copies in flight into the other one.)
-        auto tile = [&](int t, int idv, const uint8_t* buf, uint32_t base) {
+        auto tile = [&](int t, int page, const uint8_t* buf, uint32_t base) {
             // Tiles past the context, and those with a missing page, are masked.
-            const bool masked = (t + 1) * kTile > w.ctx || __any(!good(idv));
+            const bool masked = (t + 1) * kTile > w.ctx || __any(page < 0);
             const int chunk0 = t * kTile + 16 * g;  // this lane's first token
-            const int present = good(idv) ? min(max(w.tokens - chunk0, 0), 16) : 0;
+            const int present = page >= 0 ? min(max(w.tokens - chunk0, 0), 16) : 0;
             f32x4 s[HH][NR][2];
 #pragma unroll
             for (int hu = 0; hu < HH; ++hu) {
@@ -500,9 +543,9 @@ __global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(AttArgs a) {
         // Tokens past the end, and those of a missing page, may hold anything,
         // NaN included: their values are zeroed in LDS, each wave in the chunk that
         // it copied.
-        auto clear = [&](int t, int idv, uint8_t* buf) {
+        auto clear = [&](int t, int page, uint8_t* buf) {
             const int left = w.tokens - (t * kTile + 16 * wave);
-            const int keep = good(__builtin_amdgcn_readlane(idv, 16 * wave)) ? min(max(left, 0), 16) : 0;
+            const int keep = page >= 0 ? min(max(left, 0), 16) : 0;
             if (keep == 16) return;
             uint8_t* v = buf + (4 + wave) * kChunk;
             for (int e = lane; e < kChunk / 16; e += 64) {
@@ -514,34 +557,33 @@ __global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(AttArgs a) {
         };
         // One step: its copies have landed, the next step's are issued, and it
         // is computed.  The barrier also ends every wave's reads of the other
-        // buffer, two steps back in the list of copies.
-        auto step = [&](int t, int (&ids)[SUB], int (&next)[SUB], uint8_t* buf, uint8_t* other) {
+        // buffer.
+        auto step = [&](int t, uint8_t* buf, int (*pages)[4], uint8_t* other, int (*other_pages)[4]) {
             __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+            __builtin_amdgcn_s_waitcnt(kLgkmcnt0);
             barrier_nofence();
-            int cur[SUB];
-#pragma unroll
-            for (int u = 0; u < SUB; ++u) cur[u] = ids[u];
-            if (t + SUB < t1) {
-                issue(t + SUB, next, other);
-                load_ids(min(t + 2 * SUB, t1 - 1), ids);
-            }
+            issue(t + SUB, next_ids, other, other_pages);
+            load_ids(t + 2 * SUB, next_ids);
+            int page[SUB];  // of this lane's chunk, g
             bool missing = (t + SUB) * kTile > w.tokens;
 #pragma unroll
-            for (int u = 0; u < SUB; ++u) missing |= __any(!good(cur[u])) != 0;
+            for (int u = 0; u < SUB; ++u) {
+                page[u] = pages[u][g];
+                missing |= __any(page[u] < 0) != 0;
+            }
             if (missing) {
 #pragma unroll
-                for (int u = 0; u < SUB; ++u) clear(t + u, cur[u], buf + u * T::kTileBytes);
-                __syncthreads();
+                for (int u = 0; u < SUB; ++u) clear(t + u, pages[u][wave], buf + u * T::kTileBytes);
+                __builtin_amdgcn_s_waitcnt(kLgkmcnt0);
+                barrier_nofence();
             }
 #pragma unroll
             for (int u = 0; u < SUB; ++u)
-                if (t + u < t1) tile(t + u, cur[u], buf, u * T::kTileBytes);
+                if (t + u < t1) tile(t + u, page[u], buf, u * T::kTileBytes);
         };
-        issue(t0, id0, lds0);
-        load_ids(min(t0 + SUB, t1 - 1), id1);
         for (int t = t0; t < t1; t += 2 * SUB) {
-            step(t, id0, id1, lds0, lds1);
-            if (t + SUB < t1) step(t + SUB, id1, id0, lds1, lds0);
+            step(t, lds0, lds_page[0], lds1, lds_page[1]);
+            if (t + SUB < t1) step(t + SUB, lds1, lds_page[1], lds0, lds_page[0]);
         }
 
         // Sums over the four token groups of a row.
@@ -550,6 +592,7 @@ __global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(AttArgs a) {
             l[r] += __shfl_xor(l[r], 16);
             l[r] += __shfl_xor(l[r], 32);
         }
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));  // the last, empty copies
         __syncthreads();
         // The two waves that split the token halves meet in LDS.
         if (TW > 1) {
@@ -611,7 +654,7 @@ __global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(AttArgs a) {
             }
         }
         // Next item.
-        at += t1 - t0;
+        at += a.whole ? 1 : t1 - t0;
         t0 = 0;
         if (at < end) {
             if (++item == w.blocks * a.c.kv_heads) {
@@ -624,49 +667,54 @@ __global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(AttArgs a) {
     }
 }
 
-// Joins the partial results of items that several workers shared: one wave per
-// row, contributors in worker order, kFan of them loaded at once.
+// Joins the partial results of items that several workers shared.  A row is taken
+// by one wave, or by the block's four (WIDE) where it can have more contributors
+// than kFan; a wave loads kFan of them at once.  The order of the sums is that of
+// the workers.
 constexpr int kFan = 16;
-template <int D>
+template <int D, bool WIDE>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttArgs a, int block_rows, int max_blocks) {
+    constexpr int E = D / 64;
+    typedef float vec __attribute__((ext_vector_type(E)));
+    __shared__ float lds_acc[WIDE ? 4 : 1][D];
+    __shared__ float2 lds_ml[4];
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), lane = threadIdx.x & 63;
     const int b = blockIdx.z, h = (int)(blockIdx.y / (unsigned)max_blocks), rb = blockIdx.y - h * max_blocks;
-    const int in_block = blockIdx.x * 4 + wave, row = rb * block_rows + in_block;
+    const int in_block = WIDE ? blockIdx.x : blockIdx.x * 4 + wave, row = rb * block_rows + in_block;
     LaneWork w;
     int upto;
     const Shares share = shares_of(a, block_rows, w, upto);
-    int before = 0;  // tiles of the lanes before b
+    int before = 0;  // parts of the lanes before b
     if (b < 64) {
-        before = __builtin_amdgcn_readlane(upto, b) - __builtin_amdgcn_readlane(lane_tiles(a, w), b);
+        before = __builtin_amdgcn_readlane(upto, b) - __builtin_amdgcn_readlane(lane_parts(a, w), b);
         w.row0 = __builtin_amdgcn_readlane(w.row0, b);
         w.rows = __builtin_amdgcn_readlane(w.rows, b);
         w.blocks = __builtin_amdgcn_readlane(w.blocks, b);
         w.tiles = __builtin_amdgcn_readlane(w.tiles, b);
     } else {
         for (int b0 = 0; b0 < b; b0 += 64) {
-            const int v = b0 + lane < b ? lane_tiles(a, lane_work(a, b0 + lane, block_rows)) : 0;
+            const int v = b0 + lane < b ? lane_parts(a, lane_work(a, b0 + lane, block_rows)) : 0;
             before += __builtin_amdgcn_readlane(wave_scan(v), 63);
         }
         w = lane_work(a, b, block_rows);
     }
-    if (rb >= w.blocks || row >= w.rows * a.group || in_block >= block_rows || w.tiles == 0) return;  // whole wave
+    if (rb >= w.blocks || row >= w.rows * a.group || in_block >= block_rows || w.tiles == 0) return;  // whole wave (WIDE: block)
     const int start = before + (h * w.blocks + rb) * w.tiles;  // the item's first tile
     const int r0 = share.owner(start), r1 = share.owner(start + w.tiles - 1);
     if (r0 == r1) return;
-    const int tt = (int)((unsigned)row / (unsigned)a.group), head = h * a.group + row - tt * a.group;
-    constexpr int E = D / 64;
-    typedef float vec __attribute__((ext_vector_type(E)));
     auto slot = [&](int r) { return (long long)(2 * r + (r > r0 ? 0 : 1)) * block_rows + in_block; };
     float mx = -__builtin_inff(), sum = 0.f;
     float acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    for (int r = r0; r <= r1; r += kFan) {
+    const int each = WIDE ? (r1 - r0 + 4) / 4 : 0;
+    const int from = WIDE ? r0 + wave * each : r0, to = WIDE ? min(from + each - 1, r1) : r1;
+    for (int r = from; r <= to; r += kFan) {
         float2 ml[kFan];
         vec v[kFan];
 #pragma unroll
         for (int u = 0; u < kFan; ++u) {
-            const long long s = slot(min(r + u, r1));
+            const long long s = slot(min(r + u, to));
             ml[u] = a.part_ml[s];
             v[u] = *(const vec*)(a.part_o + s * D + E * lane);
         }
@@ -681,12 +729,32 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttArgs a, int block_r
         for (int e = 0; e < E; ++e) acc[e] *= old;
 #pragma unroll
         for (int u = 0; u < kFan; ++u) {
-            const float f = r + u <= r1 ? exp2_fast(ml[u].x - use) : 0.f;
+            const float f = r + u <= to ? exp2_fast(ml[u].x - use) : 0.f;
             sum = __builtin_fmaf(ml[u].y, f, sum);
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = __builtin_fmaf(E == 1 ? v[u][0] : v[u][e], f, acc[e]);
+            for (int e = 0; e < E; ++e) acc[e] = __builtin_fmaf(v[u][e], f, acc[e]);
         }
     }
+    if (WIDE) {
+        if (lane == 0) lds_ml[wave] = make_float2(mx, sum);
+#pragma unroll
+        for (int e = 0; e < E; ++e) lds_acc[wave][E * lane + e] = acc[e];
+        __syncthreads();
+        if (wave != 0) return;
+        mx = fmaxf(fmaxf(lds_ml[0].x, lds_ml[1].x), fmaxf(lds_ml[2].x, lds_ml[3].x));
+        const float use = mx == -__builtin_inff() ? 0.f : mx;
+        sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const float f = exp2_fast(lds_ml[u].x - use);
+            sum = __builtin_fmaf(lds_ml[u].y, f, sum);
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = __builtin_fmaf(lds_acc[u][E * lane + e], f, acc[e]);
+        }
+    }
+    const int tt = (int)((unsigned)row / (unsigned)a.group), head = h * a.group + row - tt * a.group;
     const float inv = sum > 0.f ? a.c.v_scale / sum : 0.f;
     uint16_t* dst = a.out + (long long)(w.row0 + tt) * a.out_ld + (long long)head * D + E * lane;
     if constexpr (E == 1) {
@@ -716,9 +784,11 @@ AttShape att_shape(int rows, int dim) {
     return {2, 4, 1, 1};
 }
 
-int att_workers() {
-    const int n = 2 * device_cus();
-    return n / 8 * 8;
+// Workgroups: as many as the compute units hold at once.
+int att_workers(const AttShape& sh, int dim, bool fp8) {
+    const int step = dim == 256 && !fp8 ? 65536 : 32768;
+    const int per_unit = step > 32768 || sh.block_rows() <= kFewRows ? 1 : 2;
+    return per_unit * device_cus() / 8 * 8;
 }
 
 template <int D, bool FP8>
@@ -750,15 +820,22 @@ int launch_attend(const AttShape& sh, const AttArgs& a, bool joins, hipStream_t 
     if (!joins) return NVFP4_OK;
     const int rows = a.max_rows * a.group, br = sh.block_rows();
     const int max_blocks = (rows + br - 1) / br;
-    const dim3 grid((unsigned)((rows < br ? rows : br) + 3) / 4, (unsigned)(a.c.kv_heads * max_blocks), (unsigned)a.lanes);
-    hipLaunchKernelGGL((attend_join_kernel<D>), grid, dim3(256), 0, s, a, br, max_blocks);
+    // An item of an even split has at most so many contributors; rows of few
+    // blocks (a decode step of few lanes) are the ones with more than kFan.
+    const int in_block = rows < br ? rows : br;
+    const long long items = (long long)a.lanes * a.c.kv_heads * max_blocks;
+    const bool wide = a.workers / items >= kFan;
+    const dim3 grid((unsigned)(wide ? in_block : (in_block + 3) / 4), (unsigned)(a.c.kv_heads * max_blocks), (unsigned)a.lanes);
+    if (wide)
+        hipLaunchKernelGGL((attend_join_kernel<D, true>), grid, dim3(256), 0, s, a, br, max_blocks);
+    else
+        hipLaunchKernelGGL((attend_join_kernel<D, false>), grid, dim3(256), 0, s, a, br, max_blocks);
     NVFP4_HIP(hipGetLastError());
     return NVFP4_OK;
 }
 
-size_t part_ml_bytes(const AttShape& sh) {
-    return (size_t)2 * att_workers() * sh.block_rows() * sizeof(float2);
-}
+// Most partial results of a call: two per worker, of a block's rows.
+size_t part_rows(const AttShape& sh) { return (size_t)2 * 2 * device_cus() * sh.block_rows(); }
 
 }  // namespace nvfp4
 
@@ -772,7 +849,7 @@ size_t nvfp4_tree_attention_workspace_bytes(int q_heads, int kv_heads, int head_
         q_heads > 65536)
         return 0;
     const AttShape sh = att_shape(max_rows * (q_heads / kv_heads), head_dim);
-    return part_ml_bytes(sh) + (size_t)2 * att_workers() * sh.block_rows() * head_dim * sizeof(float);
+    return part_rows(sh) * (sizeof(float2) + head_dim * sizeof(float));
 }
 
 int nvfp4_tree_mask(const int* parent, int n, uint64_t* mask, int* depth) {
@@ -844,12 +921,21 @@ int nvfp4_tree_attention(const nvfp4_cache* cache, int layer, const uint16_t* q_
     a.out_ld = out_ld;
     a.lse = lse_dev;
     // No more workgroups than the tables could ever feed.
-    const long long most = (tiles + kMinTiles - 1) / kMinTiles;
-    a.workers = most < att_workers() ? (int)most : att_workers();
+    const long long items = (long long)lanes * kv * blocks, per_item = tiles / items;
+    a.whole = per_item <= kWholeTiles;
+    const long long shared = (tiles + kMinTiles - 1) / kMinTiles, most = a.whole || shared < items ? items : shared;
+    const int workers = att_workers(sh, dim, a.c.fp8 != 0);
+    a.workers = most < workers ? (int)most : workers;
     a.part_ml = (float2*)workspace_dev;
-    a.part_o = (float*)((char*)workspace_dev + part_ml_bytes(sh));
-    // One worker never shares an item.
-    const bool joins = a.workers > 1;
+    a.part_o = (float*)((char*)workspace_dev + part_rows(sh) * sizeof(float2));
+    const bool joins = !a.whole && a.workers > 1;
+    // The streaming hint, where K and V are read once (one block holds every row of
+    // a lane and head) and the cache is larger than the 256 MiB that the chip's last
+    // cache can keep from call to call.  8 lanes of 40960 tokens (451 MB), 12 rows:
+    // 91 us without, 81 with; 8 of 4096 (45 MB): 19.4 without, 21.3 with; four blocks
+    // of 128 rows: 131 without, 149 with.
+    const double cache_bytes = 2.0 * a.c.layers * a.c.pages * ((double)kv * dim * (a.c.fp8 ? 1 : 2) * (1 << a.c.log_page));
+    a.stream = blocks == 1 && cache_bytes > 64.0 * (1 << 20);
     hipStream_t s = (hipStream_t)stream;
     if (dim == 64) return launch_attend<64>(sh, a, joins, s);
     if (dim == 128) return launch_attend<128>(sh, a, joins, s);
