@@ -390,47 +390,50 @@ __global__ __launch_bounds__(kAttThreads, (AttTraits<D, FP8, NR, RW, TW, DW, SPL
             const int chunk0 = t * kTile + 16 * g;  // this lane's first token
             const int present = page >= 0 ? min(max(w.tokens - chunk0, 0), 16) : 0;
             f32x4 s[HH][NR][2];
-#pragma unroll
-            for (int hu = 0; hu < HH; ++hu) {
-                const int hh = TW == 2 ? tw : hu;
-#pragma unroll
-                for (int r = 0; r < NR; ++r)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) s[hu][r][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-                const uint32_t kb = base + (uint32_t)(hh * 8 * T::kRowBytes);
-                // All operand reads of a product go out before its first
-                // instruction (left alone, the compiler waits for each read).
-                uint4 kr[KL][2];
+            // Operand reads go out well before their products, all of K first and
+            // V of a half during the products before it (left alone, the compiler
+            // waits for each read).
+            uint4 kr[HH][KL][2];
+            VRaw vr[HH][DB];
+            auto read_k = [&](int hu) {
+                const uint32_t kb = base + (uint32_t)((TW == 2 ? tw : hu) * 8 * T::kRowBytes);
 #pragma unroll
                 for (int u = 0; u < KL; ++u)
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
-                        kr[u][i] = *(const uint4*)(buf + (kb + (uint32_t)k_at[u % KA] + (uint32_t)((u / KA) * KA * 64 + i * 4 * T::kRowBytes)));
+                        kr[hu][u][i] = *(const uint4*)(buf + (kb + (uint32_t)k_at[u % KA] + (uint32_t)((u / KA) * KA * 64 + i * 4 * T::kRowBytes)));
+            };
+            auto read_v = [&](int hu) {
+                const int hh = TW == 2 ? tw : hu;
+                const uint32_t vo = base + 4u * kChunk + (uint32_t)v_at + (uint32_t)(dw * DB * (FP8 ? 256 : 512)) +
+                                    (uint32_t)(FP8 ? 8 * hh : (hh ^ v_flip) * 16);
+#pragma unroll
+                for (int db = 0; db < DB; ++db) vr[hu][db] = *(const VRaw*)(buf + (vo + db * (FP8 ? 256u : 512u)));
+            };
+#pragma unroll
+            for (int hu = 0; hu < HH; ++hu) read_k(hu);
+#pragma unroll
+            for (int hu = 0; hu < HH; ++hu) {
                 __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int r = 0; r < NR; ++r)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) s[hu][r][i] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         bf16x8 kv;
                         if (FP8)
-                            kv = (ks & 1) ? e4m3x8_to_bf16(kr[ks / 2][i].z, kr[ks / 2][i].w) : e4m3x8_to_bf16(kr[ks / 2][i].x, kr[ks / 2][i].y);
+                            kv = (ks & 1) ? e4m3x8_to_bf16(kr[hu][ks / 2][i].z, kr[hu][ks / 2][i].w) : e4m3x8_to_bf16(kr[hu][ks / 2][i].x, kr[hu][ks / 2][i].y);
                         else
-                            kv = bytes8(kr[FP8 ? 0 : ks][i]);
+                            kv = bytes8(kr[hu][FP8 ? 0 : ks][i]);
 #pragma unroll
                         for (int r = 0; r < NR; ++r)
                             s[hu][r][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kv, qf[r][ks], s[hu][r][i], 0, 0, 0);
                     }
+                if (hu == 0) read_v(0);
             }
-            // V is on its way during the softmax.
-            VRaw vr[DB];
-            auto read_v = [&](int hu) {
-                const int hh = TW == 2 ? tw : hu;
-                const uint32_t vo = base + 4u * kChunk + (uint32_t)v_at + (uint32_t)(dw * DB * (FP8 ? 256 : 512)) +
-                                    (uint32_t)(FP8 ? 8 * hh : (hh ^ v_flip) * 16);
-#pragma unroll
-                for (int db = 0; db < DB; ++db) vr[db] = *(const VRaw*)(buf + (vo + db * (FP8 ? 256u : 512u)));
-            };
-            read_v(0);
             __builtin_amdgcn_sched_barrier(0);
             if (masked) {
 #pragma unroll
@@ -501,13 +504,13 @@ __global__ __launch_bounds__(kAttThreads, (AttTraits<D, FP8, NR, RW, TW, DW, SPL
             // accumulator stand apart: the second waits for the first.
             constexpr int kSteps = NR * DB * (SPLIT ? 2 : 1);
             bf16x8 vv[DB];
-            auto convert = [&]() {
+            auto convert = [&](int hu) {
 #pragma unroll
                 for (int db = 0; db < DB; ++db) {
                     if constexpr (FP8)
-                        vv[db] = e4m3x8_to_bf16(vr[db].x, vr[db].y);
+                        vv[db] = e4m3x8_to_bf16(vr[hu][db].x, vr[hu][db].y);
                     else
-                        vv[db] = bytes8(vr[db]);
+                        vv[db] = bytes8(vr[hu][db]);
                 }
             };
             auto product = [&](int hu, int i) {
@@ -518,7 +521,7 @@ __global__ __launch_bounds__(kAttThreads, (AttTraits<D, FP8, NR, RW, TW, DW, SPL
             for (int r = 0; r < NR; ++r)
 #pragma unroll
                 for (int e = 0; e < 8; e += 2) weights(0, r, e);
-            convert();
+            convert(0);
             if (HH == 1) {
 #pragma unroll
                 for (int i = 0; i < kSteps; ++i) product(0, i);
@@ -526,6 +529,7 @@ __global__ __launch_bounds__(kAttThreads, (AttTraits<D, FP8, NR, RW, TW, DW, SPL
                 // The second half's weights are formed while the matrix cores
                 // are busy with the first half's product, piece by piece.
                 constexpr int kPieces = 4 * NR;
+                read_v(HH - 1);
 #pragma unroll
                 for (int u = 0; u < kPieces; ++u) {
                     __builtin_amdgcn_sched_barrier(0);
@@ -534,8 +538,7 @@ __global__ __launch_bounds__(kAttThreads, (AttTraits<D, FP8, NR, RW, TW, DW, SPL
                     weights(HH - 1, u / 4, u % 4 * 2);
                 }
                 __builtin_amdgcn_sched_barrier(0);
-                read_v(HH - 1);
-                convert();
+                convert(HH - 1);
 #pragma unroll
                 for (int i = 0; i < kSteps; ++i) product(HH - 1, i);
             }
