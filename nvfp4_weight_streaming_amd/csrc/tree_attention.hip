@@ -410,34 +410,22 @@ __global__ __launch_bounds__(kAttThreads, (AttTraits<D, FP8, NR, RW, TW, DW, SPL
 #pragma unroll
                 for (int db = 0; db < DB; ++db) vr[hu][db] = *(const VRaw*)(buf + (vo + db * (FP8 ? 256u : 512u)));
             };
-#pragma unroll
-            for (int hu = 0; hu < HH; ++hu) read_k(hu);
-#pragma unroll
-            for (int hu = 0; hu < HH; ++hu) {
-                __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                for (int r = 0; r < NR; ++r)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) s[hu][r][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        bf16x8 kv;
-                        if (FP8)
-                            kv = (ks & 1) ? e4m3x8_to_bf16(kr[hu][ks / 2][i].z, kr[hu][ks / 2][i].w) : e4m3x8_to_bf16(kr[hu][ks / 2][i].x, kr[hu][ks / 2][i].y);
-                        else
-                            kv = bytes8(kr[hu][FP8 ? 0 : ks][i]);
-#pragma unroll
-                        for (int r = 0; r < NR; ++r)
-                            s[hu][r][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kv, qf[r][ks], s[hu][r][i], 0, 0, 0);
-                    }
-                if (hu == 0) read_v(0);
-            }
-            __builtin_amdgcn_sched_barrier(0);
-            if (masked) {
-#pragma unroll
-                for (int hu = 0; hu < HH; ++hu)
+            // S of a half, instruction i of kDots.
+            constexpr int kDots = KS * 2 * NR;
+            auto dot = [&](int hu, int j) {
+                const int ks = j / (2 * NR), i = j / NR % 2, r = j % NR;
+                bf16x8 kv;
+                if (FP8)
+                    kv = (ks & 1) ? e4m3x8_to_bf16(kr[hu][ks / 2][i].z, kr[hu][ks / 2][i].w) : e4m3x8_to_bf16(kr[hu][ks / 2][i].x, kr[hu][ks / 2][i].y);
+                else
+                    kv = bytes8(kr[hu][FP8 ? 0 : ks][i]);
+                const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+                s[hu][r][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kv, qf[r][ks], ks == 0 ? zero : s[hu][r][i], 0, 0, 0);
+            };
+            // Masks a half and raises the rows' maxima where they grew too far; then
+            // `before` runs ahead of the rescale of O.  True if there was one.
+            auto settle = [&](int hu, auto&& before) -> bool {
+                if (masked) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const int c = 8 * (TW == 2 ? tw : hu) + e, p = chunk0 + c;
@@ -448,21 +436,19 @@ __global__ __launch_bounds__(kAttThreads, (AttTraits<D, FP8, NR, RW, TW, DW, SPL
                             s[hu][r][e >> 2][e & 3] = seen ? s[hu][r][e >> 2][e & 3] : -__builtin_inff();
                         }
                     }
-            }
-            float top[NR];
-            bool grow = false;
+                }
+                float top[NR];
+                bool grow = false;
 #pragma unroll
-            for (int r = 0; r < NR; ++r) {
-                float x = -__builtin_inff();
+                for (int r = 0; r < NR; ++r) {
+                    float x = s[hu][r][0][0];
 #pragma unroll
-                for (int hu = 0; hu < HH; ++hu)
-#pragma unroll
-                    for (int e = 0; e < 8; e += 2)
-                        x = fmaxf(x, fmaxf(s[hu][r][e >> 2][e & 3], s[hu][r][e >> 2][(e & 3) + 1]));
-                top[r] = x * a.scale2;
-                grow |= top[r] > m[r] + kRescaleAt;
-            }
-            if (__any(grow)) {
+                    for (int e = 1; e < 8; ++e) x = fmaxf(x, s[hu][r][e >> 2][e & 3]);
+                    top[r] = x * a.scale2;
+                    grow |= top[r] > m[r] + kRescaleAt;
+                }
+                if (!__any(grow)) return false;
+                before();
 #pragma unroll
                 for (int r = 0; r < NR; ++r) {
                     float mx = fmaxf(top[r], __shfl_xor(top[r], 16));
@@ -478,11 +464,14 @@ __global__ __launch_bounds__(kAttThreads, (AttTraits<D, FP8, NR, RW, TW, DW, SPL
 #pragma unroll
                         for (int j = 0; j < 4; ++j) o[r][db][j] *= f;
                 }
-            }
-            // Weights of a half, as one or two bf16 operands: piece e of row tile
-            // r is a pair.
-            bf16x8 ph[HH][NR], pl[HH][NR];
-            auto weights = [&](int hu, int r, int e) {
+                return true;
+            };
+            // Weights of a half, as one or two bf16 operands: piece u is the pair
+            // u % 4 of row tile u / 4.
+            uint32_t pw[HH][NR][SPLIT ? 2 : 1][4];
+            constexpr int kPieces = 4 * NR;
+            auto weights = [&](int hu, int u) {
+                const int r = u / 4, e = u % 4 * 2;
                 f32x2v p;
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
@@ -490,14 +479,17 @@ __global__ __launch_bounds__(kAttThreads, (AttTraits<D, FP8, NR, RW, TW, DW, SPL
                     l[r] += p[q];
                 }
                 const bf16x2v hi = __builtin_convertvector(p, bf16x2v);
-                ph[hu][r][e] = hi[0];
-                ph[hu][r][e + 1] = hi[1];
+                uint32_t bits;
+                __builtin_memcpy(&bits, &hi, 4);
+                opaque(bits);  // formed here, not where it is used
+                pw[hu][r][0][e / 2] = bits;
                 if (SPLIT) {
-                    const f32x2v back = __builtin_convertvector(hi, f32x2v);
+                    const f32x2v back = {__uint_as_float(bits << 16), __uint_as_float(bits & 0xFFFF0000u)};
                     const f32x2v rest = {p[0] - back[0], p[1] - back[1]};
                     const bf16x2v lo = __builtin_convertvector(rest, bf16x2v);
-                    pl[hu][r][e] = lo[0];
-                    pl[hu][r][e + 1] = lo[1];
+                    __builtin_memcpy(&bits, &lo, 4);
+                    opaque(bits);
+                    pw[hu][r][1][e / 2] = bits;
                 }
             };
             // The product of a half, instruction i of kSteps.  The two of an
@@ -515,33 +507,62 @@ __global__ __launch_bounds__(kAttThreads, (AttTraits<D, FP8, NR, RW, TW, DW, SPL
             };
             auto product = [&](int hu, int i) {
                 const int db = i % (NR * DB) / NR, r = i % NR;
-                o[r][db] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vv[db], i < NR * DB ? ph[hu][r] : pl[hu][r], o[r][db], 0, 0, 0);
+                const uint32_t(&w)[4] = pw[hu][r][i < NR * DB ? 0 : SPLIT];
+                o[r][db] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vv[db], bytes8(make_uint4(w[0], w[1], w[2], w[3])), o[r][db], 0, 0, 0);
             };
+
 #pragma unroll
-            for (int r = 0; r < NR; ++r)
+            for (int hu = 0; hu < HH; ++hu) read_k(hu);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int e = 0; e < 8; e += 2) weights(0, r, e);
-            convert(0);
+            for (int j = 0; j < kDots; ++j) dot(0, j);
             if (HH == 1) {
+                read_v(0);
+                __builtin_amdgcn_sched_barrier(0);
+                settle(0, [] {});
+#pragma unroll
+                for (int u = 0; u < kPieces; ++u) weights(0, u);
+                convert(0);
 #pragma unroll
                 for (int i = 0; i < kSteps; ++i) product(0, i);
+                return;
+            }
+            // Two halves: the vector work of each stands beside matrix instructions
+            // that do not need it, piece by piece: the first half's weights beside
+            // the second half's S, the second's beside the first's product.
+            constexpr int H = HH - 1;
+            settle(0, [] {});
+            read_v(0);
+#pragma unroll
+            for (int u = 0; u < kPieces; ++u) {
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int j = u * kDots / kPieces; j < (u + 1) * kDots / kPieces; ++j) dot(H, j);
+                weights(0, u);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            convert(0);
+            const bool grew = settle(H, [&] {
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i) product(0, i);
+            });
+            read_v(H);
+            if (grew) {
+#pragma unroll
+                for (int u = 0; u < kPieces; ++u) weights(H, u);
             } else {
-                // The second half's weights are formed while the matrix cores
-                // are busy with the first half's product, piece by piece.
-                constexpr int kPieces = 4 * NR;
-                read_v(HH - 1);
 #pragma unroll
                 for (int u = 0; u < kPieces; ++u) {
                     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                     for (int i = u * kSteps / kPieces; i < (u + 1) * kSteps / kPieces; ++i) product(0, i);
-                    weights(HH - 1, u / 4, u % 4 * 2);
+                    weights(H, u);
                 }
-                __builtin_amdgcn_sched_barrier(0);
-                convert(HH - 1);
-#pragma unroll
-                for (int i = 0; i < kSteps; ++i) product(HH - 1, i);
             }
+            __builtin_amdgcn_sched_barrier(0);
+            convert(H);
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) product(H, i);
         };
         // Tokens past the end, and those of a missing page, may hold anything,
         // NaN included: their values are zeroed in LDS, each wave in the chunk that
