@@ -349,12 +349,12 @@ def beam_select(logits, beams, score, k, done=None, eos=-1, stream=None):
         _refuse("done: not %d contiguous uint8 values" % rows)
     L, dev = _lib or lib(), logits.device
     shape = (batch, k)
-    out = torch.empty(shape, dtype=torch.float32, device=dev)
+    out = score.new_empty(shape)
     parent = torch.empty(shape, dtype=torch.int32, device=dev)
-    token = torch.empty(shape, dtype=torch.int32, device=dev)
-    ended = torch.empty(shape, dtype=torch.uint8, device=dev)
+    token = torch.empty_like(parent)
+    ended = torch.empty(shape, dtype=torch.uint8, device=dev) if done is None else done.new_empty(shape)
     wsb = L.nvfp4_beam_workspace_bytes(batch, beams, V)
-    ws = torch.empty(wsb or 16, dtype=torch.uint8, device=dev)
+    ws = score.new_empty(wsb // 4 + 4)
     st = L.nvfp4_beam_select(logits.data_ptr(), dtype, ld if rows > 1 else max(ld, V), batch, beams, V,
                              score.data_ptr(), None if done is None else done.data_ptr(), eos, k,
                              out.data_ptr(), parent.data_ptr(), token.data_ptr(), ended.data_ptr(),
@@ -533,6 +533,7 @@ class PagedCache:
                           CACHE_BF16 if es == 2 else CACHE_E4M3, float(k_scale), float(v_scale),
                           strides[0][1], strides[0][0])
         self._ref = ctypes.byref(self.desc)
+        self._attend_ws = {}  # workspace bytes by (q heads, rows)
 
     def _bad_lanes(self, row_start, ctx_len, page_table, lanes):
         """Names what is wrong with a call's lanes."""
@@ -569,7 +570,7 @@ class PagedCache:
                                           and pair_axis.numel() == pairs):
             _refuse("pair_axis: not %d contiguous uint8 values" % pairs)
         if out is None:
-            out, q_ld = torch.empty((rows, width), dtype=bf16, device=dev), width
+            out, q_ld = qkv.new_empty((rows, width)), width
         else:
             q_ld = self._out_ld(out, rows, width)
         rot = Rotary(positions.data_ptr(), inv_freq.data_ptr(),
@@ -615,12 +616,15 @@ class PagedCache:
         if not (mask.dtype is torch.int64 and mask.numel() == rows and mask.is_contiguous()):
             _refuse("mask: not %d contiguous int64 values" % rows)
         if out is None:
-            out, out_ld = torch.empty((rows, width), dtype=bf16, device=dev), width
+            out, out_ld = q.new_empty((rows, width)), width
         else:
             out_ld = self._out_ld(out, rows, width)
         lse = torch.empty((rows, q_heads), dtype=torch.float32, device=dev) if with_lse else None
-        wsb = L.nvfp4_tree_attention_workspace_bytes(q_heads, self.kv_heads, dim, max_rows)
-        ws = torch.empty(wsb or 16, dtype=torch.uint8, device=dev)
+        wsb = self._attend_ws.get((q_heads, max_rows))
+        if wsb is None:
+            wsb = L.nvfp4_tree_attention_workspace_bytes(q_heads, self.kv_heads, dim, max_rows)
+            self._attend_ws[q_heads, max_rows] = wsb
+        ws = q.new_empty(wsb // 2 + 8)
         st = L.nvfp4_tree_attention(self._ref, layer, q.data_ptr(), ld if rows > 1 else max(ld, width), q_heads,
                                     lanes, max_rows, row_start.data_ptr(), ctx_len.data_ptr(),
                                     page_table.data_ptr(), page_table.shape[1], mask.data_ptr(), scale,
@@ -662,12 +666,12 @@ class PagedCache:
         for x, name in ((parent, "parent"), (keep, "keep"), (reserve, "reserve")):
             if x is not None and not (x.dtype is i32 and x.is_contiguous() and x.numel() == n):
                 _refuse("%s: not %d contiguous int32 values" % (name, n))
-        table = torch.empty((n, width), dtype=i32, device=dev)
-        new_len = torch.empty(n, dtype=i32, device=dev)
-        new_refs = torch.empty(self.pages, dtype=i32, device=dev)
-        short = torch.empty(1, dtype=i32, device=dev)
+        table = page_table.new_empty((n, width))
+        new_len = torch.empty_like(parent)
+        new_refs = torch.empty_like(refs)
+        short = refs.new_empty(1)
         wsb = L.nvfp4_cache_update_workspace_bytes(self.pages, n, width)
-        ws = torch.empty(wsb or 16, dtype=torch.uint8, device=dev)
+        ws = refs.new_empty(wsb // 4 + 4)
         st = L.nvfp4_cache_update(self._ref, lanes, page_table.data_ptr(), length.data_ptr(), refs.data_ptr(),
                                   width, n, parent.data_ptr(), None if keep is None else keep.data_ptr(),
                                   None if reserve is None else reserve.data_ptr(), table.data_ptr(),
