@@ -21,8 +21,8 @@ namespace nvfp4 {
 
 constexpr int kBeamGroup = 1024;
 constexpr int kBeamThreads = 256;      // scan: 4 waves, one group each
-constexpr int kBeamRun = 2;            // groups per wave
-constexpr int kBeamPickThreads = 512;  // pick: 8 waves
+constexpr int kBeamRun = 2;             // groups per wave
+constexpr int kBeamPickThreads = 1024;  // pick: 16 waves
 constexpr int kBeamList = 1024;        // keys the pick kernel ranks at once
 
 struct BeamArgs {
@@ -172,11 +172,15 @@ __global__ __launch_bounds__(kBeamThreads) void beam_scan_kernel(BeamArgs a) {
 #pragma unroll
         for (int e = 1; e < 16; ++e) m = fmaxf(m, x[u][e]);
         m = wave_max(m);
+        // exp(x - m) as 2^(x c - m c), the product m c rounded: what that loses is
+        // the same for every term and put right once.
         const float use = m == -__builtin_inff() ? 0.f : m;
+        constexpr float c = 1.44269504088896340736f;
+        const float mc = use * c, lost = __builtin_fmaf(use, c, -mc);
         float s = 0.f;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) s += exp_diff(x[u][e], use);
-        s = wave_sum(s);
+        for (int e = 0; e < 16; ++e) s += __builtin_amdgcn_exp2f(__builtin_fmaf(x[u][e], c, -mc));
+        s = wave_sum(s) * __builtin_amdgcn_exp2f(-lost);
         if (lane == 0 && group0 + u < a.groups) a.part[(long long)row * a.groups + group0 + u] = make_float2(m, s);
     }
 }
@@ -228,20 +232,22 @@ __device__ __forceinline__ void rank_keys(const u64* list, int n, int k, u64* be
     if ((int)threadIdx.x >= n && (int)threadIdx.x < k) best[threadIdx.x] = 0;
 }
 
-// The k-th largest of the wave's 64 keys, one a lane (the smallest nonzero one
-// if there are fewer than k; keys are distinct but for zeros).
-__device__ __forceinline__ u64 wave_kth(u64 head, int k) {
-    u64 lo = 1, hi = ~0ull;  // at least k keys >= lo (or lo = 1), fewer than k > hi
+// A bar that at least k, and if it can fewer than 2 k, of the wave's 64 keys
+// pass, one key a lane; the smallest nonzero one passes where fewer than k are not 0.
+__device__ __forceinline__ u64 wave_bar(u64 head, int k) {
+    const unsigned int h = (unsigned int)(head >> 32);
+    unsigned int lo = 0, hi = (unsigned int)(wave_max64(head) >> 32);  // at least k keys >= lo, or lo is 0
     while (lo < hi) {
-        const u64 mid = lo + (hi - lo) / 2 + ((hi - lo) & 1);
-        const int n = __popcll(__ballot(head >= mid));
-        if (n == k) return mid;
-        if (n > k)
-            lo = mid;
-        else
+        const unsigned int mid = lo + (hi - lo) / 2 + ((hi - lo) & 1);
+        const int n = __popcll(__ballot(h >= mid && head != 0));
+        if (n < k) {
             hi = mid - 1;
+        } else {
+            lo = mid;
+            if (n < 2 * k) break;
+        }
     }
-    return lo;
+    return lo ? (u64)lo << 32 : 1;
 }
 
 template <bool BF16, bool VEC>
@@ -250,7 +256,7 @@ __global__ __launch_bounds__(kBeamPickThreads) void beam_pick_kernel(BeamArgs a)
     __shared__ float row_m[NVFP4_BEAM_MAX_BEAMS], row_z[NVFP4_BEAM_MAX_BEAMS], row_c[NVFP4_BEAM_MAX_BEAMS];
     __shared__ int row_s[NVFP4_BEAM_MAX_BEAMS];
     __shared__ u64 list[kBeamList];
-    __shared__ u64 best[64];
+    __shared__ u64 best[64], bars[kWaves];
     __shared__ int counts[2];
     static_assert(kBeamList >= kWaves * 64, "the waves' lists fit");
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), lane = threadIdx.x & 63;
@@ -289,8 +295,7 @@ __global__ __launch_bounds__(kBeamPickThreads) void beam_pick_kernel(BeamArgs a)
     }
     __syncthreads();
 
-    // The k best groups.  The k-th best of the lanes' best groups bounds them
-    // from below; what passes it is ranked.
+    // The k best groups: what passes a bar that at least k pass is ranked.
     const int n = a.beams * a.groups;
     auto group_key = [&](int i) -> u64 {
         if (i >= n) return 0;
@@ -300,7 +305,15 @@ __global__ __launch_bounds__(kBeamPickThreads) void beam_pick_kernel(BeamArgs a)
     };
     u64 head = 0;
     for (int i = threadIdx.x; i < n; i += kBeamPickThreads) head = max64(head, group_key(i));
-    const u64 bar = wave_kth(head, a.k);
+    // (A wave's own k keys pass its bar, so the highest of the bars is one for all.)
+    {
+        const u64 mine = wave_bar(head, a.k);
+        if (lane == 0) bars[wave] = mine;
+    }
+    __syncthreads();
+    u64 bar = 0;
+#pragma unroll
+    for (int j = 0; j < kWaves; ++j) bar = max64(bar, bars[j]);
     for (int i0 = wave * 64; i0 < n; i0 += kBeamPickThreads) {
         const u64 key = group_key(i0 + lane);
         append_keys(key, key >= bar, list, &counts[0], lane);

@@ -609,13 +609,20 @@ __global__ __launch_bounds__(kAssignThreads) void update_assign_kernel(UpdateArg
 constexpr int kFusedPages = 32768, kFusedLanes = kAssignThreads, kFusedEntries = 65536;
 __global__ __launch_bounds__(kAssignThreads) void update_fused_kernel(UpdateArgs a, int* slots) {
     extern __shared__ int refs[];  // [pages]
-    __shared__ int lasts[kFusedLanes];
+    __shared__ int lasts[kFusedLanes], parents[kFusedLanes], lens[kFusedLanes];
     __shared__ int lds[kAssignThreads / 64];
     constexpr int kBatch = 8;
     const int tid = threadIdx.x, i = tid;
     const bool lane = i < a.lanes_out;
     NewLane n = {-1, 0, 0, 0};
-    if (lane) n = new_lane(a, i);
+    if (lane) {
+        n = new_lane(a, i);
+        parents[i] = n.parent;
+        lens[i] = n.len;
+        lasts[i] = -1;
+        a.len_out[i] = n.len;
+    }
+    const int page_mask = (1 << a.c.log_page) - 1;
     for (int p0 = 0; p0 < a.c.pages; p0 += kBatch * kAssignThreads) {
         int v[kBatch];
 #pragma unroll
@@ -625,41 +632,29 @@ __global__ __launch_bounds__(kAssignThreads) void update_fused_kernel(UpdateArgs
             if (p0 + j * kAssignThreads + tid < a.c.pages) refs[p0 + j * kAssignThreads + tid] = v[j];
     }
     __syncthreads();
-    const int old = a.lanes_in * a.table_ld;
-    for (int e0 = 0; e0 < old; e0 += kBatch * kAssignThreads) {
-        int v[kBatch];
+    // Old entries give their references back, inherited ones take theirs.
+    const int old = a.lanes_in * a.table_ld, fresh = a.lanes_out * a.table_ld;
+    for (int e0 = 0; e0 < max(old, fresh); e0 += kBatch * kAssignThreads) {
+        int gone[kBatch], kept[kBatch], row[kBatch], col[kBatch];
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) v[j] = a.table_in[min(e0 + j * kAssignThreads + tid, old - 1)];
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j)
-            if (e0 + j * kAssignThreads + tid < old && is_page(a, v[j])) atomicSub(&refs[v[j]], 1);
-    }
-    // New rows, a wave each in turn.
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
-    for (int r = wave; r < a.lanes_out; r += kAssignThreads / 64) {
-        const NewLane m = new_lane(a, r);
-        const int* row = a.table_in + (long long)max(m.parent, 0) * a.table_ld;
-        int* out = a.table_out + (long long)r * a.table_ld;
-        int last = -1;
-        for (int j0 = 0; j0 < a.table_ld; j0 += kBatch * 64) {
-            int v[kBatch];
-#pragma unroll
-            for (int j = 0; j < kBatch; ++j) v[j] = row[min(j0 + 64 * j + l, a.table_ld - 1)];
-#pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
-                const int e = j0 + 64 * j + l;
-                if (e >= a.table_ld) continue;
-                const int id = e < m.held && is_page(a, v[j]) ? v[j] : -1;
-                out[e] = id;
-                if (id >= 0) atomicAdd(&refs[id], 1);
-                if (e == m.held - 1 && (m.len & ((1 << a.c.log_page) - 1))) last = id;
-            }
+        for (int j = 0; j < kBatch; ++j) {
+            const int e = e0 + j * kAssignThreads + tid;
+            gone[j] = a.table_in[min(e, old - 1)];
+            row[j] = (int)((unsigned)min(e, fresh - 1) / (unsigned)a.table_ld);
+            col[j] = min(e, fresh - 1) - row[j] * a.table_ld;
+            kept[j] = a.table_in[(long long)max(parents[row[j]], 0) * a.table_ld + col[j]];
         }
 #pragma unroll
-        for (int d = 1; d < 64; d <<= 1) last = max(last, __shfl_xor(last, d));
-        if (l == 0) {
-            lasts[r] = last;
-            a.len_out[r] = m.len;
+        for (int j = 0; j < kBatch; ++j) {
+            const int e = e0 + j * kAssignThreads + tid;
+            if (e < old && is_page(a, gone[j])) atomicSub(&refs[gone[j]], 1);
+            if (e < fresh) {
+                const int len = lens[row[j]], held = (len + page_mask) >> a.c.log_page;
+                const int id = col[j] < held && is_page(a, kept[j]) ? kept[j] : -1;
+                a.table_out[e] = id;
+                if (id >= 0) atomicAdd(&refs[id], 1);
+                if (col[j] == held - 1 && (len & page_mask)) lasts[row[j]] = id;
+            }
         }
     }
     __syncthreads();
