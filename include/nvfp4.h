@@ -444,8 +444,8 @@ int nvfp4_tree_mask(const int* parent, int n, uint64_t* mask, int* depth);
  *   lse[row][head] = log sum_p w_p   (if lse_dev is not NULL)
  * q head i uses kv head i / (q_heads / kv_heads).  A row that sees nothing gives
  * 0 and -inf.  q_dev: bf16 [rows][q_ld]; out_dev: bf16 [rows][out_ld]; lse_dev: fp32
- * [rows][q_heads].  max_rows (up to 64): an upper bound of a lane's rows; rows past it
- * are not computed.  Tokens past a lane's last row, and those in missing pages, may hold
+ * [rows][q_heads].  max_rows (up to 64): an upper bound of a lane's rows; rows past it,
+ * and lanes whose rows lie outside [0, rows), are not computed.  Tokens past a lane's last row, and those in missing pages, may hold
  * anything, NaN included; a drafted token that only some rows see must be
  * finite.  Products of bf16 (E4M3 is exact in it) are summed in fp32; the
  * weights enter the second product with 16 significant bits.  The split over
@@ -457,7 +457,7 @@ int nvfp4_tree_mask(const int* parent, int n, uint64_t* mask, int* depth);
  * aligned.  Asynchronous on `stream`. */
 size_t nvfp4_tree_attention_workspace_bytes(int q_heads, int kv_heads, int head_dim, int max_rows);
 int nvfp4_tree_attention(const nvfp4_cache* cache, int layer, const uint16_t* q_dev, int64_t q_ld,
-                         int q_heads, int lanes, int max_rows, const int* row_start_dev,
+                         int q_heads, int rows, int lanes, int max_rows, const int* row_start_dev,
                          const int* ctx_len_dev, const int* page_table_dev, int table_ld,
                          const uint64_t* mask_dev, float scale, uint16_t* out_dev, int64_t out_ld,
                          float* lse_dev, void* workspace_dev, size_t workspace_bytes, void* stream);

@@ -150,7 +150,7 @@ def lib():
         L.nvfp4_tree_mask.argtypes = [c.POINTER(i), i, c.POINTER(c.c_uint64), c.POINTER(i)]
         L.nvfp4_tree_attention_workspace_bytes.argtypes = [i, i, i, i]
         L.nvfp4_tree_attention_workspace_bytes.restype = sz
-        L.nvfp4_tree_attention.argtypes = [c.POINTER(Cache), i, vp, i64, i, i, i, vp, vp, vp, i,
+        L.nvfp4_tree_attention.argtypes = [c.POINTER(Cache), i, vp, i64, i, i, i, i, vp, vp, vp, i,
                                            vp, f, vp, i64, vp, vp, sz, vp]
         L.nvfp4_beam_workspace_bytes.argtypes = [i, i, i]
         L.nvfp4_beam_workspace_bytes.restype = sz
@@ -304,11 +304,11 @@ def nvfp4_tree_attention_workspace_bytes(q_heads, kv_heads, head_dim, max_rows) 
     return lib().nvfp4_tree_attention_workspace_bytes(q_heads, kv_heads, head_dim, max_rows)
 
 
-def nvfp4_tree_attention(cache, layer, q, q_ld, q_heads, lanes, max_rows, row_start, ctx_len,
+def nvfp4_tree_attention(cache, layer, q, q_ld, q_heads, rows, lanes, max_rows, row_start, ctx_len,
                          page_table, table_ld, mask, scale, out, out_ld, lse, workspace,
                          workspace_bytes, stream=None):
-    _check(lib().nvfp4_tree_attention(ctypes.byref(cache), layer, _ptr(q), q_ld, q_heads, lanes,
-                                      max_rows, _ptr(row_start), _ptr(ctx_len),
+    _check(lib().nvfp4_tree_attention(ctypes.byref(cache), layer, _ptr(q), q_ld, q_heads, rows,
+                                      lanes, max_rows, _ptr(row_start), _ptr(ctx_len),
                                       _ptr(page_table), table_ld, _ptr(mask), scale, _ptr(out),
                                       out_ld, _ptr(lse), _ptr(workspace), workspace_bytes,
                                       _stream(stream)))
@@ -626,7 +626,7 @@ class PagedCache:
             self._attend_ws[q_heads, max_rows] = wsb
         ws = q.new_empty(wsb // 2 + 8)
         st = L.nvfp4_tree_attention(self._ref, layer, q.data_ptr(), ld if rows > 1 else max(ld, width), q_heads,
-                                    lanes, max_rows, row_start.data_ptr(), ctx_len.data_ptr(),
+                                    rows, lanes, max_rows, row_start.data_ptr(), ctx_len.data_ptr(),
                                     page_table.data_ptr(), page_table.shape[1], mask.data_ptr(), scale,
                                     out.data_ptr(), out_ld, lse.data_ptr() if with_lse else None,
                                     ws.data_ptr(), wsb, _current(dev) if stream is None else _stream(stream))

@@ -55,7 +55,7 @@ struct AttArgs {
     const uint16_t* q;
     long long q_ld;
     int q_heads, group;  // group = q_heads / kv_heads
-    int lanes, max_rows;
+    int lanes, rows, max_rows;  // rows: of q and out; max_rows: of a lane
     const int* row_start;
     const int* ctx_len;
     const int* table;
@@ -82,6 +82,7 @@ __device__ __forceinline__ LaneWork lane_work(const AttArgs& a, int b, int block
     LaneWork w;
     w.row0 = a.row_start[b];
     w.rows = min(max(a.row_start[b + 1] - w.row0, 0), a.max_rows);
+    if (w.row0 < 0 || w.row0 > a.rows - w.rows) w.rows = 0;  // rows that do not exist
     w.ctx = max(a.ctx_len[b], 0);
     w.tokens = (int)min((long long)w.ctx + w.rows, (long long)a.table_ld << a.c.log_page);
     w.blocks = (w.rows * a.group + block_rows - 1) / block_rows;
@@ -894,7 +895,7 @@ int nvfp4_tree_mask(const int* parent, int n, uint64_t* mask, int* depth) {
 }
 
 int nvfp4_tree_attention(const nvfp4_cache* cache, int layer, const uint16_t* q_dev, int64_t q_ld,
-                         int q_heads, int lanes, int max_rows, const int* row_start_dev,
+                         int q_heads, int rows, int lanes, int max_rows, const int* row_start_dev,
                          const int* ctx_len_dev, const int* page_table_dev, int table_ld,
                          const uint64_t* mask_dev, float scale, uint16_t* out_dev, int64_t out_ld,
                          float* lse_dev, void* workspace_dev, size_t workspace_bytes, void* stream) {
@@ -906,6 +907,7 @@ int nvfp4_tree_attention(const nvfp4_cache* cache, int layer, const uint16_t* q_
     const int dim = a.c.dim, kv = a.c.kv_heads;
     if (q_heads < kv || q_heads % kv || q_heads > 65536)
         return set_error(NVFP4_EINVAL, "q_heads: %d is not a multiple of kv_heads %d up to 65536", q_heads, kv);
+    if (rows < 0 || rows > (1 << 24)) return set_error(NVFP4_EINVAL, "rows: %d outside [0, 2^24]", rows);
     if (max_rows < 1 || max_rows > NVFP4_TREE_MAX_ROWS)
         return set_error(NVFP4_EINVAL, "max_rows: %d outside [1, %d]", max_rows, NVFP4_TREE_MAX_ROWS);
     if ((st = check_lanes(a.c, lanes, page_table_dev, table_ld))) return st;
@@ -929,11 +931,13 @@ int nvfp4_tree_attention(const nvfp4_cache* cache, int layer, const uint16_t* q_
         return set_error(NVFP4_EUNSUPPORTED, "lanes: %d lanes of %d kv heads, %d row blocks and %d pages exceed 2^31 tiles", lanes, kv, blocks, table_ld);
     if ((long long)kv * blocks > 65535)
         return set_error(NVFP4_EUNSUPPORTED, "q_heads: %d kv heads of %d row blocks exceed 65535", kv, blocks);
+    if (rows == 0) return NVFP4_OK;
     a.q = q_dev;
     a.q_ld = q_ld;
     a.q_heads = q_heads;
     a.group = q_heads / kv;
     a.lanes = lanes;
+    a.rows = rows;
     a.max_rows = max_rows;
     a.row_start = row_start_dev;
     a.ctx_len = ctx_len_dev;

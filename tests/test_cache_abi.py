@@ -41,7 +41,7 @@ BAD_CACHES = [(dict(layers=0), "cache.layers", 1), (dict(pages=0), "cache.pages"
 
 
 def _attend(nv, c, **kw):
-    d = dict(layer=0, q=P, q_ld=1024, q_heads=8, lanes=2, max_rows=8, row_start=P, ctx_len=P, page_table=P, table_ld=4, mask=P,
+    d = dict(layer=0, q=P, q_ld=1024, q_heads=8, rows=8, lanes=2, max_rows=8, row_start=P, ctx_len=P, page_table=P, table_ld=4, mask=P,
              scale=0.1, out=P, out_ld=1024, lse=None, workspace=P, workspace_bytes=1 << 40)
     d.update(kw)
     return nv.nvfp4_tree_attention(c, *d.values(), stream=0)
@@ -82,7 +82,7 @@ def test_null_cache(nv):
 
 @pytest.mark.parametrize("bad,word", [
     (dict(layer=2), "layer"), (dict(layer=-1), "layer"), (dict(q_heads=6), "q_heads"), (dict(q_heads=0), "q_heads"), (dict(max_rows=0), "max_rows"),
-    (dict(max_rows=65), "max_rows"), (dict(lanes=0), "lanes"), (dict(lanes=70000), "lanes"), (dict(table_ld=0), "table_ld"),
+    (dict(max_rows=65), "max_rows"), (dict(rows=-1), "rows"), (dict(rows=1 << 25), "rows"), (dict(lanes=0), "lanes"), (dict(lanes=70000), "lanes"), (dict(table_ld=0), "table_ld"),
     (dict(table_ld=1 << 25), "table_ld"), (dict(page_table=None), "page_table"), (dict(page_table=P + 2), "page_table"),
     (dict(q_ld=1016), "q_ld"), (dict(q_ld=1028), "q_ld"), (dict(out_ld=1022), "out_ld"), (dict(out_ld=1026), "out_ld"),
     (dict(q=None), "q"), (dict(q=P + 8), "q"), (dict(out=P + 4), "out"), (dict(out=None), "out"), (dict(row_start=None), "row_start"),

@@ -229,3 +229,19 @@ def test_rows_past_max_rows_are_left(nv):
     out = torch.full((6, 64), 5.0, dtype=torch.bfloat16, device="cuda")
     nv.PagedCache(k, v).attend(0, q, start, ctx, table, masks, 4, 0.1, out=out)
     assert (out[4:] == 5.0).all() and not (out[:4] == 5.0).all(1).any()
+
+
+def test_lanes_outside_the_rows_are_left(nv):
+    """Lanes whose rows start or end outside the call's rows are not computed; the others are."""
+    import torch
+    lanes = Lanes(15, [40, 20, 30], [2, 2, 2], 16)
+    k, v = cache_tensors(5, 1, lanes.pages, 1, 16, 64, "bf16")
+    _, ctx, table = lanes.dev()
+    q = _queries(4, 4, 64)
+    cache, masks = nv.PagedCache(k, v), dev(chain(2).repeat(2).reshape(2, 2).T.copy().ravel())
+    out = torch.full((4, 64), 5.0, dtype=torch.bfloat16, device="cuda")
+    cache.attend(0, q, dev(np.array([0, 2, 4, 6], np.int32)), ctx, table, masks, 2, 0.1, out=out)
+    assert not (out == 5.0).all(1).any()  # the third lane's rows 4 and 5 do not exist
+    out.fill_(5.0)
+    cache.attend(0, q, dev(np.array([-2, 0, 2, 9], np.int32)), ctx, table, masks, 2, 0.1, out=out)
+    assert not (out[:2] == 5.0).all(1).any() and not (out[2:4] == 5.0).all(1).any()
