@@ -24,10 +24,19 @@
 //    multiplication by it.
 //
 // Staging.  A workgroup's four waves copy a tile's K and V straight into LDS
-// (wave w the w-th 16 tokens: one run of 16 x dim values of each), the next
-// step's copies in flight while the current step is computed.  K segments of 16
+// (wave w the w-th 16 tokens: one run of 16 x dim values of each), the copies of
+// the next step, or of the next three, in flight while a step is computed.  K segments of 16
 // bytes sit in slots xor-ed with their token, and V segments with their dim, so
 // that the operand reads spread over the banks.
+//
+// Measured (12 rows of dim 128 a kv head, 4 kv heads, times with the joining
+// kernel): 8 lanes of up to 40960 tokens, bf16, 451 MB: 80.5 us, 5.6 TB/s (copies
+// alone, nothing computed: 79); 8 of up to 4096, 45 MB: 18.8 us, of which about 10
+// are launches and loads that wait for each other.  64 drafted tokens a lane (768
+// rows a head), 4 lanes of up to 16384: 131 us, 555 TFLOP/s of the formula's
+// arithmetic, 830 of what the matrix units do (weights enter the second product as
+// two bf16 numbers), against 1250 of a large product: bound by the vector work of
+// the softmax beside the matrix instructions, 2.9 for each.
 #include <type_traits>
 
 #include "cache.h"
@@ -45,10 +54,17 @@ constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kRescaleAt = 8.f;
 // Fewest tiles a worker takes where there are more workers than items: below,
 // storing and joining partial results costs more than the shorter walk saves
-// (8 lanes of 4096 tokens and 12 rows: 21.3 us with 2 or 4 tiles, 19.5 with 8).
-constexpr int kMinTiles = 8;
+// (8 lanes of 4096 tokens and 12 rows: 19.1 us with 5 tiles, 19.6 with 8).
+constexpr int kMinTiles = 5;
 // Items of at most so many tiles are never shared, and no joining kernel runs.
 constexpr int kWholeTiles = 8;
+constexpr int kNoPieces = 1 << 28;  // a piece that holds any item
+// Pieces may be so many tiles longer than an equal share.  A worker whose share goes
+// over an item's end reads the new item's lengths, page numbers and rows before its
+// first tile (3 to 4 us, the time of 5 tiles of few rows), and one such worker holds
+// up the call: 8 lanes of 4096 tokens 18.8 us in pieces, 21.2 in equal shares; one
+// lane of 40960 24.4 against 27.0; 4 lanes of 768 rows and 16384 tokens 131 and 132.
+constexpr int kMoreTiles = 6;
 
 struct AttArgs {
     CacheView c;  // base pointers of the layer
@@ -72,10 +88,9 @@ struct AttArgs {
     int stream;  // K and V are read with the streaming hint
 };
 
-// One lane's share of the work: `units` items (kv head x row block) of `tiles`.
+// One lane's share of the work: items (kv head x row block) of `tiles`.
 struct LaneWork {
     int row0, rows, ctx, tokens, blocks, tiles;
-    int parts;  // tiles that can be shared out apart: all, or 1
 };
 
 __device__ __forceinline__ LaneWork lane_work(const AttArgs& a, int b, int block_rows) {
@@ -87,7 +102,6 @@ __device__ __forceinline__ LaneWork lane_work(const AttArgs& a, int b, int block
     w.tokens = (int)min((long long)w.ctx + w.rows, (long long)a.table_ld << a.c.log_page);
     w.blocks = (w.rows * a.group + block_rows - 1) / block_rows;
     w.tiles = w.rows > 0 ? (w.tokens + kTile - 1) / kTile : 0;
-    w.parts = a.whole ? min(w.tiles, 1) : w.tiles;
     return w;
 }
 
@@ -106,20 +120,25 @@ __device__ __forceinline__ int wave_scan(int v) {
     return dpp_add<0x143, 0xC>(v);  // row_bcast 31 into rows 2 and 3
 }
 
-// Items of a lane's work, and all of their parts.
+// Items of a lane's work.
 __device__ __forceinline__ int lane_items(const AttArgs& a, const LaneWork& w) {
     return w.tiles > 0 ? w.blocks * a.c.kv_heads : 0;
 }
-__device__ __forceinline__ int lane_parts(const AttArgs& a, const LaneWork& w) { return lane_items(a, w) * w.parts; }
 
-// Equal shares: worker r < active takes parts [begin(r), begin(r + 1)).
+// How the tiles are shared out.  An item has parts(tiles) parts: its tiles
+// (piece 0), or pieces of at most `piece` tiles.  Worker r < active takes parts
+// [begin(r), begin(r + 1)) of all: an equal number of tiles, over the items' ends,
+// or a piece (several only where items are whole).
 struct Shares {
-    int active, each, rem;
+    int active, each, rem, piece;
+    __device__ __forceinline__ int parts(int tiles) const {
+        return piece ? (int)((unsigned)(tiles + piece - 1) / (unsigned)piece) : tiles;
+    }
     __device__ __forceinline__ int begin(int r) const { return r * each + min(r, rem); }
-    __device__ __forceinline__ int owner(int tile) const {
+    __device__ __forceinline__ int owner(int part) const {
         const int wide = rem * (each + 1);
-        return tile < wide ? (int)((unsigned)tile / (unsigned)(each + 1))
-                           : rem + (int)((unsigned)(tile - wide) / (unsigned)each);
+        return part < wide ? (int)((unsigned)part / (unsigned)(each + 1))
+                           : rem + (int)((unsigned)(part - wide) / (unsigned)each);
     }
 };
 
@@ -128,19 +147,46 @@ struct Shares {
 // parts of lanes 0 .. l, for the first 64.
 __device__ __forceinline__ Shares shares_of(const AttArgs& a, int block_rows, LaneWork& first, int& upto) {
     const int l = threadIdx.x & 63;
-    first = LaneWork{0, 0, 0, 0, 0, 0, 0};
+    first = LaneWork{0, 0, 0, 0, 0, 0};
     if (l < a.lanes) first = lane_work(a, l, block_rows);
-    upto = wave_scan(lane_parts(a, first));
-    int total = __builtin_amdgcn_readlane(upto, 63);
-    int items = __builtin_amdgcn_readlane(wave_scan(lane_items(a, first)), 63);
-    for (int b0 = 64; b0 < a.lanes; b0 += 64) {
-        LaneWork w = {0, 0, 0, 0, 0, 0, 0};
-        if (b0 + l < a.lanes) w = lane_work(a, b0 + l, block_rows);
-        total += __builtin_amdgcn_readlane(wave_scan(lane_parts(a, w)), 63);
-        items += __builtin_amdgcn_readlane(wave_scan(lane_items(a, w)), 63);
+    // Sum over all lanes of items x each(tiles).
+    auto sum = [&](auto&& each) {
+        upto = wave_scan(lane_items(a, first) * each(first.tiles));
+        int all = __builtin_amdgcn_readlane(upto, 63);
+        for (int b0 = 64; b0 < a.lanes; b0 += 64) {
+            LaneWork w = {0, 0, 0, 0, 0, 0};
+            if (b0 + l < a.lanes) w = lane_work(a, b0 + l, block_rows);
+            all += __builtin_amdgcn_readlane(wave_scan(lane_items(a, w) * each(w.tiles)), 63);
+        }
+        return all;
+    };
+    Shares s = {0, 0, 0, kNoPieces};
+    const int items = sum([](int) { return 1; });
+    int parts = items;
+    if (!a.whole) {
+        s.piece = 0;
+        const int total = sum([](int tiles) { return tiles; });
+        // Pieces that start and end with their item, if that many workers can take one
+        // each and the longest is not much longer than an equal share.  (An item's
+        // last piece is half a piece on average: the first length tried allows for it.)
+        if (items <= a.workers) {
+            const int most = max(kMinTiles, total / a.workers) + kMoreTiles;
+            int piece = max(kMinTiles, (int)((unsigned)total / (unsigned)(a.workers - items / 2)) + 1);
+            for (; piece <= most && !s.piece; ++piece) {
+                s.piece = piece;
+                parts = sum([&](int tiles) { return s.parts(tiles); });
+                if (parts > a.workers) s.piece = 0;
+            }
+        }
+        if (!s.piece) parts = sum([](int tiles) { return tiles; });
+        s.active = s.piece ? parts : min(a.workers, max(items, total / kMinTiles));
+    } else {
+        s.active = min(a.workers, items);
     }
-    const int active = max(1, min(a.workers, max(items, total / kMinTiles)));
-    return {active, (int)((unsigned)total / (unsigned)active), (int)((unsigned)total % (unsigned)active)};
+    s.active = max(s.active, 1);
+    s.each = (int)((unsigned)parts / (unsigned)s.active);
+    s.rem = (int)((unsigned)parts % (unsigned)s.active);
+    return s;
 }
 
 __device__ __forceinline__ bf16x8 bytes8(const uint4& v) {
@@ -210,23 +256,40 @@ struct AttTraits {
     // lanes of 16384 tokens of dim 256: 47 us against 55), or where LDS has room
     // for no more.
     static constexpr int kPerUnit = kRows <= kFewRows || kStepBytes > 32768 ? 1 : 2;
+    // Buffers: all but one in flight.  (8 lanes of 40960 tokens, 12 rows: 80.5 us with
+    // four, 87.5 with two; one of 40960: 24.4 and 26.1.)
+    static constexpr int NB = kPerUnit == 1 && kStepBytes <= 32768 ? 4 : 2;
+    static constexpr int kStepCopies = kStepBytes / kAttWaves / 1024;  // a wave's
 };
+
+// The kernel's arguments read anew where they are used: kept in registers from its
+// start they fill the scalar file, and what the tile loop needs spills (37 to 90
+// scalar registers; 14 to 45, none of them in the loop, with the arguments and the
+// copies' addresses formed where they are used).
+using ArgsRef = const __attribute__((address_space(4))) AttArgs&;
+__device__ __forceinline__ ArgsRef args_anew() {
+    auto at = (uintptr_t)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(at));
+    return *(const __attribute__((address_space(4))) AttArgs*)at;
+}
 
 template <int D, bool FP8, int NR, int RW, int TW, int DW, bool SPLIT>
 __global__ __launch_bounds__(kAttThreads, (AttTraits<D, FP8, NR, RW, TW, DW, SPLIT>::kPerUnit)) void attend_kernel(AttArgs a) {
     using T = AttTraits<D, FP8, NR, RW, TW, DW, SPLIT>;
-    constexpr int ES = T::ES, kRows = T::kRows, kSegs = T::kSegs, kChunk = T::kChunk, SUB = T::SUB;
+    constexpr int ES = T::ES, kRows = T::kRows, kSegs = T::kSegs, kChunk = T::kChunk, SUB = T::SUB, NB = T::NB;
     constexpr int KS = D / 32;       // K steps of 32 dims
     constexpr int DB = D / 16 / DW;  // this wave's dim blocks of O
     constexpr int HH = 2 / TW;       // token halves a wave takes
     constexpr int KL = FP8 ? KS / 2 : KS;  // 16-byte reads of a token's K
     using VRaw = typename std::conditional<FP8, uint2, uint4>::type;  // 8 tokens of V
     constexpr int KA = kSegs >= 16 ? 4 : kSegs / 4;  // distinct K operand addresses
-    // Two arrays, so that the compiler can tell the copies in flight from the
-    // reads of the other one.
+    // Arrays of their own, so that the compiler can tell the copies in flight from
+    // the reads of another one.
     __shared__ __align__(16) uint8_t lds0[T::kStepBytes];
     __shared__ __align__(16) uint8_t lds1[T::kStepBytes];
-    __shared__ int lds_page[2][SUB][4];  // page of each 16-token chunk of a step, -1: none
+    __shared__ __align__(16) uint8_t lds2[NB == 4 ? T::kStepBytes : 16];
+    __shared__ __align__(16) uint8_t lds3[NB == 4 ? T::kStepBytes : 16];
+    __shared__ int lds_page[NB][SUB][4];  // page of each 16-token chunk of a step, -1: none
     __shared__ float2 lds_ml[TW > 1 ? kRows : 1];
     static_assert(TW == 1 || (RW <= 2 && NR * 16 * D * 4 <= T::kStepBytes), "sums of a row wave fit");
 
@@ -242,23 +305,27 @@ __global__ __launch_bounds__(kAttThreads, (AttTraits<D, FP8, NR, RW, TW, DW, SPL
     int worker = blockIdx.x;
     // Consecutive ranges on one XCD (workgroup b runs on XCD b mod 8), so that
     // the row blocks of one lane and head share their K and V in its L2.
-    if (share.active == a.workers && a.workers % 8 == 0) worker = (worker & 7) * (a.workers >> 3) + (worker >> 3);
+    if (a.workers % 8 == 0) {
+        const int each = (share.active + 7) >> 3;
+        if (worker >> 3 >= each) return;
+        worker = (worker & 7) * each + (worker >> 3);
+    }
     if (worker >= share.active) return;
     int at = share.begin(worker);
     const int end = share.begin(worker + 1);
     if (at >= end) return;
 
-    // The lane, item and tile that `at` falls on.
-    int b, before;
+    // The lane, item and part that `at` falls on.
+    int b, parts, item, part;
     {
         int b0 = 0, upto = first_upto, base = 0;
         unsigned long long past = __ballot(upto > at);
         while (!past) {
             base += __builtin_amdgcn_readlane(upto, 63);
             b0 += 64;
-            w = LaneWork{0, 0, 0, 0, 0, 0, 0};
+            w = LaneWork{0, 0, 0, 0, 0, 0};
             if (b0 + lane < a.lanes) w = lane_work(a, b0 + lane, kRows);
-            upto = wave_scan(lane_parts(a, w));
+            upto = wave_scan(lane_items(a, w) * share.parts(w.tiles));
             past = __ballot(base + upto > at);
         }
         const int first = __ffsll(past) - 1;
@@ -268,12 +335,12 @@ __global__ __launch_bounds__(kAttThreads, (AttTraits<D, FP8, NR, RW, TW, DW, SPL
         w.tokens = __builtin_amdgcn_readlane(w.tokens, first);
         w.blocks = __builtin_amdgcn_readlane(w.blocks, first);
         w.tiles = __builtin_amdgcn_readlane(w.tiles, first);
-        w.parts = a.whole ? 1 : w.tiles;
         b = b0 + first;
-        before = base + __builtin_amdgcn_readlane(upto, first) - lane_parts(a, w);
+        parts = share.parts(w.tiles);
+        const int left = at - (base + __builtin_amdgcn_readlane(upto, first) - lane_items(a, w) * parts);
+        item = (int)((unsigned)left / (unsigned)parts);
+        part = left - item * parts;
     }
-    int item = (int)((unsigned)(at - before) / (unsigned)w.parts);
-    int t0 = at - before - item * w.parts;
 
     const int page_mask = (1 << a.c.log_page) - 1;
     const long long head_bytes = (long long)T::kRowBytes << a.c.log_page;
@@ -301,7 +368,13 @@ __global__ __launch_bounds__(kAttThreads, (AttTraits<D, FP8, NR, RW, TW, DW, SPL
     const int v_flip = FP8 ? 0 : ((n >> 2) & 1);
 
     while (at < end) {
-        const int t1 = a.whole ? w.tiles : min(w.tiles, t0 + (end - at));
+        // Tiles [t0, t1): a piece (the item's are equal to one tile), or what is left.
+        int t0 = part, t1 = min(w.tiles, t0 + (end - at));
+        if (share.piece) {
+            const int each = (int)((unsigned)w.tiles / (unsigned)parts), rem = w.tiles - each * parts;
+            t0 = part * each + min(part, rem);
+            t1 = t0 + each + (part < rem ? 1 : 0);
+        }
         const int h = (int)((unsigned)item / (unsigned)w.blocks), rb = item - h * w.blocks;
         const int rows = w.rows * a.group;  // rows of the item's lane and head
         // (constant address space: scalar loads, which wait apart from the copies)
@@ -321,13 +394,17 @@ __global__ __launch_bounds__(kAttThreads, (AttTraits<D, FP8, NR, RW, TW, DW, SPL
         // masked); past the range the copies read nothing (zero records).
         auto issue = [&](int t, const int (&id)[SUB], uint8_t* buf, int (*pages)[4]) {
             const int records = t < t1 ? kChunk : 0;
+            // (formed anew in each step: the addresses of all copies of all steps, kept,
+            // are more than the scalar file holds)
+            int mine_at = wave * kChunk;
+            asm volatile("" : "+s"(mine_at));
 #pragma unroll
             for (int u = 0; u < SUB; ++u) {
                 const int mine = id[u];
                 if (lane == 0) pages[u][wave] = good(mine) ? mine : -1;
                 const int tok = min((t + u) * kTile + 16 * wave, (w.tokens - 1) & ~15) & page_mask;
                 const long long off = (long long)(good(mine) ? mine : 0) * a.c.page_stride + (long long)tok * T::kRowBytes;
-                uint8_t* kd = buf + u * T::kTileBytes + wave * kChunk;
+                uint8_t* kd = buf + u * T::kTileBytes + mine_at;
                 if (a.stream) {
 #pragma unroll
                     for (int c = 0; c < T::kCopies; ++c)
@@ -346,29 +423,35 @@ __global__ __launch_bounds__(kAttThreads, (AttTraits<D, FP8, NR, RW, TW, DW, SPL
             }
         };
 
-        int ids[SUB], next_ids[SUB];
-        load_ids(t0, ids);
-        load_ids(t0 + SUB, next_ids);
-        issue(t0, ids, lds0, lds_page[0]);
-        // Q operand: row n of each row tile, 8 dims per step.
+        int ids[NB - 1][SUB], next_ids[SUB];
+#pragma unroll
+        for (int u = 0; u < NB - 1; ++u) load_ids(t0 + u * SUB, ids[u]);
+        load_ids(t0 + (NB - 1) * SUB, next_ids);
+        // Q operand: row n of each row tile, 8 dims per step (past the last row:
+        // row 0's, whose results are not kept).  It is read ahead of the copies: they
+        // end in order, and its first use waits for none of them.
         bf16x8 qf[NR][KS];
         unsigned long long mask[NR];
+        ArgsRef aq = args_anew();
+        const int group = aq.group;
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
             const int row = rb * kRows + (rw * NR + r) * 16 + n;
-            const bool real = row < rows;
-            const int t = real ? (int)((unsigned)row / (unsigned)a.group) : 0;
-            const int head = h * a.group + (real ? row - t * a.group : 0);
-            const uint16_t* src = a.q + (long long)(w.row0 + t) * a.q_ld + (long long)head * D;
-            mask[r] = real ? a.mask[w.row0 + t] : 0ull;
+            const int t = row < rows ? (int)((unsigned)row / (unsigned)group) : 0;
+            const int head = h * group + (row < rows ? row - t * group : 0);
+            const uint16_t* src = aq.q + (long long)(w.row0 + t) * aq.q_ld + (long long)head * D;
+            mask[r] = aq.mask[w.row0 + t];
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
                 // fp8: 16 bytes hold 16 dims of a token, two steps' slots
                 const int d = FP8 ? 64 * (s >> 1) + 16 * g + 8 * (s & 1) : 32 * s + 8 * g;
-                uint4 v = *(const uint4*)(src + d);
-                if (!real) v = make_uint4(0, 0, 0, 0);
-                qf[r][s] = bytes8(v);
+                qf[r][s] = bytes8(*(const uint4*)(src + d));
             }
+        }
+        issue(t0, ids[0], lds0, lds_page[0]);
+        if constexpr (NB == 4) {
+            issue(t0 + SUB, ids[1], lds1, lds_page[1]);
+            issue(t0 + 2 * SUB, ids[2], lds2, lds_page[2]);
         }
         f32x4 o[NR][DB];
         float m[NR], mu[NR], l[NR];  // maximum, the one in use (0 for -inf), sum
@@ -580,15 +663,15 @@ __global__ __launch_bounds__(kAttThreads, (AttTraits<D, FP8, NR, RW, TW, DW, SPL
                 *p = keep_first(*p, (keep - first) * ES);
             }
         };
-        // One step: its copies have landed, the next step's are issued, and it
-        // is computed.  The barrier also ends every wave's reads of the other
-        // buffer.
+        // One step: its copies have landed, those into the buffer of the step before
+        // are issued, and it is computed.  The barrier also ends every wave's reads of
+        // that buffer.
         auto step = [&](int t, uint8_t* buf, int (*pages)[4], uint8_t* other, int (*other_pages)[4]) {
-            __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+            __builtin_amdgcn_s_waitcnt(vmcnt_imm((NB - 2) * T::kStepCopies));
             __builtin_amdgcn_s_waitcnt(kLgkmcnt0);
             barrier_nofence();
-            issue(t + SUB, next_ids, other, other_pages);
-            load_ids(t + 2 * SUB, next_ids);
+            issue(t + (NB - 1) * SUB, next_ids, other, other_pages);
+            load_ids(t + NB * SUB, next_ids);
             int page[SUB];  // of this lane's chunk, g
             bool missing = (t + SUB) * kTile > w.tokens;
 #pragma unroll
@@ -606,9 +689,16 @@ __global__ __launch_bounds__(kAttThreads, (AttTraits<D, FP8, NR, RW, TW, DW, SPL
             for (int u = 0; u < SUB; ++u)
                 if (t + u < t1) tile(t + u, page[u], buf, u * T::kTileBytes);
         };
-        for (int t = t0; t < t1; t += 2 * SUB) {
-            step(t, lds0, lds_page[0], lds1, lds_page[1]);
-            if (t + SUB < t1) step(t + SUB, lds1, lds_page[1], lds0, lds_page[0]);
+        for (int t = t0; t < t1; t += NB * SUB) {
+            if constexpr (NB == 4) {
+                step(t, lds0, lds_page[0], lds3, lds_page[3]);
+                if (t + SUB < t1) step(t + SUB, lds1, lds_page[1], lds0, lds_page[0]);
+                if (t + 2 * SUB < t1) step(t + 2 * SUB, lds2, lds_page[2], lds1, lds_page[1]);
+                if (t + 3 * SUB < t1) step(t + 3 * SUB, lds3, lds_page[3], lds2, lds_page[2]);
+            } else {
+                step(t, lds0, lds_page[0], lds1, lds_page[1]);
+                if (t + SUB < t1) step(t + SUB, lds1, lds_page[1], lds0, lds_page[0]);
+            }
         }
 
         // Sums over the four token groups of a row.
@@ -655,6 +745,8 @@ __global__ __launch_bounds__(kAttThreads, (AttTraits<D, FP8, NR, RW, TW, DW, SPL
         }
         const bool whole = t0 == 0 && t1 == w.tiles;
         if (tw == 0) {
+            ArgsRef ae = args_anew();
+            const int group = ae.group;
             const int slot = 2 * worker + (t0 > 0 ? 0 : 1);
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
@@ -662,31 +754,34 @@ __global__ __launch_bounds__(kAttThreads, (AttTraits<D, FP8, NR, RW, TW, DW, SPL
                 const int row = rb * kRows + in_block;
                 if (row >= rows) continue;
                 if (whole) {
-                    const int tt = (int)((unsigned)row / (unsigned)a.group), head = h * a.group + row - tt * a.group;
-                    const float inv = l[r] > 0.f ? a.c.v_scale / l[r] : 0.f;
-                    uint16_t* dst = a.out + (long long)(w.row0 + tt) * a.out_ld + (long long)head * D + 16 * dw * DB;
+                    const int tt = (int)((unsigned)row / (unsigned)group), head = h * group + row - tt * group;
+                    const float inv = l[r] > 0.f ? ae.c.v_scale / l[r] : 0.f;
+                    uint16_t* dst = ae.out + (long long)(w.row0 + tt) * ae.out_ld + (long long)head * D + 16 * dw * DB;
 #pragma unroll
                     for (int db = 0; db < DB; ++db)
                         *(uint2*)(dst + 16 * db + 4 * g) = bf16x4(o[r][db][0] * inv, o[r][db][1] * inv, o[r][db][2] * inv, o[r][db][3] * inv);
-                    if (a.lse && g == 0 && dw == 0)
-                        a.lse[(long long)(w.row0 + tt) * a.q_heads + head] = l[r] > 0.f ? (m[r] + log2f(l[r])) * kLn2 : -__builtin_inff();
+                    if (ae.lse && g == 0 && dw == 0)
+                        ae.lse[(long long)(w.row0 + tt) * ae.q_heads + head] = l[r] > 0.f ? (m[r] + log2f(l[r])) * kLn2 : -__builtin_inff();
                 } else {
-                    float* dst = a.part_o + ((long long)slot * kRows + in_block) * D + 16 * dw * DB;
+                    float* dst = ae.part_o + ((long long)slot * kRows + in_block) * D + 16 * dw * DB;
 #pragma unroll
                     for (int db = 0; db < DB; ++db) *(f32x4*)(dst + 16 * db + 4 * g) = o[r][db];
-                    if (g == 0 && dw == 0) a.part_ml[(long long)slot * kRows + in_block] = make_float2(m[r], l[r]);
+                    if (g == 0 && dw == 0) ae.part_ml[(long long)slot * kRows + in_block] = make_float2(m[r], l[r]);
                 }
             }
         }
         // Next item.
-        at += a.whole ? 1 : t1 - t0;
-        t0 = 0;
-        if (at < end) {
+        const int done = share.piece ? 1 : t1 - t0;
+        at += done;
+        part += done;
+        if (at < end && part == parts) {
+            part = 0;
             if (++item == w.blocks * a.c.kv_heads) {
                 item = 0;
                 do {
                     w = lane_work(a, ++b, kRows);
                 } while (w.tiles == 0);
+                parts = share.parts(w.tiles);
             }
         }
     }
@@ -711,21 +806,23 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttArgs a, int block_r
     const Shares share = shares_of(a, block_rows, w, upto);
     int before = 0;  // parts of the lanes before b
     if (b < 64) {
-        before = __builtin_amdgcn_readlane(upto, b) - __builtin_amdgcn_readlane(lane_parts(a, w), b);
+        before = b > 0 ? __builtin_amdgcn_readlane(upto, b - 1) : 0;
         w.row0 = __builtin_amdgcn_readlane(w.row0, b);
         w.rows = __builtin_amdgcn_readlane(w.rows, b);
         w.blocks = __builtin_amdgcn_readlane(w.blocks, b);
         w.tiles = __builtin_amdgcn_readlane(w.tiles, b);
     } else {
         for (int b0 = 0; b0 < b; b0 += 64) {
-            const int v = b0 + lane < b ? lane_parts(a, lane_work(a, b0 + lane, block_rows)) : 0;
-            before += __builtin_amdgcn_readlane(wave_scan(v), 63);
+            LaneWork o = {0, 0, 0, 0, 0, 0};
+            if (b0 + lane < b) o = lane_work(a, b0 + lane, block_rows);
+            before += __builtin_amdgcn_readlane(wave_scan(lane_items(a, o) * share.parts(o.tiles)), 63);
         }
         w = lane_work(a, b, block_rows);
     }
     if (rb >= w.blocks || row >= w.rows * a.group || in_block >= block_rows || w.tiles == 0) return;  // whole wave (WIDE: block)
-    const int start = before + (h * w.blocks + rb) * w.tiles;  // the item's first tile
-    const int r0 = share.owner(start), r1 = share.owner(start + w.tiles - 1);
+    const int parts = share.parts(w.tiles);
+    const int start = before + (h * w.blocks + rb) * parts;  // the item's first part
+    const int r0 = share.owner(start), r1 = share.owner(start + parts - 1);
     if (r0 == r1) return;
     auto slot = [&](int r) { return (long long)(2 * r + (r > r0 ? 0 : 1)) * block_rows + in_block; };
     float mx = -__builtin_inff(), sum = 0.f;
