@@ -30,8 +30,8 @@
 // that the operand reads spread over the banks.
 //
 // Measured (12 rows of dim 128 a kv head, 4 kv heads, times with the joining
-// kernel): 8 lanes of up to 40960 tokens, bf16, 451 MB: 80.5 us, 5.6 TB/s (copies
-// alone, nothing computed: 79); 8 of up to 4096, 45 MB: 18.8 us, of which about 10
+// kernel): 8 lanes of up to 40960 tokens, bf16, 451 MB: 79.5 us, 5.7 TB/s (copies
+// alone, nothing computed: 79); 8 of up to 4096, 45 MB: 18.3 us, of which about 10
 // are launches and loads that wait for each other.  64 drafted tokens a lane (768
 // rows a head), 4 lanes of up to 16384: 131 us, 555 TFLOP/s of the formula's
 // arithmetic, 830 of what the matrix units do (weights enter the second product as
@@ -66,6 +66,23 @@ constexpr int kNoPieces = 1 << 28;  // a piece that holds any item
 // lane of 40960 24.4 against 27.0; 4 lanes of 768 rows and 16384 tokens 131 and 132.
 constexpr int kMoreTiles = 6;
 
+// How the tiles are shared out.  An item has parts(tiles) parts: its tiles
+// (piece 0), or pieces of at most `piece` tiles.  Worker r < active takes parts
+// [begin(r), begin(r + 1)) of all: an equal number of tiles, over the items' ends,
+// or a piece (several only where items are whole).
+struct Shares {
+    int active, each, rem, piece;
+    __device__ __forceinline__ int parts(int tiles) const {
+        return piece ? (int)((unsigned)(tiles + piece - 1) / (unsigned)piece) : tiles;
+    }
+    __device__ __forceinline__ int begin(int r) const { return r * each + min(r, rem); }
+    __device__ __forceinline__ int owner(int part) const {
+        const int wide = rem * (each + 1);
+        return part < wide ? (int)((unsigned)part / (unsigned)(each + 1))
+                           : rem + (int)((unsigned)(part - wide) / (unsigned)each);
+    }
+};
+
 struct AttArgs {
     CacheView c;  // base pointers of the layer
     const uint16_t* q;
@@ -81,6 +98,7 @@ struct AttArgs {
     uint16_t* out;
     long long out_ld;
     float* lse;  // [rows][q_heads] or null
+    Shares* shares;   // for the joining kernel
     float2* part_ml;  // [2 x workers][block rows]: maximum (log2 units), sum
     float* part_o;    // [2 x workers][block rows][dim]
     int workers;
@@ -124,23 +142,6 @@ __device__ __forceinline__ int wave_scan(int v) {
 __device__ __forceinline__ int lane_items(const AttArgs& a, const LaneWork& w) {
     return w.tiles > 0 ? w.blocks * a.c.kv_heads : 0;
 }
-
-// How the tiles are shared out.  An item has parts(tiles) parts: its tiles
-// (piece 0), or pieces of at most `piece` tiles.  Worker r < active takes parts
-// [begin(r), begin(r + 1)) of all: an equal number of tiles, over the items' ends,
-// or a piece (several only where items are whole).
-struct Shares {
-    int active, each, rem, piece;
-    __device__ __forceinline__ int parts(int tiles) const {
-        return piece ? (int)((unsigned)(tiles + piece - 1) / (unsigned)piece) : tiles;
-    }
-    __device__ __forceinline__ int begin(int r) const { return r * each + min(r, rem); }
-    __device__ __forceinline__ int owner(int part) const {
-        const int wide = rem * (each + 1);
-        return part < wide ? (int)((unsigned)part / (unsigned)(each + 1))
-                           : rem + (int)((unsigned)(part - wide) / (unsigned)each);
-    }
-};
 
 // The shares, worked out by a wave: its lane l looks at lanes l, l + 64, ... of
 // the call.  first, upto: lane l's own work (none past the last) and the sum of
@@ -302,6 +303,7 @@ __global__ __launch_bounds__(kAttThreads, (AttTraits<D, FP8, NR, RW, TW, DW, SPL
     LaneWork w;
     int first_upto;
     const Shares share = shares_of(a, kRows, w, first_upto);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.shares = share;
     int worker = blockIdx.x;
     // Consecutive ranges on one XCD (workgroup b runs on XCD b mod 8), so that
     // the row blocks of one lane and head share their K and V in its L2.
@@ -788,9 +790,10 @@ __global__ __launch_bounds__(kAttThreads, (AttTraits<D, FP8, NR, RW, TW, DW, SPL
 }
 
 // Joins the partial results of items that several workers shared.  A row is taken
-// by one wave, or by the block's four (WIDE) where it can have more contributors
-// than kFan; a wave loads kFan of them at once.  The order of the sums is that of
-// the workers.
+// by one wave, or by the block's four (WIDE); a wave loads kFan of its contributors
+// at once.  The order of the sums is that of the workers.  Bound by the chain launch,
+// shares and lengths, partial results (4.3 us for 8 lanes of one token), or by the bytes
+// of the partial results (8 x 8 rows over 512 workers: 24 MB, 12 us).
 constexpr int kFan = 16;
 template <int D, bool WIDE>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttArgs a, int block_rows, int max_blocks) {
@@ -801,11 +804,12 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttArgs a, int block_r
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), lane = threadIdx.x & 63;
     const int b = blockIdx.z, h = (int)(blockIdx.y / (unsigned)max_blocks), rb = blockIdx.y - h * max_blocks;
     const int in_block = WIDE ? blockIdx.x : blockIdx.x * 4 + wave, row = rb * block_rows + in_block;
-    LaneWork w;
-    int upto;
-    const Shares share = shares_of(a, block_rows, w, upto);
+    const Shares share = *a.shares;
+    LaneWork w = {0, 0, 0, 0, 0, 0};
     int before = 0;  // parts of the lanes before b
     if (b < 64) {
+        if (lane <= b) w = lane_work(a, lane, block_rows);
+        const int upto = wave_scan(lane_items(a, w) * share.parts(w.tiles));
         before = b > 0 ? __builtin_amdgcn_readlane(upto, b - 1) : 0;
         w.row0 = __builtin_amdgcn_readlane(w.row0, b);
         w.rows = __builtin_amdgcn_readlane(w.rows, b);
@@ -942,11 +946,12 @@ int launch_attend(const AttShape& sh, const AttArgs& a, bool joins, hipStream_t 
     if (!joins) return NVFP4_OK;
     const int rows = a.max_rows * a.group, br = sh.block_rows();
     const int max_blocks = (rows + br - 1) / br;
-    // An item of an even split has at most so many contributors; rows of few
-    // blocks (a decode step of few lanes) are the ones with more than kFan.
+    // WIDE where rows have many contributors and are too few to fill the chip with a
+    // wave each (8 lanes of 16384 tokens of dim 256, 12 rows: 39.9 us with, 42.3
+    // without; 8 x 8 rows of 40960 in 8 bits: 112.9 with, 109.5 without).
     const int in_block = rows < br ? rows : br;
     const long long items = (long long)a.lanes * a.c.kv_heads * max_blocks;
-    const bool wide = a.workers / items >= kFan;
+    const bool wide = a.workers / items >= kFan && items * in_block <= 4 * device_cus();
     const dim3 grid((unsigned)(wide ? in_block : (in_block + 3) / 4), (unsigned)(a.c.kv_heads * max_blocks), (unsigned)a.lanes);
     if (wide)
         hipLaunchKernelGGL((attend_join_kernel<D, true>), grid, dim3(256), 0, s, a, br, max_blocks);
@@ -971,7 +976,7 @@ size_t nvfp4_tree_attention_workspace_bytes(int q_heads, int kv_heads, int head_
         q_heads > 65536)
         return 0;
     const AttShape sh = att_shape(max_rows * (q_heads / kv_heads), head_dim);
-    return part_rows(sh) * (sizeof(float2) + head_dim * sizeof(float));
+    return sizeof(Shares) + part_rows(sh) * (sizeof(float2) + head_dim * sizeof(float));
 }
 
 int nvfp4_tree_mask(const int* parent, int n, uint64_t* mask, int* depth) {
@@ -1051,8 +1056,10 @@ int nvfp4_tree_attention(const nvfp4_cache* cache, int layer, const uint16_t* q_
     const long long shared = (tiles + kMinTiles - 1) / kMinTiles, most = a.whole || shared < items ? items : shared;
     const int workers = att_workers(sh, dim, a.c.fp8 != 0);
     a.workers = most < workers ? (int)most : workers;
-    a.part_ml = (float2*)workspace_dev;
-    a.part_o = (float*)((char*)workspace_dev + part_rows(sh) * sizeof(float2));
+    static_assert(sizeof(Shares) % 16 == 0, "what follows is read by 16 bytes");
+    a.shares = (Shares*)workspace_dev;
+    a.part_ml = (float2*)(a.shares + 1);
+    a.part_o = (float*)(a.part_ml + part_rows(sh));
     const bool joins = !a.whole && a.workers > 1;
     // The streaming hint, where K and V are read once (one block holds every row of
     // a lane and head) and the cache is larger than the 256 MiB that the chip's last
