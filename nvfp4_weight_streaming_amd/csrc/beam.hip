@@ -9,7 +9,7 @@
 // scores by ascending row, then token.
 //
 // The logits are read once.  They are cut into groups of 1024 tokens, and the
-// first kernel (one wave per group, a pure stream) keeps each group's maximum and
+// first kernel (two groups a wave, a pure stream) keeps each group's maximum and
 // sum of exponentials.  The k best candidates lie in the k best groups: a
 // group's best candidate is its maximum, and if k other groups have a better
 // one, those k are better than everything in it.  The second kernel, one
@@ -25,7 +25,7 @@
 namespace nvfp4 {
 
 constexpr int kBeamGroup = 1024;
-constexpr int kBeamThreads = 256;      // scan: 4 waves, one group each
+constexpr int kBeamThreads = 256;       // scan: 4 waves
 constexpr int kBeamRun = 2;             // groups per wave
 constexpr int kBeamPickThreads = 1024;  // pick: 16 waves
 constexpr int kBeamList = 1024;        // keys the pick kernel ranks at once
