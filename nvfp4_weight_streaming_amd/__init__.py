@@ -534,6 +534,7 @@ class PagedCache:
                           strides[0][1], strides[0][0])
         self._ref = ctypes.byref(self.desc)
         self._attend_ws = {}  # workspace bytes by (q heads, rows)
+        self._update_ws = {}  # by lanes and table width
 
     def _bad_lanes(self, row_start, ctx_len, page_table, lanes):
         """Names what is wrong with a call's lanes."""
@@ -670,7 +671,10 @@ class PagedCache:
         new_len = torch.empty_like(parent)
         new_refs = torch.empty_like(refs)
         short = refs.new_empty(1)
-        wsb = L.nvfp4_cache_update_workspace_bytes(self.pages, n, width)
+        wsb = self._update_ws.get((n, width))
+        if wsb is None:
+            wsb = L.nvfp4_cache_update_workspace_bytes(self.pages, n, width)
+            self._update_ws[n, width] = wsb
         ws = refs.new_empty(wsb // 4 + 4)
         st = L.nvfp4_cache_update(self._ref, lanes, page_table.data_ptr(), length.data_ptr(), refs.data_ptr(),
                                   width, n, parent.data_ptr(), None if keep is None else keep.data_ptr(),
