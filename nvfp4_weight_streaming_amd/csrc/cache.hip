@@ -81,9 +81,12 @@ int check_lanes(const CacheView& c, int lanes, const int* table, int table_ld) {
 //
 // Bound by the bytes of the rows (read once, q and the cache written once) and,
 // for a few rows, by latency: blocks of 256 threads take one row and a share of
-// its heads, the cosines of the row once per block in LDS.  K rows are written
-// 4 or 8 bytes at a time.  V blocks are dim-major: a block
-// takes an aligned group of 8 tokens and stores a dim's 8 tokens at once.
+// its heads, a thread one unit of dims with its cosines in registers.  K rows are
+// written 4 or 8 bytes at a time.  V blocks are dim-major: a block takes an
+// aligned group of 8 tokens and stores a dim's 8 tokens at once.
+//
+// Measured (48 q and 4 kv heads of 128): 2048 rows, three axes, into 8 bits, 57 MB:
+// 15.2 us, 3.8 TB/s against 5.1 of a large copy; 64 rows into bf16 4.8 us.
 
 struct AppendArgs {
     CacheView c;
@@ -322,8 +325,9 @@ __global__ __launch_bounds__(kAppendThreads) void append_kernel(AppendArgs a) {
 // destination are read whole (runs of 16 x dim values) and the destinations'
 // vectors put together in LDS, so memory sees only 16-byte accesses.
 //
-// Bound by latency for few lanes (lengths, then table, then data) and by bytes
-// for many.
+// Bound by latency for few lanes (lengths, then table, then data: 8 lanes of 8
+// drafts, 16 layers, 5.0 us) and by bytes for many (64 lanes of 64, 8 bits, 78 MB:
+// 19 us, 4.1 TB/s against 5.1 of a large copy).
 
 struct CompactArgs {
     CacheView c;
@@ -711,6 +715,7 @@ __global__ __launch_bounds__(kAssignThreads) void update_fused_kernel(UpdateArgs
 }
 
 // Copies K and V of the pages that became a lane's own: block (lane, layer, part).
+// (8 lanes of 16 layers, 21 MB read and written: 6.7 us, launch and ramp included.)
 __global__ __launch_bounds__(256) void update_copy_kernel(UpdateArgs a, long long page_bytes) {
     const int2 c = a.copies[blockIdx.x];
     if (c.x < 0 || c.y < 0) return;
