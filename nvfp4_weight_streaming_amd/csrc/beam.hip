@@ -76,14 +76,15 @@ __device__ __forceinline__ void load_group(const BeamArgs& a, int row, int group
     const float* f = (const float*)a.logits + (long long)row * a.ld;
     if (VEC) {
         // Vectors that cross V are read element by element: the caller's rows
-        // may end there.
+        // may end there.  (Compared with V less a vector: for the largest V the sum
+        // t + 8 of the group after the last one would pass 2^31.)
         if (BF16) {
             uint4 v[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int t = token_of<BF16, VEC>(group, lane, 8 * j);
                 v[j] = make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);
-                if (t + 8 <= a.V) v[j] = *(const uint4*)(h + t);
+                if (t <= a.V - 8) v[j] = *(const uint4*)(h + t);
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -94,7 +95,7 @@ __device__ __forceinline__ void load_group(const BeamArgs& a, int row, int group
                     x[8 * j + 2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
                 }
                 const int t = token_of<BF16, VEC>(group, lane, 8 * j);
-                if (t < a.V && t + 8 > a.V)
+                if (t < a.V && t > a.V - 8)
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         if (t + i < a.V) x[8 * j + i] = bf16_up(h[t + i]);
@@ -105,7 +106,7 @@ __device__ __forceinline__ void load_group(const BeamArgs& a, int row, int group
             for (int j = 0; j < 4; ++j) {
                 const int t = token_of<BF16, VEC>(group, lane, 4 * j);
                 v[j] = make_float4(none, none, none, none);
-                if (t + 4 <= a.V) v[j] = *(const float4*)(f + t);
+                if (t <= a.V - 4) v[j] = *(const float4*)(f + t);
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -114,7 +115,7 @@ __device__ __forceinline__ void load_group(const BeamArgs& a, int row, int group
                 x[4 * j + 2] = v[j].z;
                 x[4 * j + 3] = v[j].w;
                 const int t = token_of<BF16, VEC>(group, lane, 4 * j);
-                if (t < a.V && t + 4 > a.V)
+                if (t < a.V && t > a.V - 4)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         if (t + i < a.V) x[4 * j + i] = f[t + i];

@@ -78,3 +78,17 @@ def test_large_logits(nv, dtype, size):
     x[3, ::7] = -size
     x[3, 77] = size / 4
     _check(nv, x.to(getattr(torch, dtype)), 2, [0.0, -1.0, -2.0, 0.0, -3.0, -1.5], 8)
+
+
+@pytest.mark.parametrize("dtype,V", [("bfloat16", 2 ** 31 - 1032), ("bfloat16", 2 ** 31 - 1025), ("float32", 2 ** 31 - 1028)])
+def test_largest_vocabulary(nv, dtype, V):
+    """Token numbers up to the documented limit, rows read in vectors and by element.  The sum of 2^21
+    groups' sums takes 2^15 additions a lane: off by at most (2^15 + 64) 2^-24 of it."""
+    import torch
+    x = torch.zeros((1, V), dtype=getattr(torch, dtype), device="cuda")
+    x[0, V - 1], x[0, 5], x[0, V - 1000], x[0, 1 << 30] = 8.0, 7.0, 6.0, 5.0
+    s, parent, token, _ = (host(t) for t in nv.beam_select(x, 1, dev(np.zeros(1, np.float32)), 6))
+    assert token[0].tolist() == [V - 1, 5, V - 1000, 1 << 30, 0, 1] and not parent.any()
+    v = np.array([8.0, 7.0, 6.0, 5.0, 0.0, 0.0])
+    want = v - np.log(V - 4 + np.exp(v[:4]).sum())
+    assert (np.abs(s[0] - want) <= (2 ** 15 + 64) * 2.0 ** -24 + 2.0 ** -21 * 42).all(), (s, want)
