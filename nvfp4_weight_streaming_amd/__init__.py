@@ -521,6 +521,8 @@ class PagedCache:
                               (v, (tokens * dim, 16 * dim, 16, 1), "v")):
             if any(n != 1 and a != b for n, a, b in zip(x.shape[2:], x.stride()[2:], want)):
                 _refuse("%s: a page is not contiguous" % name)
+            if any(n > 1 and s == 0 for n, s in zip(x.shape[:2], x.stride()[:2])):
+                _refuse("%s: layers or pages share memory" % name)
         es = k.element_size()
         strides = [[0 if n == 1 else s * es for n, s in zip(x.shape[:2], x.stride()[:2])]
                    for x in (k, v)]
