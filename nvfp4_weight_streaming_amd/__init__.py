@@ -343,10 +343,15 @@ def beam_select(logits, beams, score, k, done=None, eos=-1, stream=None):
         dtype = OUT_BF16
     else:
         _refuse("logits: not float32 or bfloat16")
-    if not (score.dtype is torch.float32 and score.numel() == rows and score.is_contiguous()):
-        _refuse("score: not %d contiguous float32 values" % rows)
-    if done is not None and not (done.dtype is torch.uint8 and done.numel() == rows and done.is_contiguous()):
-        _refuse("done: not %d contiguous uint8 values" % rows)
+    gpu = logits.get_device()
+    if gpu < 0:
+        _refuse("logits: not on a GPU")
+    if not (score.dtype is torch.float32 and score.numel() == rows and score.is_contiguous()
+            and score.get_device() == gpu):
+        _refuse("score: not %d contiguous float32 values on the logits' GPU" % rows)
+    if done is not None and not (done.dtype is torch.uint8 and done.numel() == rows and done.is_contiguous()
+                                 and done.get_device() == gpu):
+        _refuse("done: not %d contiguous uint8 values on the logits' GPU" % rows)
     L, dev = _lib or lib(), logits.device
     shape = (batch, k)
     out = score.new_empty(shape)
@@ -503,7 +508,8 @@ class PagedCache:
     value.  A page is contiguous; layers and pages may have other strides (equal ones for k and v).
 
     ``row_start`` (int32 [lanes + 1]), ``ctx_len`` (int32 [lanes]) and ``page_table`` (int32
-    [lanes][pages of a lane], contiguous) are device tensors; include/nvfp4.h has the rules of
+    [lanes][pages of a lane], contiguous) and a call's other tensors are on k's and v's GPU, and are
+    refused elsewhere; include/nvfp4.h has the rules of
     each call.  Workspaces come from torch's allocator on the current stream, call by call.
     (The checks are written out in each method: they run once per layer and round.)
     """
@@ -515,6 +521,8 @@ class PagedCache:
         layers, pages, heads, tokens, dim = k.shape
         if tuple(v.shape) != (layers, pages, heads, tokens // 16, dim, 16):
             _refuse("v: shape %s does not go with k's %s" % (tuple(v.shape), tuple(k.shape)))
+        if k.device != v.device:
+            _refuse("v: not on k's device")
         if k.dtype != v.dtype or k.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
             _refuse("k, v: not both bfloat16 or float8_e4m3fn")
         for x, want, name in ((k, (tokens * dim, dim, 1), "k"),
@@ -531,6 +539,7 @@ class PagedCache:
         self.k, self.v = k, v
         self.layers, self.pages, self.kv_heads, self.page_tokens, self.head_dim = k.shape
         self.device = k.device
+        self._gpu = k.get_device()  # -1: none, and every call is refused
         self.desc = Cache(k.data_ptr(), v.data_ptr(), layers, pages, heads, tokens, dim,
                           CACHE_BF16 if es == 2 else CACHE_E4M3, float(k_scale), float(v_scale),
                           strides[0][1], strides[0][0])
@@ -541,37 +550,43 @@ class PagedCache:
     def _bad_lanes(self, row_start, ctx_len, page_table, lanes):
         """Names what is wrong with a call's lanes."""
         import torch
+        if self._gpu < 0:
+            _refuse("cache: not on a GPU")
         for x, n, name in ((row_start, lanes + 1, "row_start"), (ctx_len, lanes, "ctx_len")):
-            if x is not None and not (x.dtype is torch.int32 and x.numel() == n and x.is_contiguous()):
-                _refuse("%s: not %d contiguous int32 values" % (name, n))
-        _refuse("page_table: not a contiguous int32 matrix of %d rows" % lanes)
+            if x is not None and not (x.dtype is torch.int32 and x.numel() == n and x.is_contiguous()
+                                      and x.get_device() == self._gpu):
+                _refuse("%s: not %d contiguous int32 values on the cache's GPU" % (name, n))
+        _refuse("page_table: not a contiguous int32 matrix of %d rows on the cache's GPU" % lanes)
 
     def append(self, layer, qkv, q_heads, row_start, ctx_len, page_table, positions, inv_freq,
                pair_axis=None, interleaved=False, factor=1.0, out=None, stream=None):
         """Rotates q and k of a qkv product's rows, stores k and v, returns q [rows][q_heads * dim]."""
         import torch
         i32, bf16 = torch.int32, torch.bfloat16
-        lanes, dim, L, dev = ctx_len.numel(), self.head_dim, _lib or lib(), self.device
+        lanes, dim, L, dev, gpu = ctx_len.numel(), self.head_dim, _lib or lib(), self.device, self._gpu
         if not (ctx_len.dtype is i32 and ctx_len.is_contiguous() and row_start.dtype is i32
                 and row_start.is_contiguous() and row_start.numel() == lanes + 1
                 and page_table.dtype is i32 and page_table.is_contiguous()
-                and page_table.dim() == 2 and page_table.shape[0] == lanes):
+                and page_table.dim() == 2 and page_table.shape[0] == lanes
+                and gpu >= 0 and ctx_len.get_device() == gpu and row_start.get_device() == gpu
+                and page_table.get_device() == gpu):
             self._bad_lanes(row_start, ctx_len, page_table, lanes)
         width = q_heads * dim
-        if qkv.dtype is not bf16 or qkv.dim() != 2:
-            _refuse("qkv: not a bfloat16 matrix")
+        if qkv.dtype is not bf16 or qkv.dim() != 2 or qkv.get_device() != gpu:
+            _refuse("qkv: not a bfloat16 matrix on the cache's GPU")
         rows, cols = qkv.shape
         ld, inner = qkv.stride()
         if cols < width + 2 * self.kv_heads * dim or inner != 1:
             _refuse("qkv: rows are not %d contiguous values" % (width + 2 * self.kv_heads * dim))
         pairs, axes = inv_freq.numel(), positions.shape[1] if positions.dim() == 2 else 1
-        if not (inv_freq.dtype is torch.float32 and inv_freq.is_contiguous()):
-            _refuse("inv_freq: not contiguous float32 values")
-        if not (positions.dtype is i32 and positions.is_contiguous() and positions.numel() == rows * axes):
-            _refuse("positions: not %d contiguous int32 values" % (rows * axes))
+        if not (inv_freq.dtype is torch.float32 and inv_freq.is_contiguous() and inv_freq.get_device() == gpu):
+            _refuse("inv_freq: not contiguous float32 values on the cache's GPU")
+        if not (positions.dtype is i32 and positions.is_contiguous() and positions.numel() == rows * axes
+                and positions.get_device() == gpu):
+            _refuse("positions: not %d contiguous int32 values on the cache's GPU" % (rows * axes))
         if pair_axis is not None and not (pair_axis.dtype is torch.uint8 and pair_axis.is_contiguous()
-                                          and pair_axis.numel() == pairs):
-            _refuse("pair_axis: not %d contiguous uint8 values" % pairs)
+                                          and pair_axis.numel() == pairs and pair_axis.get_device() == gpu):
+            _refuse("pair_axis: not %d contiguous uint8 values on the cache's GPU" % pairs)
         if out is None:
             out, q_ld = qkv.new_empty((rows, width)), width
         else:
@@ -589,8 +604,8 @@ class PagedCache:
     def _out_ld(self, out, rows, width):
         """Leading dimension of a caller's output of at least `rows` rows."""
         import torch
-        if out.dtype is not torch.bfloat16 or out.dim() != 2 or out.shape[0] < rows:
-            _refuse("out: not a bfloat16 matrix of %d rows" % rows)
+        if out.dtype is not torch.bfloat16 or out.dim() != 2 or out.shape[0] < rows or out.get_device() != self._gpu:
+            _refuse("out: not a bfloat16 matrix of %d rows on the cache's GPU" % rows)
         if out.shape[1] < width or out.stride(1) != 1:
             _refuse("out: rows are not %d contiguous values" % width)
         return out.stride(0) if out.shape[0] > 1 else max(out.stride(0), out.shape[1])
@@ -602,22 +617,25 @@ class PagedCache:
         out, or (out, lse fp32 [rows][q_heads])."""
         import torch
         i32, bf16 = torch.int32, torch.bfloat16
-        lanes, dim, L, dev = ctx_len.numel(), self.head_dim, _lib or lib(), self.device
+        lanes, dim, L, dev, gpu = ctx_len.numel(), self.head_dim, _lib or lib(), self.device, self._gpu
         if not (ctx_len.dtype is i32 and ctx_len.is_contiguous() and row_start.dtype is i32
                 and row_start.is_contiguous() and row_start.numel() == lanes + 1
                 and page_table.dtype is i32 and page_table.is_contiguous()
-                and page_table.dim() == 2 and page_table.shape[0] == lanes):
+                and page_table.dim() == 2 and page_table.shape[0] == lanes
+                and gpu >= 0 and ctx_len.get_device() == gpu and row_start.get_device() == gpu
+                and page_table.get_device() == gpu):
             self._bad_lanes(row_start, ctx_len, page_table, lanes)
-        if q.dtype is not bf16 or q.dim() != 2:
-            _refuse("q: not a bfloat16 matrix")
+        if q.dtype is not bf16 or q.dim() != 2 or q.get_device() != gpu:
+            _refuse("q: not a bfloat16 matrix on the cache's GPU")
         rows, cols = q.shape
         ld, inner = q.stride()
         q_heads = cols // dim
         width = q_heads * dim
         if inner != 1:
             _refuse("q: rows are not contiguous")
-        if not (mask.dtype is torch.int64 and mask.numel() == rows and mask.is_contiguous()):
-            _refuse("mask: not %d contiguous int64 values" % rows)
+        if not (mask.dtype is torch.int64 and mask.numel() == rows and mask.is_contiguous()
+                and mask.get_device() == gpu):
+            _refuse("mask: not %d contiguous int64 values on the cache's GPU" % rows)
         if out is None:
             out, out_ld = q.new_empty((rows, width)), width
         else:
@@ -641,14 +659,17 @@ class PagedCache:
         """Moves each lane's accepted drafts (path int32 [lanes][n], accepted int32 [lanes]) to the
         front of its drafted tokens, in every layer."""
         import torch
-        i32, lanes, L = torch.int32, ctx_len.numel(), _lib or lib()
+        i32, lanes, L, gpu = torch.int32, ctx_len.numel(), _lib or lib(), self._gpu
         if not (ctx_len.dtype is i32 and ctx_len.is_contiguous() and page_table.dtype is i32
-                and page_table.is_contiguous() and page_table.dim() == 2 and page_table.shape[0] == lanes):
+                and page_table.is_contiguous() and page_table.dim() == 2 and page_table.shape[0] == lanes
+                and gpu >= 0 and ctx_len.get_device() == gpu and page_table.get_device() == gpu):
             self._bad_lanes(None, ctx_len, page_table, lanes)
-        if not (path.dtype is i32 and path.is_contiguous() and path.dim() == 2 and path.shape[0] == lanes):
-            _refuse("path: not a contiguous int32 matrix of %d rows" % lanes)
-        if not (accepted.dtype is i32 and accepted.is_contiguous() and accepted.numel() == lanes):
-            _refuse("accepted: not %d contiguous int32 values" % lanes)
+        if not (path.dtype is i32 and path.is_contiguous() and path.dim() == 2 and path.shape[0] == lanes
+                and path.get_device() == gpu):
+            _refuse("path: not a contiguous int32 matrix of %d rows on the cache's GPU" % lanes)
+        if not (accepted.dtype is i32 and accepted.is_contiguous() and accepted.numel() == lanes
+                and accepted.get_device() == gpu):
+            _refuse("accepted: not %d contiguous int32 values on the cache's GPU" % lanes)
         st = L.nvfp4_cache_compact(self._ref, lanes, ctx_len.data_ptr(), page_table.data_ptr(),
                                    page_table.shape[1], path.data_ptr(), path.shape[1], accepted.data_ptr(),
                                    _current(self.device) if stream is None else _stream(stream))
@@ -659,16 +680,19 @@ class PagedCache:
         """New tables from old ones (reorder, fork, truncate, free, make room): returns
         (page_table, length, refs, short), all int32; shared partly filled pages are copied."""
         import torch
-        i32, lanes, L, dev = torch.int32, length.numel(), _lib or lib(), self.device
+        i32, lanes, L, dev, gpu = torch.int32, length.numel(), _lib or lib(), self.device, self._gpu
         if not (length.dtype is i32 and length.is_contiguous() and page_table.dtype is i32
-                and page_table.is_contiguous() and page_table.dim() == 2 and page_table.shape[0] == lanes):
+                and page_table.is_contiguous() and page_table.dim() == 2 and page_table.shape[0] == lanes
+                and gpu >= 0 and length.get_device() == gpu and page_table.get_device() == gpu):
             self._bad_lanes(None, length, page_table, lanes)
-        if not (refs.dtype is i32 and refs.is_contiguous() and refs.numel() == self.pages):
-            _refuse("refs: not %d contiguous int32 values" % self.pages)
+        if not (refs.dtype is i32 and refs.is_contiguous() and refs.numel() == self.pages
+                and refs.get_device() == gpu):
+            _refuse("refs: not %d contiguous int32 values on the cache's GPU" % self.pages)
         n, width = parent.numel(), page_table.shape[1]
         for x, name in ((parent, "parent"), (keep, "keep"), (reserve, "reserve")):
-            if x is not None and not (x.dtype is i32 and x.is_contiguous() and x.numel() == n):
-                _refuse("%s: not %d contiguous int32 values" % (name, n))
+            if x is not None and not (x.dtype is i32 and x.is_contiguous() and x.numel() == n
+                                      and x.get_device() == gpu):
+                _refuse("%s: not %d contiguous int32 values on the cache's GPU" % (name, n))
         table = page_table.new_empty((n, width))
         new_len = torch.empty_like(parent)
         new_refs = torch.empty_like(refs)

@@ -35,3 +35,59 @@ def test_layers_between_pages_are_taken(nv):
     k, v = _kv(layers=5, pages=3)
     c = nv.PagedCache(k.transpose(0, 1), v.transpose(0, 1))
     assert (c.desc.page_stride, c.desc.layer_stride) == (3 * 2 * 32 * 64 * 2, 2 * 32 * 64 * 2)
+
+
+def _calls(nv, put):
+    """(name, function, arguments) of every call on a cache, each tensor passed through `put`."""
+    import torch
+    i32 = lambda *s: put(torch.zeros(s, dtype=torch.int32))  # noqa: E731
+    bf16 = lambda *s: put(torch.zeros(s, dtype=torch.bfloat16))  # noqa: E731
+    cache = nv.PagedCache(*(put(x) for x in _kv()))
+    lanes = dict(row_start=i32(3), ctx_len=i32(2), page_table=i32(2, 4))
+    logits = put(torch.zeros((4, 10)))
+    return [
+        ("append", cache.append, dict(layer=0, qkv=bf16(3, 512), q_heads=4, **lanes, positions=i32(3, 2), inv_freq=put(torch.zeros(32)),
+                                      pair_axis=put(torch.zeros(32, dtype=torch.uint8)), out=bf16(3, 256))),
+        ("attend", cache.attend, dict(layer=0, q=bf16(3, 256), **lanes, mask=put(torch.zeros(3, dtype=torch.int64)), max_rows=2, scale=0.1,
+                                      out=bf16(3, 256))),
+        ("compact", cache.compact, dict(ctx_len=i32(2), page_table=i32(2, 4), path=i32(2, 4), accepted=i32(2))),
+        ("update", cache.update, dict(page_table=i32(2, 4), length=i32(2), refs=i32(5), parent=i32(2), keep=i32(2), reserve=i32(2))),
+        ("beam_select", nv.beam_select, dict(logits=logits, beams=2, score=put(torch.zeros(4)), k=2, done=put(torch.zeros(4, dtype=torch.uint8)),
+                                             eos=1)),
+    ]
+
+
+def _never(nv, monkeypatch):
+    """No entry point may be reached: host tensors must not come as far as a kernel."""
+    import types
+    sizes = {n: getattr(nv.lib(), n) for n in nv.EXPORTS if n.endswith("_bytes")}
+    monkeypatch.setattr(nv, "_lib", types.SimpleNamespace(**sizes))
+
+
+def test_host_tensors_are_refused(nv, monkeypatch):
+    """Each argument of each call left in host memory beside others on a GPU, and all of them."""
+    import torch
+
+    class OnGpu(torch.Tensor):
+        def get_device(self):
+            return 0
+
+    _never(nv, monkeypatch)
+    for name, f, args in _calls(nv, lambda x: x):
+        with pytest.raises(nv.Nvfp4Error, match="not on a GPU"):
+            f(**args)
+    for name, f, args in _calls(nv, lambda x: x.as_subclass(OnGpu)):
+        tensors = [n for n, x in args.items() if isinstance(x, torch.Tensor)]
+        assert len(tensors) >= 3
+        for n in tensors:
+            with pytest.raises(nv.Nvfp4Error, match="GPU") as e:
+                f(**{**args, n: args[n].as_subclass(torch.Tensor)})
+            word = "ctx_len" if n == "length" else n
+            assert e.value.message.startswith(word + ":"), (name, n, e.value.message)
+
+
+def test_k_and_v_on_one_device(nv):
+    import torch
+    k, v = _kv()
+    with pytest.raises(nv.Nvfp4Error, match="not on k's device"):
+        nv.PagedCache(k, torch.empty_like(v, device="meta"))
