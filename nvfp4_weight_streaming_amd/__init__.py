@@ -328,8 +328,12 @@ def nvfp4_beam_select(logits, logits_dtype, ld, batch, beams, V, score, done, eo
 
 def beam_select(logits, beams, score, k, done=None, eos=-1, stream=None):
     """The k best continuations of each request: (score fp32, parent int32, token int32, done
-    uint8), each [requests][k], of a device fp32 or bf16 logits tensor [requests * beams][V]."""
+    uint8), each [requests][k], of a device fp32 or bf16 logits tensor [requests * beams][V].  A
+    stream that is given is torch's current one during the call, so outputs belong to it."""
     import torch
+    if stream is not None and logits.is_cuda:
+        with _on(stream, logits.device):
+            return beam_select(logits, beams, score, k, done, eos)
     rows, V = logits.shape
     batch = rows // beams if beams > 0 else 0
     if rows != batch * beams:
@@ -363,7 +367,7 @@ def beam_select(logits, beams, score, k, done=None, eos=-1, stream=None):
     st = L.nvfp4_beam_select(logits.data_ptr(), dtype, ld if rows > 1 else max(ld, V), batch, beams, V,
                              score.data_ptr(), None if done is None else done.data_ptr(), eos, k,
                              out.data_ptr(), parent.data_ptr(), token.data_ptr(), ended.data_ptr(),
-                             ws.data_ptr(), wsb, _current(dev) if stream is None else _stream(stream))
+                             ws.data_ptr(), wsb, _current(dev))
     if st:
         _check(st)
     return out, parent, token, ended
@@ -500,6 +504,18 @@ def _current(device):
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
+def _on(stream, device):
+    """Context in which a stream (torch's, or a handle of `device`) is torch's current one: what a call
+    allocates is then taken from that stream's memory, and reused by it alone."""
+    import torch
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)
+        stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+    if stream.device != device:
+        _refuse("stream: on %s, not %s" % (stream.device, device))
+    return torch.cuda.stream(stream)
+
+
 class PagedCache:
     """A paged key/value cache over the caller's tensors and the operators on it.
 
@@ -510,7 +526,9 @@ class PagedCache:
     ``row_start`` (int32 [lanes + 1]), ``ctx_len`` (int32 [lanes]) and ``page_table`` (int32
     [lanes][pages of a lane], contiguous) and a call's other tensors are on k's and v's GPU, and are
     refused elsewhere; include/nvfp4.h has the rules of
-    each call.  Workspaces come from torch's allocator on the current stream, call by call.
+    each call.  A call runs on torch's current stream, or makes the one that it is given current:
+    outputs and workspaces come from that stream's memory, call by call, and tensors of other streams
+    need what torch asks for there (a wait before, ``record_stream`` before they are dropped).
     (The checks are written out in each method: they run once per layer and round.)
     """
 
@@ -562,6 +580,10 @@ class PagedCache:
                pair_axis=None, interleaved=False, factor=1.0, out=None, stream=None):
         """Rotates q and k of a qkv product's rows, stores k and v, returns q [rows][q_heads * dim]."""
         import torch
+        if stream is not None and self._gpu >= 0:
+            with _on(stream, self.device):
+                return self.append(layer, qkv, q_heads, row_start, ctx_len, page_table, positions, inv_freq,
+                                   pair_axis, interleaved, factor, out)
         i32, bf16 = torch.int32, torch.bfloat16
         lanes, dim, L, dev, gpu = ctx_len.numel(), self.head_dim, _lib or lib(), self.device, self._gpu
         if not (ctx_len.dtype is i32 and ctx_len.is_contiguous() and row_start.dtype is i32
@@ -596,7 +618,7 @@ class PagedCache:
         st = L.nvfp4_cache_append(self._ref, layer, qkv.data_ptr(), ld if rows > 1 else max(ld, cols), rows,
                                   q_heads, lanes, row_start.data_ptr(), ctx_len.data_ptr(),
                                   page_table.data_ptr(), page_table.shape[1], ctypes.byref(rot), out.data_ptr(),
-                                  q_ld, _current(dev) if stream is None else _stream(stream))
+                                  q_ld, _current(dev))
         if st:
             _check(st)
         return out
@@ -616,6 +638,9 @@ class PagedCache:
         drafts its mask words (int64 [rows]) name; max_rows: at least any lane's rows.  Returns
         out, or (out, lse fp32 [rows][q_heads])."""
         import torch
+        if stream is not None and self._gpu >= 0:
+            with _on(stream, self.device):
+                return self.attend(layer, q, row_start, ctx_len, page_table, mask, max_rows, scale, out, with_lse)
         i32, bf16 = torch.int32, torch.bfloat16
         lanes, dim, L, dev, gpu = ctx_len.numel(), self.head_dim, _lib or lib(), self.device, self._gpu
         if not (ctx_len.dtype is i32 and ctx_len.is_contiguous() and row_start.dtype is i32
@@ -650,7 +675,7 @@ class PagedCache:
                                     rows, lanes, max_rows, row_start.data_ptr(), ctx_len.data_ptr(),
                                     page_table.data_ptr(), page_table.shape[1], mask.data_ptr(), scale,
                                     out.data_ptr(), out_ld, lse.data_ptr() if with_lse else None,
-                                    ws.data_ptr(), wsb, _current(dev) if stream is None else _stream(stream))
+                                    ws.data_ptr(), wsb, _current(dev))
         if st:
             _check(st)
         return (out, lse) if with_lse else out
@@ -680,6 +705,9 @@ class PagedCache:
         """New tables from old ones (reorder, fork, truncate, free, make room): returns
         (page_table, length, refs, short), all int32; shared partly filled pages are copied."""
         import torch
+        if stream is not None and self._gpu >= 0:
+            with _on(stream, self.device):
+                return self.update(page_table, length, refs, parent, keep, reserve)
         i32, lanes, L, dev, gpu = torch.int32, length.numel(), _lib or lib(), self.device, self._gpu
         if not (length.dtype is i32 and length.is_contiguous() and page_table.dtype is i32
                 and page_table.is_contiguous() and page_table.dim() == 2 and page_table.shape[0] == lanes
@@ -706,7 +734,7 @@ class PagedCache:
                                   width, n, parent.data_ptr(), None if keep is None else keep.data_ptr(),
                                   None if reserve is None else reserve.data_ptr(), table.data_ptr(),
                                   new_len.data_ptr(), new_refs.data_ptr(), short.data_ptr(), ws.data_ptr(), wsb,
-                                  _current(dev) if stream is None else _stream(stream))
+                                  _current(dev))
         if st:
             _check(st)
         return table, new_len, new_refs, short
