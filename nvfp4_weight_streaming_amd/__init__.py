@@ -250,8 +250,12 @@ def nvfp4_topk(logits, M, V, ld, k, idx, val, workspace=None, workspace_bytes=0,
 
 
 def topk(logits, k, stream=None):
-    """(indices int32 [M][k], values [M][k]) of a device fp32 [M][V] tensor."""
+    """(indices int32 [M][k], values [M][k]) of a device fp32 [M][V] tensor.  A stream that is given is
+    torch's current one during the call, so outputs belong to it."""
     import torch
+    if stream is not None and logits.is_cuda:
+        with _on(stream, logits.device):
+            return topk(logits, k)
     M, V = logits.shape
     idx = torch.empty((M, k), dtype=torch.int32, device=logits.device)
     val = torch.empty((M, k), dtype=torch.float32, device=logits.device)

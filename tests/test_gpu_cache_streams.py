@@ -35,11 +35,12 @@ def _calls(nv):
         "attend": ("nvfp4_tree_attention", lambda **s: list(cache.attend(1, q, start, ctx, table, masks, 4, 0.09, with_lse=True, **s))),
         "update": ("nvfp4_cache_update", lambda **s: list(cache.update(table, ctx, refs, parent, **s))),
         "beam_select": ("nvfp4_beam_select", lambda **s: list(nv.beam_select(logits, 4, score, 8, **s))),
+        "topk": ("nvfp4_topk", lambda **s: list(nv.topk(logits, 8, **s))),
     }
 
 
 @pytest.mark.parametrize("kind", ["stream", "handle"])
-@pytest.mark.parametrize("name", ["append", "attend", "update", "beam_select"])
+@pytest.mark.parametrize("name", ["append", "attend", "update", "beam_select", "topk"])
 def test_a_stream_of_the_callers(nv, monkeypatch, name, kind):
     import torch
     entry, call = _calls(nv)[name]
