@@ -754,19 +754,19 @@ int nvfp4_cache_append(const nvfp4_cache* cache, int layer, const uint16_t* qkv_
         return set_error(NVFP4_EINVAL, "qkv_ld: %lld below %lld or not a multiple of 4", (long long)qkv_ld, (long long)width);
     if (q_ld < (int64_t)q_heads * dim || q_ld % 4)
         return set_error(NVFP4_EINVAL, "q_ld: %lld below %lld or not a multiple of 4", (long long)q_ld, (long long)q_heads * dim);
-    if (!qkv_dev || ((uintptr_t)qkv_dev & 7)) return set_error(NVFP4_EINVAL, "qkv: NULL or not 8-byte aligned");
-    if (!q_out_dev || ((uintptr_t)q_out_dev & 7)) return set_error(NVFP4_EINVAL, "q_out: NULL or not 8-byte aligned");
     if (!row_start_dev || ((uintptr_t)row_start_dev & 3)) return set_error(NVFP4_EINVAL, "row_start: NULL or not 4-byte aligned");
     if (!ctx_len_dev || ((uintptr_t)ctx_len_dev & 3)) return set_error(NVFP4_EINVAL, "ctx_len: NULL or not 4-byte aligned");
     if (!rotary) return set_error(NVFP4_EINVAL, "rotary: NULL");
     if (rotary->pairs < 0 || rotary->pairs > dim / 2 || rotary->pairs % 4)
         return set_error(NVFP4_EINVAL, "rotary.pairs: %d is not a multiple of 4 up to %d", rotary->pairs, dim / 2);
     if (rotary->axes < 1 || rotary->axes > 8) return set_error(NVFP4_EINVAL, "rotary.axes: %d outside [1, 8]", rotary->axes);
+    if (rows == 0) return NVFP4_OK;  // (the rows' pointers may be NULL: empty tensors have no address)
+    if (!qkv_dev || ((uintptr_t)qkv_dev & 7)) return set_error(NVFP4_EINVAL, "qkv: NULL or not 8-byte aligned");
+    if (!q_out_dev || ((uintptr_t)q_out_dev & 7)) return set_error(NVFP4_EINVAL, "q_out: NULL or not 8-byte aligned");
     if (rotary->pairs) {
         if (!rotary->positions_dev || ((uintptr_t)rotary->positions_dev & 3)) return set_error(NVFP4_EINVAL, "rotary.positions: NULL or not 4-byte aligned");
         if (!rotary->inv_freq_dev || ((uintptr_t)rotary->inv_freq_dev & 3)) return set_error(NVFP4_EINVAL, "rotary.inv_freq: NULL or not 4-byte aligned");
     }
-    if (rows == 0) return NVFP4_OK;
     a.qkv = qkv_dev;
     a.ld = qkv_ld;
     a.q_heads = q_heads;

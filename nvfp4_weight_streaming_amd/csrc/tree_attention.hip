@@ -1015,19 +1015,20 @@ int nvfp4_tree_attention(const nvfp4_cache* cache, int layer, const uint16_t* q_
     if (q_heads < kv || q_heads % kv || q_heads > 65536)
         return set_error(NVFP4_EINVAL, "q_heads: %d is not a multiple of kv_heads %d up to 65536", q_heads, kv);
     if (rows < 0 || rows > (1 << 24)) return set_error(NVFP4_EINVAL, "rows: %d outside [0, 2^24]", rows);
-    if (max_rows < 1 || max_rows > NVFP4_TREE_MAX_ROWS)
+    if (max_rows < (rows > 0 ? 1 : 0) || max_rows > NVFP4_TREE_MAX_ROWS)
         return set_error(NVFP4_EINVAL, "max_rows: %d outside [1, %d]", max_rows, NVFP4_TREE_MAX_ROWS);
     if ((st = check_lanes(a.c, lanes, page_table_dev, table_ld))) return st;
     const int64_t width = (int64_t)q_heads * dim;
     if (q_ld < width || q_ld % 8) return set_error(NVFP4_EINVAL, "q_ld: %lld below %lld or not a multiple of 8", (long long)q_ld, (long long)width);
     if (out_ld < width || out_ld % 4) return set_error(NVFP4_EINVAL, "out_ld: %lld below %lld or not a multiple of 4", (long long)out_ld, (long long)width);
-    if (!q_dev || ((uintptr_t)q_dev & 15)) return set_error(NVFP4_EINVAL, "q: NULL or not 16-byte aligned");
-    if (!out_dev || ((uintptr_t)out_dev & 7)) return set_error(NVFP4_EINVAL, "out: NULL or not 8-byte aligned");
     if (!row_start_dev || ((uintptr_t)row_start_dev & 3)) return set_error(NVFP4_EINVAL, "row_start: NULL or not 4-byte aligned");
     if (!ctx_len_dev || ((uintptr_t)ctx_len_dev & 3)) return set_error(NVFP4_EINVAL, "ctx_len: NULL or not 4-byte aligned");
+    if (!(scale > 0.f) || scale > 1e30f) return set_error(NVFP4_EINVAL, "scale: not a positive number");
+    if (rows == 0) return NVFP4_OK;  // (the rows' pointers may be NULL: empty tensors have no address)
+    if (!q_dev || ((uintptr_t)q_dev & 15)) return set_error(NVFP4_EINVAL, "q: NULL or not 16-byte aligned");
+    if (!out_dev || ((uintptr_t)out_dev & 7)) return set_error(NVFP4_EINVAL, "out: NULL or not 8-byte aligned");
     if (!mask_dev || ((uintptr_t)mask_dev & 7)) return set_error(NVFP4_EINVAL, "mask: NULL or not 8-byte aligned");
     if ((uintptr_t)lse_dev & 3) return set_error(NVFP4_EINVAL, "lse: not 4-byte aligned");
-    if (!(scale > 0.f) || scale > 1e30f) return set_error(NVFP4_EINVAL, "scale: not a positive number");
     const size_t need = nvfp4_tree_attention_workspace_bytes(q_heads, kv, dim, max_rows);
     if (workspace_bytes < need) return set_error(NVFP4_EINVAL, "workspace_bytes: %zu < %zu needed", workspace_bytes, need);
     if (!workspace_dev || ((uintptr_t)workspace_dev & 15)) return set_error(NVFP4_EINVAL, "workspace: NULL or not 16-byte aligned");
@@ -1038,7 +1039,6 @@ int nvfp4_tree_attention(const nvfp4_cache* cache, int layer, const uint16_t* q_
         return set_error(NVFP4_EUNSUPPORTED, "lanes: %d lanes of %d kv heads, %d row blocks and %d pages exceed 2^31 tiles", lanes, kv, blocks, table_ld);
     if ((long long)kv * blocks > 65535)
         return set_error(NVFP4_EUNSUPPORTED, "q_heads: %d kv heads of %d row blocks exceed 65535", kv, blocks);
-    if (rows == 0) return NVFP4_OK;
     a.q = q_dev;
     a.q_ld = q_ld;
     a.q_heads = q_heads;

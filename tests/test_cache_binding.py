@@ -91,3 +91,29 @@ def test_k_and_v_on_one_device(nv):
     k, v = _kv()
     with pytest.raises(nv.Nvfp4Error, match="not on k's device"):
         nv.PagedCache(k, torch.empty_like(v, device="meta"))
+
+
+def test_calls_of_no_rows(nv):
+    """Empty tensors have no address: such calls return empty outputs and launch nothing."""
+    import torch
+
+    class OnGpu(torch.Tensor):
+        def get_device(self):
+            return 0
+
+    def t(*s, dtype=torch.int32):
+        return torch.zeros(s, dtype=dtype).as_subclass(OnGpu)
+
+    cache = nv.PagedCache(*(x.as_subclass(OnGpu) for x in _kv()))
+    lanes = t(3), t(2), t(2, 4)
+    bf16 = torch.bfloat16
+    assert t(0, 512, dtype=bf16).data_ptr() == 0
+    q = cache.append(0, t(0, 512, dtype=bf16), 4, *lanes, t(0, 2), t(32, dtype=torch.float32))
+    assert tuple(q.shape) == (0, 256)
+    for most in (0, 1, 8):
+        out, lse = cache.attend(0, t(0, 256, dtype=bf16), *lanes, t(0, dtype=torch.int64), most, 0.1, with_lse=True)
+        assert tuple(out.shape) == (0, 256) and tuple(lse.shape) == (0, 4)
+    with pytest.raises(nv.Nvfp4Error, match="max_rows"):
+        cache.attend(0, t(0, 256, dtype=bf16), *lanes, t(0, dtype=torch.int64), 65, 0.1)
+    with pytest.raises(nv.Nvfp4Error, match="layer"):
+        cache.append(3, t(0, 512, dtype=bf16), 4, *lanes, t(0, 2), t(32, dtype=torch.float32))
