@@ -444,7 +444,7 @@ int nvfp4_tree_mask(const int* parent, int n, uint64_t* mask, int* depth);
  *   out[row][head] = sum_p w_p v_p / sum_p w_p,  w_p = exp(scale * q . k_p)
  *   lse[row][head] = log sum_p w_p   (if lse_dev is not NULL)
  * q head i uses kv head i / (q_heads / kv_heads).  A row that sees nothing gives
- * 0 and -inf.  q_dev: bf16 [rows][q_ld]; out_dev: bf16 [rows][out_ld]; lse_dev: fp32
+ * 0 and -inf, one with a NaN score NaN in both.  q_dev: bf16 [rows][q_ld]; out_dev: bf16 [rows][out_ld]; lse_dev: fp32
  * [rows][q_heads].  max_rows (up to 64): an upper bound of a lane's rows; rows past it,
  * and lanes whose rows lie outside [0, rows), are not computed.  Tokens past a lane's last row, and those in missing pages, may hold
  * anything, NaN included; a drafted token that only some rows see must be

@@ -758,13 +758,13 @@ __global__ __launch_bounds__(kAttThreads, (AttTraits<D, FP8, NR, RW, TW, DW, SPL
                 if (row >= rows) continue;
                 if (whole) {
                     const int tt = (int)((unsigned)row / (unsigned)group), head = h * group + row - tt * group;
-                    const float inv = l[r] > 0.f ? ae.c.v_scale / l[r] : 0.f;
+                    const float inv = l[r] == 0.f ? 0.f : ae.c.v_scale / l[r];
                     uint16_t* dst = ae.out + (long long)(w.row0 + tt) * ae.out_ld + (long long)head * D + 16 * dw * DB;
 #pragma unroll
                     for (int db = 0; db < DB; ++db)
                         *(uint2*)(dst + 16 * db + 4 * g) = bf16x4(o[r][db][0] * inv, o[r][db][1] * inv, o[r][db][2] * inv, o[r][db][3] * inv);
                     if (ae.lse && g == 0 && dw == 0)
-                        ae.lse[(long long)(w.row0 + tt) * ae.q_heads + head] = l[r] > 0.f ? (m[r] + log2f(l[r])) * kLn2 : -__builtin_inff();
+                        ae.lse[(long long)(w.row0 + tt) * ae.q_heads + head] = l[r] == 0.f ? -__builtin_inff() : (m[r] + log2f(l[r])) * kLn2;
                 } else {
                     float* dst = ae.part_o + ((long long)slot * kRows + in_block) * D + 16 * dw * DB;
 #pragma unroll
@@ -882,7 +882,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttArgs a, int block_r
         }
     }
     const int tt = (int)((unsigned)row / (unsigned)a.group), head = h * a.group + row - tt * a.group;
-    const float inv = sum > 0.f ? a.c.v_scale / sum : 0.f;
+    const float inv = sum == 0.f ? 0.f : a.c.v_scale / sum;
     uint16_t* dst = a.out + (long long)(w.row0 + tt) * a.out_ld + (long long)head * D + E * lane;
     if constexpr (E == 1) {
         dst[0] = f32_to_bf16_rne(acc[0] * inv);
@@ -892,7 +892,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttArgs a, int block_r
         *(uint2*)dst = bf16x4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
     }
     if (a.lse && lane == 0)
-        a.lse[(long long)(w.row0 + tt) * a.q_heads + head] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : -__builtin_inff();
+        a.lse[(long long)(w.row0 + tt) * a.q_heads + head] = sum == 0.f ? -__builtin_inff() : (mx + log2f(sum)) * kLn2;
 }
 
 // How a call's rows are cut: the smallest block that holds the largest lane's, up to
