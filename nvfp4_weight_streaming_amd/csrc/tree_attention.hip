@@ -37,6 +37,7 @@
 // arithmetic, 830 of what the matrix units do (weights enter the second product as
 // two bf16 numbers), against 1250 of a large product: bound by the vector work of
 // the softmax beside the matrix instructions, 2.9 for each.
+#include <cfloat>
 #include <type_traits>
 
 #include "cache.h"
@@ -1024,6 +1025,9 @@ int nvfp4_tree_attention(const nvfp4_cache* cache, int layer, const uint16_t* q_
     if (!row_start_dev || ((uintptr_t)row_start_dev & 3)) return set_error(NVFP4_EINVAL, "row_start: NULL or not 4-byte aligned");
     if (!ctx_len_dev || ((uintptr_t)ctx_len_dev & 3)) return set_error(NVFP4_EINVAL, "ctx_len: NULL or not 4-byte aligned");
     if (!(scale > 0.f) || scale > 1e30f) return set_error(NVFP4_EINVAL, "scale: not a positive number");
+    a.scale2 = scale * kLog2e * a.c.k_scale;
+    if (a.scale2 == 0.f || a.scale2 > FLT_MAX)  // a masked score times 0, or 0 times inf, would be NaN
+        return set_error(NVFP4_EINVAL, "scale: %g times cache.k_scale %g is outside fp32's range", scale, a.c.k_scale);
     if (rows == 0) return NVFP4_OK;  // (the rows' pointers may be NULL: empty tensors have no address)
     if (!q_dev || ((uintptr_t)q_dev & 15)) return set_error(NVFP4_EINVAL, "q: NULL or not 16-byte aligned");
     if (!out_dev || ((uintptr_t)out_dev & 7)) return set_error(NVFP4_EINVAL, "out: NULL or not 8-byte aligned");
@@ -1051,7 +1055,6 @@ int nvfp4_tree_attention(const nvfp4_cache* cache, int layer, const uint16_t* q_
     a.table = page_table_dev;
     a.table_ld = table_ld;
     a.mask = (const unsigned long long*)mask_dev;
-    a.scale2 = scale * kLog2e * a.c.k_scale;
     a.out = out_dev;
     a.out_ld = out_ld;
     a.lse = lse_dev;

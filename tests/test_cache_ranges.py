@@ -1,0 +1,38 @@
+"""CPU tests of the paged cache's entry points at the ends of their arguments' ranges."""
+import os
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def nv():
+    import nvfp4_weight_streaming_amd as nv
+    if not os.path.exists(nv.LIB_PATH):
+        from nvfp4_weight_streaming_amd import build as b
+        b.build()
+    nv.lib()
+    return nv
+
+
+P = 0x1000  # a well-aligned pointer that is never followed
+
+
+def _cache(nv, **kw):
+    d = dict(k_dev=P, v_dev=P, layers=2, pages=10, kv_heads=4, page_tokens=64, head_dim=128, dtype=0, k_scale=1.0,
+             v_scale=1.0, page_stride=0, layer_stride=0)
+    d.update(kw)
+    return nv.Cache(**d)
+
+
+@pytest.mark.parametrize("scale,k_scale,ok", [(0.1, 1.0, True), (1e-30, 1e-20, False), (1e30, 1e30, False), (1e-20, 1e-18, True),
+                                              (1e-19, 1e-18, True), (1e30, 1e8, True)])
+def test_scales_whose_product_is_no_number(nv, scale, k_scale, ok):
+    """The kernel multiplies by scale x k_scale: 0 or infinity would make masked scores NaN."""
+    f = lambda: nv.nvfp4_tree_attention(_cache(nv, dtype=1, k_scale=k_scale), 0, P, 1024, 8, 0, 2, 8, P, P, P, 4, P, scale, P, 1024,  # noqa: E731
+                                        None, P, 1 << 40, stream=0)
+    if ok:
+        f()  # of no rows: nothing is launched
+        return
+    with pytest.raises(nv.Nvfp4Error) as e:
+        f()
+    assert e.value.status == nv.EINVAL and e.value.message.startswith("scale")
