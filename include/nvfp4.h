@@ -380,7 +380,8 @@ int nvfp4_topk(const float* logits_dev, int M, int V, int ld, int k, int* idx_de
  * token t lies in page table[lane][t / page_tokens].  An entry outside
  * [0, pages) names no page: tokens there are seen by nobody and stored nowhere.
  * All tables, lengths and starts are device arrays, so a call under graph
- * capture follows the values that are there when the graph runs.  A call of 0 rows
+ * capture follows the values that are there when the graph runs.  Of a lane with a
+ * negative length nothing is stored or moved.  A call of 0 rows
  * launches nothing and looks at none of the rows' pointers.
  *
  * Limits: head_dim 64, 128 or 256; page_tokens 16, 32, 64, 128 or 256;

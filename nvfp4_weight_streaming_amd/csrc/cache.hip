@@ -246,11 +246,12 @@ __global__ __launch_bounds__(kAppendThreads) void append_kernel(AppendArgs a) {
     if (b >= a.lanes) return;  // a row past the last lane's
     const int row0 = a.row_start[b], t = r - row0;
     if (t < 0) return;
-    const long long p = (long long)a.ctx_len[b] + t;  // this row's place in the lane
+    const int ctx = a.ctx_len[b];
+    const long long p = (long long)ctx + t;  // this row's place in the lane
     const int page_tokens = 1 << a.c.log_page;
     const int* tab = a.table + (long long)b * a.table_ld;
     const int es = a.c.fp8 ? 1 : 2;
-    const bool placed = p >= 0 && (p >> a.c.log_page) < a.table_ld;
+    const bool placed = ctx >= 0 && (p >> a.c.log_page) < a.table_ld;
     const int id = placed ? tab[p >> a.c.log_page] : -1;
     const bool stored = (unsigned)id < (unsigned)a.c.pages;
 
