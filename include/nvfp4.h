@@ -493,7 +493,8 @@ int nvfp4_cache_compact(const nvfp4_cache* cache, int lanes, const int* ctx_len_
  * is -1 (a lane that finds none for its copy loses that page's tokens).
  * Writes table_out [lanes_out][table_ld], len_out [lanes_out] (n), refs_out
  * [cache->pages] and short_dev[0], the number of entries that found no page.
- * Outputs must not overlap inputs.  The answer is unique.
+ * Outputs must not overlap inputs; lanes_out * table_ld up to 2^31 - 1.  The answer is
+ * unique.
  *   workspace_dev: nvfp4_cache_update_workspace_bytes bytes (16-byte aligned), any
  *   content; owned by the call while it runs.
  * Asynchronous on `stream`. */

@@ -847,6 +847,8 @@ int nvfp4_cache_update(const nvfp4_cache* cache, int lanes_in, const int* table_
     if ((st = check_lanes(a.c, lanes_in, table_in_dev, table_ld))) return st;
     if (lanes_out < 1 || lanes_out > kMaxLanes)
         return set_error(NVFP4_EINVAL, "lanes_out: %d outside [1, %d]", lanes_out, kMaxLanes);
+    if ((int64_t)lanes_out * table_ld > 0x7FFFFFFF)  // (requests for pages are counted in 32 bits)
+        return set_error(NVFP4_EUNSUPPORTED, "lanes_out: %d lanes of %d pages exceed 2^31 - 1 table entries", lanes_out, table_ld);
     if (a.c.layers > 65535) return set_error(NVFP4_EUNSUPPORTED, "cache.layers: %d above 65535", a.c.layers);
     const struct { const void* p; const char* name; int may; } ptrs[] = {
         {len_in_dev, "len_in", 0}, {refs_in_dev, "refs_in", 0}, {parent_dev, "parent", 0},

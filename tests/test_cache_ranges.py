@@ -36,3 +36,20 @@ def test_scales_whose_product_is_no_number(nv, scale, k_scale, ok):
     with pytest.raises(nv.Nvfp4Error) as e:
         f()
     assert e.value.status == nv.EINVAL and e.value.message.startswith("scale")
+
+
+@pytest.mark.parametrize("lanes,width", [(65535, 32769), (1 << 15, 1 << 16), (2, 1 << 30)])
+def test_updates_of_too_many_entries(nv, lanes, width):
+    """Requests for pages are counted in 32 bits: tables of 2^31 entries or more are refused."""
+    c = _cache(nv, page_tokens=16)
+    width = min(width, 1 << 26)
+    args = lambda w: (c, 2, P, P, P, w, lanes, P, None, None, 2 * P, 2 * P, 2 * P, P, P, 10)  # noqa: E731
+    with pytest.raises(nv.Nvfp4Error) as e:
+        nv.nvfp4_cache_update(*args(width), stream=0)
+    if lanes * width < 2 ** 31:
+        assert e.value.message.startswith("workspace_bytes")  # (the next check: nothing is launched)
+        return
+    assert e.value.status == nv.EUNSUPPORTED and e.value.message.startswith("lanes_out")
+    with pytest.raises(nv.Nvfp4Error) as e:
+        nv.nvfp4_cache_update(*args((2 ** 31 - 1) // lanes), stream=0)
+    assert e.value.message.startswith("workspace_bytes")
