@@ -602,8 +602,9 @@ class PagedCache:
             _refuse("qkv: not a bfloat16 matrix on the cache's GPU")
         rows, cols = qkv.shape
         ld, inner = qkv.stride()
-        if cols < width + 2 * self.kv_heads * dim or inner != 1:
-            _refuse("qkv: rows are not %d contiguous values" % (width + 2 * self.kv_heads * dim))
+        taken = width + 2 * self.kv_heads * dim
+        if cols < taken or inner != 1:
+            _refuse("qkv: rows are not %d contiguous values" % taken)
         pairs, axes = inv_freq.numel(), positions.shape[1] if positions.dim() == 2 else 1
         if not (inv_freq.dtype is torch.float32 and inv_freq.is_contiguous() and inv_freq.get_device() == gpu):
             _refuse("inv_freq: not contiguous float32 values on the cache's GPU")
@@ -619,7 +620,7 @@ class PagedCache:
             q_ld = self._out_ld(out, rows, width)
         rot = Rotary(positions.data_ptr(), inv_freq.data_ptr(),
                      None if pair_axis is None else pair_axis.data_ptr(), axes, pairs, interleaved, factor)
-        st = L.nvfp4_cache_append(self._ref, layer, qkv.data_ptr(), ld if rows > 1 else max(ld, cols), rows,
+        st = L.nvfp4_cache_append(self._ref, layer, qkv.data_ptr(), ld if rows > 1 else taken, rows,
                                   q_heads, lanes, row_start.data_ptr(), ctx_len.data_ptr(),
                                   page_table.data_ptr(), page_table.shape[1], ctypes.byref(rot), out.data_ptr(),
                                   q_ld, _current(dev))
@@ -634,7 +635,7 @@ class PagedCache:
             _refuse("out: not a bfloat16 matrix of %d rows on the cache's GPU" % rows)
         if out.shape[1] < width or out.stride(1) != 1:
             _refuse("out: rows are not %d contiguous values" % width)
-        return out.stride(0) if out.shape[0] > 1 else max(out.stride(0), out.shape[1])
+        return out.stride(0) if rows > 1 else width
 
     def attend(self, layer, q, row_start, ctx_len, page_table, mask, max_rows, scale, out=None,
                with_lse=False, stream=None):
@@ -675,7 +676,7 @@ class PagedCache:
             wsb = L.nvfp4_tree_attention_workspace_bytes(q_heads, self.kv_heads, dim, max_rows)
             self._attend_ws[q_heads, max_rows] = wsb
         ws = q.new_empty(wsb // 2 + 8)
-        st = L.nvfp4_tree_attention(self._ref, layer, q.data_ptr(), ld if rows > 1 else max(ld, width), q_heads,
+        st = L.nvfp4_tree_attention(self._ref, layer, q.data_ptr(), ld if rows > 1 else width, q_heads,
                                     rows, lanes, max_rows, row_start.data_ptr(), ctx_len.data_ptr(),
                                     page_table.data_ptr(), page_table.shape[1], mask.data_ptr(), scale,
                                     out.data_ptr(), out_ld, lse.data_ptr() if with_lse else None,

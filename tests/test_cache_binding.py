@@ -117,3 +117,34 @@ def test_calls_of_no_rows(nv):
         cache.attend(0, t(0, 256, dtype=bf16), *lanes, t(0, dtype=torch.int64), 65, 0.1)
     with pytest.raises(nv.Nvfp4Error, match="layer"):
         cache.append(3, t(0, 512, dtype=bf16), 4, *lanes, t(0, 2), t(32, dtype=torch.float32))
+
+
+def test_single_rows_of_any_stride(nv, monkeypatch):
+    """The stride of a tensor of one row is never used: rows cut from wider ones of odd width are taken."""
+    import torch
+    import types
+
+    class OnGpu(torch.Tensor):
+        def get_device(self):
+            return 0
+
+    seen = {}
+    sizes = {n: getattr(nv.lib(), n) for n in nv.EXPORTS if n.endswith("_bytes")}
+    calls = {n: (lambda *a, n=n: seen.__setitem__(n, a) or 0) for n in ("nvfp4_cache_append", "nvfp4_tree_attention")}
+    monkeypatch.setattr(nv, "_lib", types.SimpleNamespace(**sizes, **calls))
+
+    def t(*s, dtype=torch.int32):
+        return torch.zeros(s, dtype=dtype).as_subclass(OnGpu)
+
+    cache = nv.PagedCache(*(x.as_subclass(OnGpu) for x in _kv()))
+    wide, bf16 = t(4, 519, dtype=torch.bfloat16), torch.bfloat16
+    lanes = t(2), t(1), t(1, 4)
+    for out in (None, wide[:1, :256], wide[:1]):
+        cache.append(0, wide[:1, :512], 4, *lanes, t(1, 1), t(32, dtype=torch.float32), out=out)
+        assert (seen["nvfp4_cache_append"][3], seen["nvfp4_cache_append"][13]) == (512, 256)
+        cache.attend(0, wide[:1, :256], *lanes, t(1, dtype=torch.int64), 1, 0.1, out=out)
+        assert (seen["nvfp4_tree_attention"][3], seen["nvfp4_tree_attention"][15]) == (256, 256)
+    cache.append(0, wide[:2, :512], 4, t(2), t(1), t(1, 4), t(2, 1), t(32, dtype=torch.float32), out=wide[:, :256])
+    assert (seen["nvfp4_cache_append"][3], seen["nvfp4_cache_append"][13]) == (519, 519)
+    cache.attend(0, wide[:2, :256], *lanes, t(2, dtype=torch.int64), 1, 0.1, out=t(2, 300, dtype=bf16))
+    assert (seen["nvfp4_tree_attention"][3], seen["nvfp4_tree_attention"][15]) == (519, 300)
