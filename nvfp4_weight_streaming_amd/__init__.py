@@ -569,12 +569,12 @@ class PagedCache:
         self._attend_ws = {}  # workspace bytes by (q heads, rows)
         self._update_ws = {}  # by lanes and table width
 
-    def _bad_lanes(self, row_start, ctx_len, page_table, lanes):
+    def _bad_lanes(self, row_start, ctx_len, page_table, lanes, length="ctx_len"):
         """Names what is wrong with a call's lanes."""
         import torch
         if self._gpu < 0:
             _refuse("cache: not on a GPU")
-        for x, n, name in ((row_start, lanes + 1, "row_start"), (ctx_len, lanes, "ctx_len")):
+        for x, n, name in ((row_start, lanes + 1, "row_start"), (ctx_len, lanes, length)):
             if x is not None and not (x.dtype is torch.int32 and x.numel() == n and x.is_contiguous()
                                       and x.get_device() == self._gpu):
                 _refuse("%s: not %d contiguous int32 values on the cache's GPU" % (name, n))
@@ -717,7 +717,7 @@ class PagedCache:
         if not (length.dtype is i32 and length.is_contiguous() and page_table.dtype is i32
                 and page_table.is_contiguous() and page_table.dim() == 2 and page_table.shape[0] == lanes
                 and gpu >= 0 and length.get_device() == gpu and page_table.get_device() == gpu):
-            self._bad_lanes(None, length, page_table, lanes)
+            self._bad_lanes(None, length, page_table, lanes, "length")
         if not (refs.dtype is i32 and refs.is_contiguous() and refs.numel() == self.pages
                 and refs.get_device() == gpu):
             _refuse("refs: not %d contiguous int32 values on the cache's GPU" % self.pages)
