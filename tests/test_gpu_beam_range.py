@@ -92,3 +92,17 @@ def test_largest_vocabulary(nv, dtype, V):
     v = np.array([8.0, 7.0, 6.0, 5.0, 0.0, 0.0])
     want = v - np.log(V - 4 + np.exp(v[:4]).sum())
     assert (np.abs(s[0] - want) <= (2 ** 15 + 64) * 2.0 ** -24 + 2.0 ** -21 * 42).all(), (s, want)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_more_groups_than_are_ranked_at_once(nv, dtype):
+    """64 rows of 128 blocks, the same two far below the others in each row: the bar that the k-th best of 64
+    shares of the blocks sets is theirs, and nearly all 8192 blocks pass it."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn((64, 131072), generator=g, device="cuda")
+    x[:, 9 * 1024:10 * 1024] -= 50
+    x[:, (9 + 64) * 1024:(10 + 64) * 1024] -= 50
+    s, parent, token = _check(nv, x.to(getattr(torch, dtype)), 64, -3 * np.random.default_rng(1).random(64), 64)
+    flat = parent[0].astype(np.int64) * 131072 + token[0]
+    assert (flat[:-1] < flat[1:])[s[0][:-1] == s[0][1:]].all()
