@@ -1069,13 +1069,16 @@ int nvfp4_tree_attention(const nvfp4_cache* cache, int layer, const uint16_t* q_
     a.part_ml = (float2*)(a.shares + 1);
     a.part_o = (float*)(a.part_ml + part_rows(sh));
     const bool joins = !a.whole && a.workers > 1;
-    // The streaming hint, where K and V are read once (one block holds every row of
-    // a lane and head) and the cache is larger than the 256 MiB that the chip's last
-    // cache can keep from call to call.  8 lanes of 40960 tokens (451 MB), 12 rows:
-    // 91 us without, 81 with; 8 of 4096 (45 MB): 19.4 without, 21.3 with; four blocks
-    // of 128 rows: 131 without, 149 with.
+    // The streaming hint, where K and V are read once (one block holds every row of a
+    // lane and head): always for few rows, and for more rows if the pool is larger than
+    // the 256 MiB that the chip's last cache can keep from call to call.  8 lanes of one
+    // row, 12 heads, without the hint and with it, the pool just read and 640 MB of
+    // others read in between: 45 MB 17.6 -> 16.4 and 20.0 -> 18.4 us, 181 MB 37.4 -> 37.4
+    // and 44.5 -> 40.1, 451 MB 89 -> 79 and 92 -> 81.  4 rows (48 a head): 181 MB 47 -> 53
+    // and 56 -> 54, 451 MB 110 -> 100 and 114 -> 102; 8 rows: 46 MB 30.4 -> 32.6 and
+    // 32.3 -> 33.3.  Four blocks of 128 rows: 131 -> 149.
     const double cache_bytes = 2.0 * a.c.layers * a.c.pages * ((double)kv * dim * (a.c.fp8 ? 1 : 2) * (1 << a.c.log_page));
-    a.stream = blocks == 1 && cache_bytes > 64.0 * (1 << 20);
+    a.stream = blocks == 1 && (sh.block_rows() <= kFewRows || cache_bytes > 256.0 * (1 << 20));
     hipStream_t s = (hipStream_t)stream;
     if (dim == 64) return launch_attend<64>(sh, a, joins, s);
     if (dim == 128) return launch_attend<128>(sh, a, joins, s);
