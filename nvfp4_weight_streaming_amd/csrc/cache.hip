@@ -608,10 +608,19 @@ __global__ __launch_bounds__(kAssignThreads) void update_assign_kernel(UpdateArg
     }
 }
 
-// Phases 1 to 3 in one workgroup, counts in LDS, where the pool and the lanes fit
-// it: one launch instead of three.  Lanes' partly filled last pages are compared
-// with each other directly.
-constexpr int kFusedPages = 32768, kFusedLanes = kAssignThreads, kFusedEntries = 65536;
+// Phases 1 to 3 in one workgroup, counts in LDS, for small calls: one launch instead of
+// three.  Lanes' partly filled last pages are compared with each other directly.
+//
+// Its time grows with the table entries (old and new), pages and new lanes, about as
+// 2 entries + pages + 256 lanes; that of the three kernels hardly does, but their two
+// further launches take the host 5.4 us (14.0 and 19.4 for a call).  Times with the page
+// copies of one layer in a captured graph, one workgroup and three kernels, in us: 8
+// lanes of 70 pages, 700 in the pool 7.3 and 11.6; 8 of 1024, 8400 10.1 and 13.6; 64 of
+// 128, 8400 12.1 and 12.3; 128 of 64, 8400 14.3 and 12.5; 64 of 257, 16832 16.0 and 12.9;
+// 256 of 32, 8400 18.9 and 12.8; 64 of 512, 32768 22.4 and 14.3; 1024 of 8, 10300 45 and
+// 16.  So they meet near a sum of 50000 in a graph and of 140000 call by call; the
+// bound is their geometric mean.  (What the counts may take of LDS bounds the pages.)
+constexpr int kFusedWork = 81920, kFusedPages = 32768, kFusedLanes = kFusedWork / 256;
 __global__ __launch_bounds__(kAssignThreads) void update_fused_kernel(UpdateArgs a, int* slots) {
     extern __shared__ int refs[];  // [pages]
     __shared__ int lasts[kFusedLanes], parents[kFusedLanes], lens[kFusedLanes];
@@ -884,8 +893,8 @@ int nvfp4_cache_update(const nvfp4_cache* cache, int lanes_in, const int* table_
     ws += round16((size_t)lanes_out * sizeof(int2));
     int* slots = (int*)ws;
     hipStream_t s = (hipStream_t)stream;
-    if (a.c.pages <= kFusedPages && lanes_out <= kFusedLanes &&
-        ((long long)lanes_in + lanes_out) * table_ld <= kFusedEntries) {
+    if (a.c.pages <= kFusedPages &&
+        2 * ((long long)lanes_in + lanes_out) * table_ld + a.c.pages + 256ll * lanes_out <= kFusedWork) {
         hipLaunchKernelGGL(update_fused_kernel, dim3(1), dim3(kAssignThreads), (size_t)a.c.pages * sizeof(int), s, a, slots);
         NVFP4_HIP(hipGetLastError());
     } else {

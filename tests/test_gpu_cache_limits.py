@@ -46,10 +46,11 @@ def _update_case(seed, lanes_in, lanes_out, width, page, pages):
             rng.integers(0, 3 * page, lanes_out))
 
 
-# pages at and past what the one-workgroup kernel holds in LDS (32768; past 16384 more than 64 KiB), entries
-# of old and new tables at and past its 65536, lanes at and past its 1024; 8-bit page copies in every case
+# pages at and past what the one-workgroup kernel holds in LDS (32768; past 16384 more than 64 KiB), its most
+# lanes, long tables, more lanes than a workgroup has threads, and both sides of the sum of the three that chooses
+# it (2 (lanes_in + lanes_out) width + pages + 256 lanes_out = 81920); 8-bit page copies in every case
 @pytest.mark.parametrize("lanes_in,lanes_out,width,pages", [
-    (20, 30, 40, 16385), (20, 30, 40, 32768), (20, 30, 40, 32769), (64, 64, 512, 32768), (64, 65, 512, 20000), (3, 1024, 8, 9000), (3, 1025, 8, 9000)])
+    (1, 120, 150, 14900), (1, 120, 150, 14901), (4, 300, 4, 2000), (1, 316, 1, 390), (1, 320, 1, 700), (20, 30, 40, 16385), (20, 30, 40, 32768), (20, 30, 40, 32769), (64, 64, 512, 32768), (64, 65, 512, 20000), (3, 1024, 8, 9000), (3, 1025, 8, 9000)])
 @pytest.mark.parametrize("dtype", ["e4m3", "bf16"])
 def test_update_at_the_limits_of_its_kernels(nv, lanes_in, lanes_out, width, pages, dtype):
     import torch
