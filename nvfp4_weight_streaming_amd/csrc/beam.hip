@@ -157,10 +157,7 @@ __device__ __forceinline__ float wave_sum(float v) {
     return (lanef(v, 0) + lanef(v, 16)) + (lanef(v, 32) + lanef(v, 48));
 }
 // exp(x - m): the difference is rounded before it is scaled, so that terms near
-// the maximum, which make up the sum, are off by 2^-22 or less, and that logits of
-// any finite size may be taken: 2^(x c - m c) in one step, corrected for the rounding
-// of m c, is inf x 0 from |m| = 3e9 on (a block masked with -1e10 or the type's lowest
-// value).  (16 requests of 8 beams, both kernels: 19.8 us, 19.5 with that form.)
+// the maximum, which make up the sum, are off by 2^-22 or less.
 __device__ __forceinline__ float exp_diff(float x, float m) {
     return __builtin_amdgcn_exp2f((x - m) * 1.44269504088896340736f);
 }
@@ -181,11 +178,17 @@ __global__ __launch_bounds__(kBeamThreads) void beam_scan_kernel(BeamArgs a) {
 #pragma unroll
         for (int e = 1; e < 16; ++e) m = fmaxf(m, x[u][e]);
         m = wave_max(m);
+        // exp(x - m) as 2^(x c - m c), the product m c rounded: what that loses is
+        // the same for every term and put right once.  From |m| = 2^30 on it would be
+        // more than 2^64, but there fp32 numbers are 64 apart and more: equal logits
+        // count 1 and others nothing, which 2^(x - m) says as well and exactly.
         const float use = m == -__builtin_inff() ? 0.f : m;
+        const float c = fabsf(use) < 1073741824.f ? 1.44269504088896340736f : 1.f;
+        const float mc = use * c, lost = __builtin_fmaf(use, c, -mc);
         float s = 0.f;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) s += exp_diff(x[u][e], use);
-        s = wave_sum(s);
+        for (int e = 0; e < 16; ++e) s += __builtin_amdgcn_exp2f(__builtin_fmaf(x[u][e], c, -mc));
+        s = wave_sum(s) * __builtin_amdgcn_exp2f(-lost);
         if (lane == 0 && group0 + u < a.groups) a.part[(long long)row * a.groups + group0 + u] = make_float2(m, s);
     }
 }
