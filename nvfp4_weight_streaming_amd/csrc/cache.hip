@@ -803,6 +803,8 @@ int nvfp4_cache_append(const nvfp4_cache* cache, int layer, const uint16_t* qkv_
     a.wide = (((uintptr_t)qkv_dev | (uintptr_t)q_out_dev) & 15) == 0 && qkv_ld % 8 == 0 && q_ld % 8 == 0;
     // V: a lane's rows cover at most rows / 8 + 2 groups of 8 tokens.
     const long long blocks = (long long)rows * a.shares + rows / 8 + 2ll * (lanes < rows ? lanes : rows);
+    if (blocks * kAppendThreads > 0xFFFFFFFFll)
+        return set_error(NVFP4_EUNSUPPORTED, "rows: %d take more than 2^32 - 1 threads", rows);
     hipLaunchKernelGGL(append_kernel, dim3((unsigned)blocks), dim3(kAppendThreads), 0, (hipStream_t)stream, a);
     NVFP4_HIP(hipGetLastError());
     return NVFP4_OK;
@@ -821,6 +823,8 @@ int nvfp4_cache_compact(const nvfp4_cache* cache, int lanes, const int* ctx_len_
     if (!path_dev || ((uintptr_t)path_dev & 3)) return set_error(NVFP4_EINVAL, "path: NULL or not 4-byte aligned");
     if (!accepted_dev || ((uintptr_t)accepted_dev & 3)) return set_error(NVFP4_EINVAL, "accepted: NULL or not 4-byte aligned");
     if (a.c.layers > 65535) return set_error(NVFP4_EUNSUPPORTED, "cache.layers: %d above 65535", a.c.layers);
+    if ((int64_t)lanes * a.c.kv_heads * kCompactThreads > 0xFFFFFFFFll)
+        return set_error(NVFP4_EUNSUPPORTED, "lanes: %d lanes of %d kv heads take more than 2^32 - 1 threads", lanes, a.c.kv_heads);
     a.lanes = lanes;
     a.ctx_len = ctx_len_dev;
     a.table = page_table_dev;

@@ -53,3 +53,16 @@ def test_updates_of_too_many_entries(nv, lanes, width):
     with pytest.raises(nv.Nvfp4Error) as e:
         nv.nvfp4_cache_update(*args((2 ** 31 - 1) // lanes), stream=0)
     assert e.value.message.startswith("workspace_bytes")
+
+
+def test_calls_of_more_threads_than_a_launch_has(nv):
+    """A launch takes fewer than 2^32 threads: what needs more is refused, not cut off."""
+    rot = nv.Rotary(positions_dev=P, inv_freq_dev=P, pair_axis_dev=None, axes=1, pairs=0, interleaved=0, factor=1.0)
+    c = _cache(nv, head_dim=64, kv_heads=1)
+    with pytest.raises(nv.Nvfp4Error) as e:
+        nv.nvfp4_cache_append(c, 0, P, 192, 1 << 24, 1, 2, P, P, P, 4, rot, P, 64, stream=0)
+    assert e.value.status == nv.EUNSUPPORTED and e.value.message.startswith("rows")
+    c = _cache(nv, kv_heads=1024)
+    with pytest.raises(nv.Nvfp4Error) as e:
+        nv.nvfp4_cache_compact(c, 1 << 15, P, P, 4, P, 8, P, stream=0)
+    assert e.value.status == nv.EUNSUPPORTED and e.value.message.startswith("lanes")
