@@ -16,10 +16,11 @@
 // workgroup per request, forms each row's log-sum, takes the k best groups by
 // score and rereads only those (at most 64 x 1024 logits).
 //
-// Measured over 152064 tokens: 128 rows in bf16 (39 MB) scan 11 us, 3.5 TB/s, bound
-// by the vector work of an exponential per logit beside its loads; 4 rows in fp32 3.4.
-// The second kernel is a chain of small reads and barriers: 6.0 us for one request
-// of 4 beams, 8.5 for 16 of 8.
+// Measured over 152064 tokens: 128 rows in bf16 (39 MB) scan 11.3 us, 3.5 TB/s: ten vector
+// instructions a logit keep the vector units busy for 5 us, and a wave, all of whose loads
+// go out at once, has none left to hide behind that work (its waves wait for 63% of their
+// time); 4 rows in fp32 3.5.  The second kernel is a chain of small reads and barriers:
+// 6.0 us for one request of 4 beams, 8.3 for 16 of 8.
 #include "key_device.h"
 
 namespace nvfp4 {
@@ -384,8 +385,9 @@ __global__ __launch_bounds__(kBeamPickThreads) void beam_pick_kernel(BeamArgs a)
         __syncthreads();
         if (threadIdx.x < 64) best[threadIdx.x] = winners[threadIdx.x];
     } else {
-        // Many equal scores: the waves insert their candidates one by one into
-        // sorted lists of their own.
+        // Many equal scores, or fewer groups than k, so that every candidate passes (a
+        // vocabulary of a few thousand): the waves insert their candidates one by one
+        // into sorted lists of their own.
         __syncthreads();
         u64 kept = 0;
         for_candidates([&](u64 key) {

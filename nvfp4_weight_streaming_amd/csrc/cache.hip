@@ -76,8 +76,8 @@ int check_lanes(const CacheView& c, int lanes, const int* table, int table_ld) {
 // position p turns by the angle a = p inv_freq[i]:
 //     (x, y) -> factor (x cos a - y sin a, x sin a + y cos a),
 // p being the row's position on the pair's axis (time, height or width).  The
-// angle is formed and reduced in fp64, where the product of an int32 and an fp32
-// number is exact, so long positions lose nothing; one rounding at the end.
+// angle is formed and reduced in fp64: exact for positions below 2^29 (29 + 24 bits),
+// off by 2^-53 of it above; one rounding at the end.
 //
 // Bound by the bytes of the rows (read once, q and the cache written once) and,
 // for a few rows, by latency: blocks of 256 threads take one row and a share of
@@ -625,9 +625,9 @@ __global__ __launch_bounds__(kAssignThreads) void update_fused_kernel(UpdateArgs
     extern __shared__ int refs[];  // [pages]
     __shared__ int lasts[kFusedLanes], parents[kFusedLanes], lens[kFusedLanes];
     __shared__ int lds[kAssignThreads / 64];
-    // Loads in flight at once.  More wait longer for less where a call has few entries:
-    // 8 beams of 65 pages 12.9 us with 8, 11.6 with 2, 11.4 with 1; 64 lanes of 257 pages
-    // 21.3, 20.5 and 22.0 (with the page copies).
+    // Loads in flight at once.  More wait longer for less where a call has few entries,
+    // fewer leave loads to wait for where it has many (with the page copies): 8 lanes of
+    // 70 pages 8.5 us with 8, 7.2 with 2, 7.1 with 1; 64 of 128 pages 12.1, 12.1 and 12.8.
     constexpr int kBatch = 2;
     const int tid = threadIdx.x, i = tid;
     const bool lane = i < a.lanes_out;
@@ -652,7 +652,7 @@ __global__ __launch_bounds__(kAssignThreads) void update_fused_kernel(UpdateArgs
     // Old entries give their references back, inherited ones take theirs.
     const int old = a.lanes_in * a.table_ld, fresh = a.lanes_out * a.table_ld;
     // Row and column of this thread's next entry, carried on (a division for each entry:
-    // 22.4 us for 64 lanes of 257 pages, 21.3 without).
+    // 12.5 us for 64 lanes of 128 pages, 12.1 without).
     int next_row = (int)((unsigned)tid / (unsigned)a.table_ld), next_col = tid - next_row * a.table_ld;
     const int row_step = (int)((unsigned)kAssignThreads / (unsigned)a.table_ld), col_step = kAssignThreads - row_step * a.table_ld;
     for (int e0 = 0; e0 < max(old, fresh); e0 += kBatch * kAssignThreads) {

@@ -30,13 +30,17 @@
 // that the operand reads spread over the banks.
 //
 // Measured (12 rows of dim 128 a kv head, 4 kv heads, times with the joining
-// kernel): 8 lanes of up to 40960 tokens, bf16, 451 MB: 79.5 us, 5.7 TB/s (copies
-// alone, nothing computed: 79); 8 of up to 4096, 45 MB: 18.3 us, of which about 10
-// are launches and loads that wait for each other.  64 drafted tokens a lane (768
-// rows a head), 4 lanes of up to 16384: 131 us, 555 TFLOP/s of the formula's
-// arithmetic, 830 of what the matrix units do (weights enter the second product as
-// two bf16 numbers), against 1250 of a large product: bound by the vector work of
-// the softmax beside the matrix instructions, 2.9 for each.
+// kernel): 8 lanes of up to 40960 tokens, bf16, 451 MB: 78.5 us, 5.7 TB/s (copies
+// alone, nothing computed: 79), in 8 bits 55 us; 8 of up to 4096, 45 MB: 17.5 us, of
+// which about 10 are launches and loads that wait for each other.  64 drafted tokens
+// a lane (768 rows a head), 4 lanes of up to 16384: 123 to 135 us over boxes, 540 to
+// 590 TFLOP/s of the formula's arithmetic, half as much again of what the matrix units
+// do (weights enter the second product as two bf16 numbers), against 1250 of a large
+// product: bound by the vector work of the softmax beside the matrix instructions, 2.9
+// for each (the matrix units are busy for 39% of the time, a third of the LDS cycles,
+// 20% of the time in all, are bank conflicts).  In 8 bits every wave of a block of
+// 128 rows converts the tiles for itself, 4.3 for each: 112 us for 8 lanes of 8 rows and
+// up to 40960 tokens, whose 96 rows a head also leave a quarter of the block empty.
 #include <cfloat>
 #include <type_traits>
 
@@ -57,8 +61,9 @@ constexpr float kRescaleAt = 8.f;
 // storing and joining partial results costs more than the shorter walk saves
 // (8 lanes of 4096 tokens and 12 rows: 19.1 us with 5 tiles, 19.6 with 8).
 constexpr int kMinTiles = 5;
-// Items of at most so many tiles are never shared, and no joining kernel runs (one
-// lane of 300 tokens of dim 256, 5 tiles: 13.3 us so, 15.7 shared and joined).
+// Where page tables hold no more than so many tiles, items are never shared and no
+// joining kernel runs (one lane of 300 tokens of dim 256, 5 tiles: 13.3 us with a table
+// of 6 pages of 64; 15.7, shared and joined, with one of 640).
 constexpr int kWholeTiles = 8;
 constexpr int kNoPieces = 1 << 28;  // a piece that holds any item
 // Pieces may be so many tiles longer than an equal share.  A worker whose share goes
@@ -268,7 +273,10 @@ struct AttTraits {
 // The kernel's arguments read anew where they are used: kept in registers from its
 // start they fill the scalar file, and what the tile loop needs spills (37 to 90
 // scalar registers; 14 to 45, none of them in the loop, with the arguments and the
-// copies' addresses formed where they are used).
+// copies' addresses formed where they are used).  Of the vector registers one variant
+// spills: bf16, dim 128, blocks of 64 rows (33 to 64 rows a head) takes 256 and 28 more
+// in scratch, 116 bytes a lane (8 lanes of 4 rows of 12 heads and up to 16384 tokens,
+// 181 MB: 47 us and 7 for the join; of 2 rows, in blocks of 32 without a spill, 33 and 5).
 using ArgsRef = const __attribute__((address_space(4))) AttArgs&;
 __device__ __forceinline__ ArgsRef args_anew() {
     auto at = (uintptr_t)__builtin_amdgcn_kernarg_segment_ptr();
