@@ -473,6 +473,9 @@ class PackedWeight:
     @classmethod
     def from_canonical(cls, codes, scales, tensor_scale, K, N, stream=None):
         """Pack canonical planes (device tensors [N][K/2], [N][K/16])."""
+        if stream is not None and codes.is_cuda:
+            with _on(stream, codes.device):
+                return cls.from_canonical(codes, scales, tensor_scale, K, N)
         c, s = cls.alloc(K, N, codes.device)
         nvfp4_pack(codes, scales, K, N, c, s, stream)
         return cls(c, s, tensor_scale, K, N)
@@ -482,6 +485,9 @@ class PackedWeight:
         """Quantise a device fp32 [N][K] tensor and pack it.  Reads the tensor
         scale back to the host (one synchronisation)."""
         import torch
+        if stream is not None and w.is_cuda:
+            with _on(stream, w.device):
+                return cls.quantize(w, None, keep_canonical)
         N, K = w.shape
         dev = w.device
         codes = torch.empty((N, K // 2), dtype=torch.uint8, device=dev)

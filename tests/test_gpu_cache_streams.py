@@ -67,6 +67,26 @@ def test_a_stream_of_the_callers(nv, monkeypatch, name, kind):
     assert torch.cuda.current_stream() != side
 
 
+def test_quantizing_on_a_stream_of_the_callers(nv, monkeypatch):
+    """The tensor scale is read once that stream has written it, and the workspace stays its own."""
+    import torch
+    w = torch.randn((64, 1024), device="cuda")
+    want = nv.PackedWeight.quantize(w, keep_canonical=True)
+    seen = []
+    through = nv.lib().nvfp4_quantize
+    monkeypatch.setattr(nv._lib, "nvfp4_quantize", lambda *a: seen.append(a) or through(*a))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = nv.PackedWeight.quantize(w, side, keep_canonical=True)
+    assert got.tensor_scale == want.tensor_scale and seen[0][-1] == side.cuda_stream
+    side.synchronize()
+    for a, b in zip((want.codes, want.scales, *want.canonical), (got.codes, got.scales, *got.canonical)):
+        assert torch.equal(a, b)
+    n = nv.nvfp4_quantize_workspace_bytes()
+    for x in [torch.empty(n, dtype=torch.uint8, device="cuda") for _ in range(8)]:
+        assert not any(isinstance(a, int) and x.data_ptr() <= a < x.data_ptr() + n for a in seen[0][3:-1])
+
+
 def test_the_default_stream_by_handle(nv):
     import torch
     for name, (_, call) in _calls(nv).items():
