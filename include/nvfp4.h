@@ -55,7 +55,8 @@ enum nvfp4_status {
     NVFP4_ESTATE = 4        /* misuse of a handle (destroyed, wrong plan) */
 };
 
-enum nvfp4_out_dtype { NVFP4_OUT_F32 = 0, NVFP4_OUT_BF16 = 1 };
+/* NVFP4_OUT_INT8: codes with one fp32 scale a row (nvfp4_rms_norm alone). */
+enum nvfp4_out_dtype { NVFP4_OUT_F32 = 0, NVFP4_OUT_BF16 = 1, NVFP4_OUT_INT8 = 2 };
 
 /* Largest number of lanes (activation rows) the decode kernel serves in one
  * weight pass. */
@@ -86,6 +87,11 @@ enum nvfp4_prefill_schedule {
 #define NVFP4_TREE_MAX_ROWS 64
 /* Largest number of beams of one request. */
 #define NVFP4_BEAM_MAX_BEAMS 64
+
+/* Longest row of nvfp4_rms_norm and nvfp4_int8_quantize. */
+#define NVFP4_ROW_MAX_K (1 << 24)
+/* Largest K of an 8-bit product: its sums, up to 2^14 K, stay within 32 bits. */
+#define NVFP4_INT8_MAX_K 131056
 
 /* ---- status ----------------------------------------------------------------- */
 
@@ -341,6 +347,83 @@ void nvfp4_round_destroy(nvfp4_round plan);
  * rounded once to bf16 (nearest, ties to even).  Asynchronous on `stream`. */
 int nvfp4_swiglu(const uint16_t* gate_up_dev, int M, int F, uint16_t* out_dev, void* stream);
 
+/* ---- norm between the products ------------------------------------------------- */
+
+/* The step between two products of a layer: the residual stream's addition and the
+ * root-mean-square norm, in the type that the next product takes (bf16 for
+ * nvfp4_gemm_run, 8 bits for nvfp4_int8_gemm).  For each of `rows` rows of K values
+ *   h = x + residual, rounded once to the residual's type and written to residual_out
+ *       (residual_dev and residual_out_dev NULL: h = x, and nothing is written);
+ *   y = h / sqrt(mean of h^2 + eps) * (weight + weight_offset)
+ *   out = y, rounded once; or, with NVFP4_OUT_INT8, codes and a scale as
+ *       nvfp4_int8_quantize makes them of y.
+ * All between is in fp64.  Rows lie x_ld, residual_ld (both residuals) and out_ld
+ * values apart, each at least K.  residual_out may be the residual or, of its
+ * type and stride, x; out may be x, of its type and stride; else outputs must not overlap inputs or
+ * each other.  Rows of K % 8 == 0 whose pointers and strides are multiples of 16 bytes
+ * (codes: 8) are read and written in vectors. */
+typedef struct nvfp4_norm {
+    const void* x_dev;
+    int x_dtype; /* types: nvfp4_out_dtype, fp32 or bf16 */
+    int64_t x_ld;
+    const void* residual_dev;
+    void* residual_out_dev;
+    int residual_dtype;
+    int64_t residual_ld;
+    const void* weight_dev; /* [K] */
+    int weight_dtype;
+    float weight_offset;    /* 0, or 1 for weights stored as their difference from 1 */
+    float eps;
+    void* out_dev;
+    int out_dtype;          /* fp32, bf16 or NVFP4_OUT_INT8 */
+    int64_t out_ld;
+    float* scale_dev;       /* [rows], for NVFP4_OUT_INT8 */
+} nvfp4_norm;
+
+/* 1 <= K <= NVFP4_ROW_MAX_K; rows 0 launches nothing.  Asynchronous on `stream`. */
+int nvfp4_rms_norm(const nvfp4_norm* norm, int rows, int K, void* stream);
+
+/* ---- 8-bit integers --------------------------------------------------------------- */
+
+/* Bodies in 4 bits keep sensitive matrices in more ("Models and artifacts", "The
+ * artifact": a few exception tensors).  Here such a matrix, often the output head, is
+ * held in 8-bit integers with one fp32 scale for each output channel, and its
+ * activations with one for each row.
+ *
+ * Rows to codes: for y = x, or, with swiglu = 1, y = silu(g) * u of a row [g | u]
+ * of 2 K values (as nvfp4_swiglu, before its rounding),
+ *   scale = max |y| / 127, rounded to fp32;  code = y / scale, to the nearest, ties to even.
+ * All else is in fp64.  A row whose scale is 0 (all zeros) gets codes 0; so does one with a NaN or an
+ * infinity, whose scale is that: its products are NaN.  x_dev: fp32 or bf16
+ * (nvfp4_out_dtype) [rows][x_ld]; codes_dev: [rows][codes_ld]; scale_dev: [rows].
+ * 1 <= K <= NVFP4_ROW_MAX_K.  Asynchronous on `stream`. */
+int nvfp4_int8_quantize(const void* x_dev, int x_dtype, int64_t x_ld, int rows, int K, int swiglu,
+                        int8_t* codes_dev, int64_t codes_ld, float* scale_dev, void* stream);
+
+/* Bytes of a packed K x N matrix of codes: K padded to a multiple of 64 and N to one
+ * of 16, with zeros.  0 for invalid K or N (K % 16 != 0, K < 16, K > NVFP4_INT8_MAX_K, N < 1). */
+size_t nvfp4_int8_packed_bytes(int K, int N);
+/* Permute codes [N][K] into the packed layout, 16-byte aligned, and back. */
+int nvfp4_int8_pack(const int8_t* codes_dev, int K, int N, int8_t* packed_dev, void* stream);
+int nvfp4_int8_unpack(const int8_t* packed_dev, int K, int N, int8_t* codes_dev, void* stream);
+
+/* out[m][n] = float(sum_k a[m][k] * w[n][k]) * a_scale[m] * w_scale[n] + bias[n]
+ * for m < M: the sum exact, then fp32 in this order, rounded once more to bf16 for
+ * NVFP4_OUT_BF16.
+ *   a_dev         : codes [M][a_ld], 16-byte aligned, a_ld a multiple of 16, at least K
+ *   a_scale_dev   : [M];  w_scale_dev: [N];  bias_dev: fp32 [N], or NULL
+ *   w_packed_dev  : packed codes (nvfp4_int8_pack), 16-byte aligned
+ *   out_dev       : fp32 or bf16 [M][out_ld], out_ld >= N
+ *   workspace_dev : nvfp4_int8_gemm_workspace_bytes(M, K, N) bytes (16-byte aligned; may be 0, for
+ *                   M <= 64 always), any content; owned by the call while it runs.
+ * M <= 64 streams the weights once; larger M runs tiles on the matrix cores.  Results do not depend on M, and
+ * repeat to the bit.  M = 0 launches nothing.  Asynchronous on `stream`. */
+size_t nvfp4_int8_gemm_workspace_bytes(int M, int K, int N);
+int nvfp4_int8_gemm(const int8_t* a_dev, int64_t a_ld, const float* a_scale_dev,
+                    const int8_t* w_packed_dev, const float* w_scale_dev, const float* bias_dev,
+                    int M, int K, int N, void* out_dev, int out_dtype, int64_t out_ld,
+                    void* workspace_dev, size_t workspace_bytes, void* stream);
+
 /* ---- top-k over the vocabulary ---------------------------------------------- */
 
 /* The step after the output head ("Ignis" README, "Speculative decoding
@@ -528,6 +611,31 @@ int nvfp4_beam_select(const void* logits_dev, int logits_dtype, int64_t ld, int 
                       const float* score_dev, const uint8_t* done_dev, int eos, int k,
                       float* score_out_dev, int* parent_dev, int* token_dev, uint8_t* done_out_dev,
                       void* workspace_dev, size_t workspace_bytes, void* stream);
+
+/* ---- log probabilities -------------------------------------------------------- */
+
+/* What a server answers beside the tokens, and what a draft is judged by ("Ignis" README, "Speculative decoding
+ * (DFlash2)").  For each row of logits x, fp32 or bf16 (nvfp4_out_dtype) [rows][ld]
+ * with V entries, and z = scale * x (scale: an inverse temperature, finite, above 0):
+ *   lse = log sum exp z,  p = exp(z - lse)
+ *   logprob[row][i] = z[tokens[row][i]] - lse        tokens: int32 [rows][n_tokens]
+ *   entropy[row]    = -sum p log p                   (entropy_dev may be NULL)
+ *   top_token, top_logprob [row][j], j < k: the k largest logits in descending order,
+ *   equal ones by ascending token (-0.0 equals +0.0), as nvfp4_topk lists them.
+ * A token outside [0, V) has log probability -inf, as has a logit of -inf, which
+ * adds nothing to the entropy.  A row of nothing else: all log probabilities -inf, entropy 0.  A row with a
+ * NaN or +inf: log probabilities (but those of tokens outside [0, V)) and entropy are NaN, and top tokens lie
+ * in [0, V) but are otherwise not defined.
+ * 0 <= n_tokens <= 1024, 0 <= k <= min(V, NVFP4_TOPK_MAX_K), V <= 2^30, ld >= V.  Sums in fp32 over
+ * short runs, joined in fp64; their order is fixed: results repeat to the bit.
+ *   workspace_dev: nvfp4_logprobs_workspace_bytes bytes (16-byte aligned), any content;
+ *   owned by the call while it runs.
+ * Asynchronous on `stream`. */
+size_t nvfp4_logprobs_workspace_bytes(int rows, int V, int k);
+int nvfp4_logprobs(const void* logits_dev, int logits_dtype, int64_t ld, int rows, int V,
+                   float scale, const int* tokens_dev, int n_tokens, int k, float* logprob_dev,
+                   float* entropy_dev, int* top_token_dev, float* top_logprob_dev,
+                   void* workspace_dev, size_t workspace_bytes, void* stream);
 
 /* ---- measurement ------------------------------------------------------------- */
 

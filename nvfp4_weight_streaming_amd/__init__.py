@@ -19,7 +19,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libnvfp4.so")
 
 OK, EINVAL, EUNSUPPORTED, EHIP, ESTATE = 0, 1, 2, 3, 4
-OUT_F32, OUT_BF16 = 0, 1
+OUT_F32, OUT_BF16, OUT_INT8 = 0, 1, 2
 PREFILL_AUTO, PREFILL_PIECES, PREFILL_STREAM_K = 0, 1, 2
 DECODE_MAX_M = 8
 VERIFY_MAX_M = 64
@@ -34,14 +34,19 @@ EXPORTS = (
     "nvfp4_workspace_clear",
     "nvfp4_round_workspace_bytes", "nvfp4_round_create", "nvfp4_round_run",
     "nvfp4_round_graph_nodes", "nvfp4_round_destroy",
+    "nvfp4_rms_norm", "nvfp4_int8_quantize", "nvfp4_int8_packed_bytes", "nvfp4_int8_pack",
+    "nvfp4_int8_unpack", "nvfp4_int8_gemm_workspace_bytes", "nvfp4_int8_gemm",
     "nvfp4_topk_workspace_bytes", "nvfp4_topk", "nvfp4_swiglu", "nvfp4_stream_read",
     "nvfp4_cache_append", "nvfp4_cache_compact", "nvfp4_cache_update",
     "nvfp4_cache_update_workspace_bytes", "nvfp4_tree_mask", "nvfp4_tree_attention",
     "nvfp4_tree_attention_workspace_bytes", "nvfp4_beam_select", "nvfp4_beam_workspace_bytes",
+    "nvfp4_logprobs_workspace_bytes", "nvfp4_logprobs",
 )
 TOPK_MAX_K = 64
 TREE_MAX_ROWS = 64
 BEAM_MAX_BEAMS = 64
+ROW_MAX_K = 1 << 24
+INT8_MAX_K = 131056
 CACHE_BF16, CACHE_E4M3 = 0, 1
 
 
@@ -89,6 +94,16 @@ class Rotary(ctypes.Structure):
                 ("pair_axis_dev", ctypes.c_void_p), ("axes", ctypes.c_int),
                 ("pairs", ctypes.c_int), ("interleaved", ctypes.c_int),
                 ("factor", ctypes.c_float)]
+
+
+class Norm(ctypes.Structure):
+    _fields_ = [("x_dev", ctypes.c_void_p), ("x_dtype", ctypes.c_int), ("x_ld", ctypes.c_int64),
+                ("residual_dev", ctypes.c_void_p), ("residual_out_dev", ctypes.c_void_p),
+                ("residual_dtype", ctypes.c_int), ("residual_ld", ctypes.c_int64),
+                ("weight_dev", ctypes.c_void_p), ("weight_dtype", ctypes.c_int),
+                ("weight_offset", ctypes.c_float), ("eps", ctypes.c_float),
+                ("out_dev", ctypes.c_void_p), ("out_dtype", ctypes.c_int),
+                ("out_ld", ctypes.c_int64), ("scale_dev", ctypes.c_void_p)]
 
 
 _lib = None
@@ -156,6 +171,18 @@ def lib():
         L.nvfp4_beam_workspace_bytes.restype = sz
         L.nvfp4_beam_select.argtypes = [vp, i, i64, i, i, i, vp, vp, i, i, vp, vp, vp, vp, vp, sz,
                                         vp]
+        L.nvfp4_rms_norm.argtypes = [c.POINTER(Norm), i, i, vp]
+        L.nvfp4_int8_quantize.argtypes = [vp, i, i64, i, i, i, vp, i64, vp, vp]
+        L.nvfp4_int8_packed_bytes.argtypes = [i, i]
+        L.nvfp4_int8_packed_bytes.restype = sz
+        L.nvfp4_int8_pack.argtypes = [vp, i, i, vp, vp]
+        L.nvfp4_int8_unpack.argtypes = [vp, i, i, vp, vp]
+        L.nvfp4_int8_gemm_workspace_bytes.argtypes = [i, i, i]
+        L.nvfp4_int8_gemm_workspace_bytes.restype = sz
+        L.nvfp4_int8_gemm.argtypes = [vp, i64, vp, vp, vp, vp, i, i, i, vp, i, i64, vp, sz, vp]
+        L.nvfp4_logprobs_workspace_bytes.argtypes = [i, i, i]
+        L.nvfp4_logprobs_workspace_bytes.restype = sz
+        L.nvfp4_logprobs.argtypes = [vp, i, i64, i, i, f, vp, i, i, vp, vp, vp, vp, vp, sz, vp]
         for name in EXPORTS:
             getattr(L, name)
         _lib = L
@@ -375,6 +402,244 @@ def beam_select(logits, beams, score, k, done=None, eos=-1, stream=None):
     if st:
         _check(st)
     return out, parent, token, ended
+
+
+def nvfp4_rms_norm(norm, rows, K, stream=None):
+    _check(lib().nvfp4_rms_norm(ctypes.byref(norm), rows, K, _stream(stream)))
+
+
+def nvfp4_int8_quantize(x, x_dtype, x_ld, rows, K, swiglu, codes, codes_ld, scale, stream=None):
+    _check(lib().nvfp4_int8_quantize(_ptr(x), x_dtype, x_ld, rows, K, swiglu, _ptr(codes),
+                                     codes_ld, _ptr(scale), _stream(stream)))
+
+
+def nvfp4_int8_packed_bytes(K, N) -> int:
+    return lib().nvfp4_int8_packed_bytes(K, N)
+
+
+def nvfp4_int8_pack(codes, K, N, packed, stream=None):
+    _check(lib().nvfp4_int8_pack(_ptr(codes), K, N, _ptr(packed), _stream(stream)))
+
+
+def nvfp4_int8_unpack(packed, K, N, codes, stream=None):
+    _check(lib().nvfp4_int8_unpack(_ptr(packed), K, N, _ptr(codes), _stream(stream)))
+
+
+def nvfp4_int8_gemm_workspace_bytes(M, K, N) -> int:
+    return lib().nvfp4_int8_gemm_workspace_bytes(M, K, N)
+
+
+def nvfp4_int8_gemm(a, a_ld, a_scale, w_packed, w_scale, bias, M, K, N, out, out_dtype, out_ld,
+                    workspace=None, workspace_bytes=0, stream=None):
+    _check(lib().nvfp4_int8_gemm(_ptr(a), a_ld, _ptr(a_scale), _ptr(w_packed), _ptr(w_scale),
+                                 _ptr(bias), M, K, N, _ptr(out), out_dtype, out_ld,
+                                 _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def nvfp4_logprobs_workspace_bytes(rows, V, k) -> int:
+    return lib().nvfp4_logprobs_workspace_bytes(rows, V, k)
+
+
+def nvfp4_logprobs(logits, logits_dtype, ld, rows, V, scale, tokens, n_tokens, k, logprob, entropy,
+                   top_token, top_logprob, workspace, workspace_bytes, stream=None):
+    _check(lib().nvfp4_logprobs(_ptr(logits), logits_dtype, ld, rows, V, scale, _ptr(tokens),
+                                n_tokens, k, _ptr(logprob), _ptr(entropy), _ptr(top_token),
+                                _ptr(top_logprob), _ptr(workspace), workspace_bytes,
+                                _stream(stream)))
+
+
+def _matrix(x, name, gpu, codes=(OUT_F32, OUT_BF16)):
+    """(rows, columns, row stride, type code) of a matrix of contiguous rows on a GPU; the stride of a
+    single row is never used, and is its columns."""
+    import torch
+    if not x.dim() == 2 or x.get_device() < 0 or x.get_device() != gpu:
+        _refuse("%s: not a matrix on %s GPU" % (name, "a" if gpu < 0 else "the call's"))
+    code = {torch.float32: OUT_F32, torch.bfloat16: OUT_BF16, torch.int8: OUT_INT8}.get(x.dtype)
+    if code not in codes:
+        _refuse("%s: of type %s" % (name, x.dtype))
+    (rows, cols), (ld, inner) = x.shape, x.stride()
+    if inner != 1 and cols > 1:
+        _refuse("%s: rows are not contiguous" % name)
+    return rows, cols, ld if rows > 1 else cols, code
+
+
+def _vector(x, n, dtype, name, gpu):
+    """Refuses anything but n contiguous values of a type on a GPU."""
+    if not (x.dtype is dtype and x.numel() == n and x.is_contiguous() and x.get_device() == gpu):
+        _refuse("%s: not %d contiguous %s values on the call's GPU" % (name, n, str(dtype).replace("torch.", "")))
+
+
+def rms_norm(x, weight, eps, residual=None, dtype=None, weight_offset=0.0, out=None, residual_out=None,
+             stream=None):
+    """Root-mean-square norm of a device fp32 or bf16 matrix [rows][K], or of the residual stream it is
+    added to, times ``weight + weight_offset`` ([K], fp32 or bf16).  ``dtype``: the output's, bfloat16 (as
+    by default), float32, or int8 for codes with a scale each row.  Returns ``out``; ``(codes, scale)`` for
+    int8; and the new residual stream as a last value if ``residual`` is given (``residual_out`` may be
+    ``residual`` itself).  A stream that is given is torch's current one during the call, so outputs belong
+    to it."""
+    import torch
+    if stream is not None and x.is_cuda:
+        with _on(stream, x.device):
+            return rms_norm(x, weight, eps, residual, dtype, weight_offset, out, residual_out)
+    gpu = x.get_device()
+    rows, K, x_ld, x_type = _matrix(x, "x", gpu)
+    wanted = {None: OUT_BF16, torch.bfloat16: OUT_BF16, torch.float32: OUT_F32, torch.int8: OUT_INT8}.get(dtype)
+    if wanted is None:
+        _refuse("dtype: %s" % dtype)
+    if weight.dtype not in (torch.float32, torch.bfloat16):
+        _refuse("weight: of type %s" % weight.dtype)
+    _vector(weight, K, weight.dtype, "weight", gpu)
+    if out is None:
+        out = torch.empty((rows, K), dtype=dtype or torch.bfloat16, device=x.device)
+    out_rows, cols, out_ld, _ = _matrix(out, "out", gpu, (wanted,))
+    if out_rows != rows or cols != K:
+        _refuse("out: shape %s, not %s" % (tuple(out.shape), (rows, K)))
+    n = Norm(x.data_ptr(), x_type, x_ld, None, None, 0, 0, weight.data_ptr(),
+             OUT_BF16 if weight.dtype is torch.bfloat16 else OUT_F32, weight_offset, eps, out.data_ptr(), wanted, out_ld, None)
+    if residual is not None:
+        shape = _matrix(residual, "residual", gpu)
+        if shape[:2] != (rows, K):
+            _refuse("residual: shape %s, not %s" % (tuple(residual.shape), (rows, K)))
+        if residual_out is None:
+            residual_out = torch.empty_strided(residual.shape, residual.stride(), dtype=residual.dtype, device=x.device)
+        if _matrix(residual_out, "residual_out", gpu) != shape:
+            _refuse("residual_out: not of the residual's shape, type and stride")
+        n.residual_dev, n.residual_out_dev = residual.data_ptr(), residual_out.data_ptr()
+        n.residual_dtype, n.residual_ld = shape[3], shape[2]
+    elif residual_out is not None:
+        _refuse("residual_out: without a residual")
+    got = [out]
+    if wanted == OUT_INT8:
+        got.append(torch.empty(rows, dtype=torch.float32, device=x.device))
+        n.scale_dev = got[1].data_ptr()
+    st = (_lib or lib()).nvfp4_rms_norm(ctypes.byref(n), rows, K, _current(x.device))
+    if st:
+        _check(st)
+    if residual is not None:
+        got.append(residual_out)
+    return tuple(got) if len(got) > 1 else out
+
+
+def int8_quantize(x, swiglu=False, codes=None, stream=None):
+    """(codes int8 [rows][K], scale fp32 [rows]) of a device fp32 or bf16 matrix [rows][K], or, with
+    ``swiglu``, of silu(gate) * up of one [rows][gate | up] of 2 K columns.  A stream that is given is
+    torch's current one during the call, so outputs belong to it."""
+    import torch
+    if stream is not None and x.is_cuda:
+        with _on(stream, x.device):
+            return int8_quantize(x, swiglu, codes)
+    gpu = x.get_device()
+    rows, K, x_ld, x_type = _matrix(x, "x", gpu)
+    if swiglu:
+        if K % 2:
+            _refuse("x: %d columns are not two halves" % K)
+        K //= 2
+    if codes is None:
+        codes = torch.empty((rows, K), dtype=torch.int8, device=x.device)
+    code_rows, cols, codes_ld, _ = _matrix(codes, "codes", gpu, (OUT_INT8,))
+    if code_rows != rows or cols != K:
+        _refuse("codes: shape %s, not %s" % (tuple(codes.shape), (rows, K)))
+    scale = torch.empty(rows, dtype=torch.float32, device=x.device)
+    st = (_lib or lib()).nvfp4_int8_quantize(x.data_ptr(), x_type, x_ld, rows, K, 1 if swiglu else 0, codes.data_ptr(), codes_ld,
+                                             scale.data_ptr(), _current(x.device))
+    if st:
+        _check(st)
+    return codes, scale
+
+
+class Int8Weight:
+    """A K x N matrix of 8-bit integers with one scale for each output channel, packed on the GPU."""
+
+    def __init__(self, packed, scale, K: int, N: int):
+        self.packed, self.scale, self.K, self.N = packed, scale, K, N
+
+    @classmethod
+    def from_canonical(cls, codes, scale, stream=None):
+        """Pack a device int8 matrix [N][K] with its channels' fp32 scales [N]."""
+        import torch
+        if stream is not None and codes.is_cuda:
+            with _on(stream, codes.device):
+                return cls.from_canonical(codes, scale)
+        gpu = codes.get_device()
+        N, K, ld, _ = _matrix(codes, "codes", gpu, (OUT_INT8,))
+        if ld != K:
+            _refuse("codes: rows are not next to each other")
+        _vector(scale, N, torch.float32, "scale", gpu)
+        packed = torch.empty(nvfp4_int8_packed_bytes(K, N), dtype=torch.int8, device=codes.device)
+        st = lib().nvfp4_int8_pack(codes.data_ptr(), K, N, packed.data_ptr(), _current(codes.device))
+        if st:
+            _check(st)
+        return cls(packed, scale, K, N)
+
+    @classmethod
+    def quantize(cls, w, stream=None):
+        """Quantise a device fp32 or bf16 matrix [N][K] and pack it."""
+        if stream is not None and w.is_cuda:
+            with _on(stream, w.device):
+                return cls.quantize(w)
+        return cls.from_canonical(*int8_quantize(w))
+
+
+def int8_gemm(codes, scale, weight, dtype=None, bias=None, out=None, stream=None):
+    """[M][N] product, bfloat16 (as by default) or float32, of a device int8 matrix [M][K] with its rows'
+    fp32 scales [M] and an ``Int8Weight``, plus ``bias`` (fp32 [N]).  A stream that is given is torch's
+    current one during the call, so outputs belong to it."""
+    import torch
+    if stream is not None and codes.is_cuda:
+        with _on(stream, codes.device):
+            return int8_gemm(codes, scale, weight, dtype, bias, out)
+    L, gpu, K, N = _lib or lib(), codes.get_device(), weight.K, weight.N
+    M, cols, ld, _ = _matrix(codes, "codes", gpu, (OUT_INT8,))
+    if cols != K:
+        _refuse("codes: %d columns, not the weight's K = %d" % (cols, K))
+    _vector(scale, M, torch.float32, "scale", gpu)
+    if weight.packed.get_device() != gpu or weight.scale.get_device() != gpu:
+        _refuse("weight: not on the call's GPU")
+    if bias is not None:
+        _vector(bias, N, torch.float32, "bias", gpu)
+    wanted = OUT_BF16 if dtype in (None, torch.bfloat16) else OUT_F32 if dtype is torch.float32 else _refuse("dtype: %s" % dtype)
+    if out is None:
+        out, out_ld = torch.empty((M, N), dtype=dtype or torch.bfloat16, device=codes.device), N
+    else:
+        rows, cols, out_ld, _ = _matrix(out, "out", gpu, (wanted,))
+        if rows != M or cols != N:
+            _refuse("out: shape %s, not %s" % (tuple(out.shape), (M, N)))
+    wsb = L.nvfp4_int8_gemm_workspace_bytes(M, K, N)
+    ws = torch.empty(wsb, dtype=torch.uint8, device=codes.device) if wsb else None
+    st = L.nvfp4_int8_gemm(codes.data_ptr(), ld, scale.data_ptr(), weight.packed.data_ptr(), weight.scale.data_ptr(),
+                           None if bias is None else bias.data_ptr(), M, K, N, out.data_ptr(), wanted, out_ld,
+                           None if ws is None else ws.data_ptr(), wsb, _current(codes.device))
+    if st:
+        _check(st)
+    return out
+
+
+def logprobs(logits, tokens, k=0, scale=1.0, stream=None):
+    """(logprob fp32 of the tokens' shape, entropy fp32 [rows], top_token int32 [rows][k], top_logprob fp32
+    [rows][k]) of a device fp32 or bf16 logits matrix [rows][V], times ``scale`` (an inverse temperature),
+    and int32 ``tokens`` [rows] or [rows][n].  A stream that is given is torch's current one during the
+    call, so outputs belong to it."""
+    import torch
+    if stream is not None and logits.is_cuda:
+        with _on(stream, logits.device):
+            return logprobs(logits, tokens, k, scale)
+    L, gpu, dev = _lib or lib(), logits.get_device(), logits.device
+    rows, V, ld, dtype = _matrix(logits, "logits", gpu)
+    if tokens.dim() not in (1, 2) or tokens.shape[0] != rows:
+        _refuse("tokens: shape %s does not go with %d rows" % (tuple(tokens.shape), rows))
+    n = tokens.shape[1] if tokens.dim() == 2 else 1
+    _vector(tokens, rows * n, torch.int32, "tokens", gpu)
+    logprob = torch.empty(tokens.shape, dtype=torch.float32, device=dev)
+    entropy = torch.empty(rows, dtype=torch.float32, device=dev)
+    top_token = torch.empty((rows, max(k, 0)), dtype=torch.int32, device=dev)
+    top = torch.empty((rows, max(k, 0)), dtype=torch.float32, device=dev)
+    wsb = L.nvfp4_logprobs_workspace_bytes(rows, V, k)
+    ws = torch.empty(wsb, dtype=torch.uint8, device=dev)
+    st = L.nvfp4_logprobs(logits.data_ptr(), dtype, ld, rows, V, scale, tokens.data_ptr(), n, k, logprob.data_ptr(),
+                          entropy.data_ptr(), top_token.data_ptr(), top.data_ptr(), ws.data_ptr(), wsb, _current(dev))
+    if st:
+        _check(st)
+    return logprob, entropy, top_token, top
 
 
 def nvfp4_gemm_create(max_M, K, N, out_dtype, split_k=0, waves=0, chunks=0, windows=0,

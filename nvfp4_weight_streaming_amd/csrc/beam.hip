@@ -21,7 +21,7 @@
 // go out at once, has none left to hide behind that work (its waves wait for 63% of their
 // time); 4 rows in fp32 3.5.  The second kernel is a chain of small reads and barriers:
 // 6.0 us for one request of 4 beams, 8.3 for 16 of 8.
-#include "key_device.h"
+#include "select_device.h"
 
 namespace nvfp4 {
 
@@ -134,35 +134,6 @@ __device__ __forceinline__ void load_group(const BeamArgs& a, int row, int group
     }
 }
 
-// The wave's maximum and sum, uniform: as wave_max64, within rows of 16 lanes by
-// DPP, then over the four rows.
-template <int CTRL>
-__device__ __forceinline__ float dppf(float v) {
-    return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(v), __float_as_int(v), CTRL, 0xF, 0xF, false));
-}
-__device__ __forceinline__ float lanef(float v, int lane) {
-    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
-}
-__device__ __forceinline__ float wave_max(float v) {
-    v = fmaxf(v, dppf<0xB1>(v));
-    v = fmaxf(v, dppf<0x4E>(v));
-    v = fmaxf(v, dppf<0x141>(v));
-    v = fmaxf(v, dppf<0x140>(v));
-    return fmaxf(fmaxf(lanef(v, 0), lanef(v, 16)), fmaxf(lanef(v, 32), lanef(v, 48)));
-}
-__device__ __forceinline__ float wave_sum(float v) {
-    v += dppf<0xB1>(v);
-    v += dppf<0x4E>(v);
-    v += dppf<0x141>(v);
-    v += dppf<0x140>(v);
-    return (lanef(v, 0) + lanef(v, 16)) + (lanef(v, 32) + lanef(v, 48));
-}
-// exp(x - m): the difference is rounded before it is scaled, so that terms near
-// the maximum, which make up the sum, are off by 2^-22 or less.
-__device__ __forceinline__ float exp_diff(float x, float m) {
-    return __builtin_amdgcn_exp2f((x - m) * 1.44269504088896340736f);
-}
-
 // A wave takes kBeamRun groups, all of their loads in flight at once.
 template <bool BF16, bool VEC>
 __global__ __launch_bounds__(kBeamThreads) void beam_scan_kernel(BeamArgs a) {
@@ -194,69 +165,8 @@ __global__ __launch_bounds__(kBeamThreads) void beam_scan_kernel(BeamArgs a) {
     }
 }
 
-// Merges the lane's N keys into the wave's sorted list (lane r: the r-th
-// largest; 0: none) and keeps the k largest.  Keys are distinct.
-template <int N>
-__device__ __forceinline__ u64 wave_keep(u64 kept, u64 (&x)[N], int k, int lane) {
-    u64 out = 0;
-    for (int r = 0; r < k; ++r) {
-        u64 head = kept;
-#pragma unroll
-        for (int j = 0; j < N; ++j) head = max64(head, x[j]);
-        const u64 top = wave_max64(head);
-        if (top == 0) break;
-        out = lane == r ? top : out;
-        kept = kept == top ? 0 : kept;
-#pragma unroll
-        for (int j = 0; j < N; ++j) x[j] = x[j] == top ? 0 : x[j];
-    }
-    return out;
-}
-
 __device__ __forceinline__ float beam_score(float c, float x, float m, float z) {
     return x == -__builtin_inff() ? x : c + ((x - m) - z);
-}
-
-// Appends the wave's keys that are at least `bar` to a list in LDS (in no
-// particular order); *count goes on past the list's end.
-__device__ __forceinline__ void append_keys(u64 key, bool take, u64* list, int* count, int lane) {
-    const unsigned long long mine = __ballot(take);
-    if (!mine) return;
-    int at = 0;
-    if (lane == 0) at = atomicAdd(count, __popcll(mine));
-    at = __builtin_amdgcn_readfirstlane(at) + __popcll(mine & ((1ull << lane) - 1ull));
-    if (take && at < kBeamList) list[at] = key;
-}
-
-// The k largest of n distinct keys, in order: a key's place is the number of
-// larger ones.  best[] past n is 0.
-__device__ __forceinline__ void rank_keys(const u64* list, int n, int k, u64* best) {
-    for (int i = threadIdx.x; i < n; i += kBeamPickThreads) {
-        const u64 x = list[i];
-        int place = 0;
-#pragma unroll 8
-        for (int j = 0; j < n; ++j) place += list[j] > x ? 1 : 0;
-        if (place < k) best[place] = x;
-    }
-    if ((int)threadIdx.x >= n && (int)threadIdx.x < k) best[threadIdx.x] = 0;
-}
-
-// Largest key of each row of 16 lanes, and the sum of a count, in all of its lanes.
-__device__ __forceinline__ u64 row_max64(u64 v) {
-    v = max64(v, dpp64<0xB1>(v));
-    v = max64(v, dpp64<0x4E>(v));
-    v = max64(v, dpp64<0x141>(v));
-    return max64(v, dpp64<0x140>(v));
-}
-template <int CTRL>
-__device__ __forceinline__ int dppi(int v) {
-    return __builtin_amdgcn_update_dpp(v, v, CTRL, 0xF, 0xF, false);
-}
-__device__ __forceinline__ int row_sum(int v) {
-    v += dppi<0xB1>(v);
-    v += dppi<0x4E>(v);
-    v += dppi<0x141>(v);
-    return v + dppi<0x140>(v);
 }
 
 template <bool BF16, bool VEC>
@@ -332,11 +242,11 @@ __global__ __launch_bounds__(kBeamPickThreads) void beam_pick_kernel(BeamArgs a)
     __syncthreads();
     for (int i0 = 0; i0 < n; i0 += kBeamPickThreads) {
         const u64 key = i0 ? group_key(i0 + mine) : own;
-        append_keys(key, key >= bar, list, &counts[0], lane);
+        append_keys<kBeamList>(key, key >= bar, list, &counts[0], lane);
     }
     __syncthreads();
     if (counts[0] <= kBeamList) {
-        rank_keys(list, counts[0], a.k, best);
+        rank_keys<kBeamPickThreads>(list, counts[0], a.k, best);
         __syncthreads();
     } else {
         // Too many pass (a large k over many beams): every wave keeps the k
@@ -376,12 +286,12 @@ __global__ __launch_bounds__(kBeamPickThreads) void beam_pick_kernel(BeamArgs a)
             }
         }
     };
-    for_candidates([&](u64 key) { append_keys(key, key >= floor, list, &counts[1], lane); });
+    for_candidates([&](u64 key) { append_keys<kBeamList>(key, key >= floor, list, &counts[1], lane); });
     __syncthreads();
     if (counts[1] <= kBeamList) {
         const int found = counts[1];
         __shared__ u64 winners[64];
-        rank_keys(list, found, a.k, winners);
+        rank_keys<kBeamPickThreads>(list, found, a.k, winners);
         __syncthreads();
         if (threadIdx.x < 64) best[threadIdx.x] = winners[threadIdx.x];
     } else {
@@ -391,14 +301,7 @@ __global__ __launch_bounds__(kBeamPickThreads) void beam_pick_kernel(BeamArgs a)
         __syncthreads();
         u64 kept = 0;
         for_candidates([&](u64 key) {
-            unsigned long long todo = __ballot(key >= floor && key > lane64(kept, a.k - 1));
-            while (todo) {
-                const u64 v = lane64(key, __ffsll(todo) - 1);
-                todo &= todo - 1;
-                u64 prev = ((u64)(unsigned int)__shfl_up((int)(kept >> 32), 1) << 32) | (unsigned int)__shfl_up((int)kept, 1);
-                if (lane == 0) prev = ~0ull;
-                kept = kept > v ? kept : prev > v ? v : prev;
-            }
+            kept = wave_insert(kept, key, key >= floor, a.k, lane);
         });
         list[wave * 64 + lane] = lane < a.k ? kept : 0;
         __syncthreads();
