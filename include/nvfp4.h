@@ -400,7 +400,7 @@ int nvfp4_rms_norm(const nvfp4_norm* norm, int rows, int K, void* stream);
 int nvfp4_int8_quantize(const void* x_dev, int x_dtype, int64_t x_ld, int rows, int K, int swiglu,
                         int8_t* codes_dev, int64_t codes_ld, float* scale_dev, void* stream);
 
-/* Bytes of a packed K x N matrix of codes: K padded to a multiple of 64 and N to one
+/* Bytes of a packed K x N matrix of codes: K padded to a multiple of 128 and N to one
  * of 16, with zeros.  0 for invalid K or N (K % 16 != 0, K < 16, K > NVFP4_INT8_MAX_K, N < 1). */
 size_t nvfp4_int8_packed_bytes(int K, int N);
 /* Permute codes [N][K] into the packed layout, 16-byte aligned, and back. */
@@ -408,16 +408,16 @@ int nvfp4_int8_pack(const int8_t* codes_dev, int K, int N, int8_t* packed_dev, v
 int nvfp4_int8_unpack(const int8_t* packed_dev, int K, int N, int8_t* codes_dev, void* stream);
 
 /* out[m][n] = float(sum_k a[m][k] * w[n][k]) * a_scale[m] * w_scale[n] + bias[n]
- * for m < M: the sum exact, then fp32 in this order, rounded once more to bf16 for
+ * for m < M <= 2^22: the sum exact, then fp32 in this order, rounded once more to bf16 for
  * NVFP4_OUT_BF16.
- *   a_dev         : codes [M][a_ld], 16-byte aligned, a_ld a multiple of 16, at least K
+ *   a_dev         : codes [M][a_ld], 16-byte aligned, a_ld a multiple of 16, from K to 2^22
  *   a_scale_dev   : [M];  w_scale_dev: [N];  bias_dev: fp32 [N], or NULL
  *   w_packed_dev  : packed codes (nvfp4_int8_pack), 16-byte aligned
  *   out_dev       : fp32 or bf16 [M][out_ld], out_ld >= N
- *   workspace_dev : nvfp4_int8_gemm_workspace_bytes(M, K, N) bytes (16-byte aligned; may be 0, for
- *                   M <= 64 always), any content; owned by the call while it runs.
- * M <= 64 streams the weights once; larger M runs tiles on the matrix cores.  Results do not depend on M, and
- * repeat to the bit.  M = 0 launches nothing.  Asynchronous on `stream`. */
+ *   workspace_dev : nvfp4_int8_gemm_workspace_bytes(M, K, N) bytes (16-byte aligned; may be 0),
+ *                   any content; owned by the call while it runs.
+ * Few rows stream the weights once; more run tiles on the matrix cores, cut along K where they are few.  Results do
+ * not depend on M, and repeat to the bit.  M = 0 launches nothing.  Asynchronous on `stream`. */
 size_t nvfp4_int8_gemm_workspace_bytes(int M, int K, int N);
 int nvfp4_int8_gemm(const int8_t* a_dev, int64_t a_ld, const float* a_scale_dev,
                     const int8_t* w_packed_dev, const float* w_scale_dev, const float* bias_dev,

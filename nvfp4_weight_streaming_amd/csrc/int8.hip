@@ -7,22 +7,18 @@
 // The weights are its first operand, so that a lane ends with four consecutive
 // outputs of one row.
 //
-// Packed weights: [ceil(N / 16)][ceil(K / 64)][lane][16 bytes], one 1 KiB operand
-// after the other as a wave reads them, zeros past K and N.  Past K an activation
-// is read from the row's last 16 values instead, and meets a zero.
-#include "common.h"
+// Packed weights lie one 1 KiB operand after the other as a wave reads them, zeros
+// past K and N.  What is read of a row past K (the next row, or zeros past the last) meets a zero.
+//
+// Up to 16 rows the weights are streamed (here); above, tiles run on the matrix cores
+// (int8_tile.hip): 64 rows of 17408 x 5120 take 23 us there.  16 of them take 23.7 here and 21.6 there, 16 of
+// 5120 x 152064 129 and 140, 8 of 5120 x 34816 28.8 and 41.
+#include "int8_device.h"
 
 namespace nvfp4 {
 
-typedef int i32x4 __attribute__((ext_vector_type(4)));
-typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
-constexpr int kI8Step = 64;                // k of an operand
-constexpr int kI8Bytes = 16 * kI8Step;     // bytes of an operand
-constexpr int kI8MaxSplit = 16;            // waves over K
-
-inline int i8_steps(int K) { return (K + kI8Step - 1) / kI8Step; }
-inline int i8_tiles(int N) { return (N + 15) / 16; }
-inline bool i8_shape(int K, int N) { return K >= 16 && K % 16 == 0 && K <= NVFP4_INT8_MAX_K && N >= 1; }
+constexpr int kI8MaxSplit = 16;    // waves over K
+constexpr int kI8StreamRows = 16;  // most rows of the streaming kernel
 
 // One 16-byte piece a thread; UNPACK: the other way, and no padding.
 template <bool UNPACK>
@@ -43,110 +39,88 @@ __global__ __launch_bounds__(256) void int8_pack_kernel(const int8_t* __restrict
     }
 }
 
-struct I8Args {
-    const int8_t* a;
-    const float* a_scale;
-    const int8_t* w;
-    const float* w_scale;
-    const float* bias;
-    void* out;
-    long long a_ld, out_ld;
-    int M, K, N, steps, tiles;
-    int vec;  // outputs are stored four at a time
-};
-
-__device__ __forceinline__ uint32_t i8_bf16(float x) {
-    const uint32_t u = __float_as_uint(x);
-    if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (u >> 16) | 0x40u;
-    return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
-}
-
-// Four outputs of row m from n on.
-template <bool BF16>
-__device__ __forceinline__ void i8_store(const I8Args& p, int m, int n, i32x4 acc) {
-    if (m >= p.M || n >= p.N) return;
-    const float as = p.a_scale[m];
-    float y[4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const int c = min(n + r, p.N - 1);
-        y[r] = (float)acc[r] * as * p.w_scale[c];
-        if (p.bias) y[r] += p.bias[c];
-    }
-    const long long at = (long long)m * p.out_ld + n;
-    if (p.vec && n + 4 <= p.N) {
-        if (BF16)
-            *(uint2*)((uint16_t*)p.out + at) = make_uint2(i8_bf16(y[0]) | i8_bf16(y[1]) << 16, i8_bf16(y[2]) | i8_bf16(y[3]) << 16);
-        else
-            *(float4*)((float*)p.out + at) = make_float4(y[0], y[1], y[2], y[3]);
-    } else {
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-            if (n + r < p.N) {
-                if (BF16)
-                    ((uint16_t*)p.out)[at + r] = (uint16_t)i8_bf16(y[r]);
-                else
-                    ((float*)p.out)[at + r] = y[r];
-            }
-    }
-}
-
-// Up to 16 G rows: a workgroup takes C column tiles over all of K, its waves
-// splitting K and adding in LDS.
-template <int G, int C, bool BF16>
+// Up to 16 rows: the weights are streamed once.  The waves of a workgroup split K, and each holds the
+// rows' part of its own steps (NP at most) in registers for all of the column tiles that the workgroup takes, one after
+// the other; the waves' sums meet in LDS.  A wave has U steps of weights in flight, those of the
+// next tile behind those of this one.
+//
+// (Read anew for each tile, rows cost as much of the vector cache's time as weights: 8 rows of 5120 x 34816 took
+// 35.0 us, and 29.2 with one load of them.)
+template <int NP, int U, bool BF16>
 __global__ __launch_bounds__(1024) void int8_stream_kernel(I8Args p) {
-    constexpr int U = 4;  // steps a wave has in flight
-    extern __shared__ i32x4 sums[];  // [wave][C][G][lane]
+    static_assert(NP % U == 0, "a step of any tile has one place");
+    extern __shared__ i32x4 sums[];  // [2][wave][lane]
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), lane = threadIdx.x & 63;
     const int waves = blockDim.x >> 6;
-    const int tile0 = blockIdx.x * C, row0 = blockIdx.y * 16 * G;
-    const int s0 = (int)((long long)p.steps * wave / waves), s1 = (int)((long long)p.steps * (wave + 1) / waves);
-    const int8_t* w[C];
-    const int8_t* a[G];
+    const int s0 = p.steps * wave / waves, n = p.steps * (wave + 1) / waves - s0;
+    const int row = lane & 15, quarter = lane >> 4;
+    // Steps past the wave's last one are read past the end of what their resource covers: zeros, with no
+    // branch and no traffic.
+    const __amdgpu_buffer_rsrc_t ra = i8_rsrc(p.a, (long long)(p.M - 1) * p.a_ld + p.K);
+    const int arow = min(row, p.M - 1) * (int)p.a_ld + s0 * kI8Step + 16 * quarter;
+    u32x4 av[NP], wv[U];
 #pragma unroll
-    for (int c = 0; c < C; ++c) w[c] = p.w + (long long)min(tile0 + c, p.tiles - 1) * p.steps * kI8Bytes + 16 * lane;
+    for (int i = 0; i < NP; ++i) av[i] = i8_load<0>(ra, i < n ? arow + i * kI8Step : 0x7FFFFFFF);
+    const long long stride = (long long)p.steps * kI8Bytes;
+    const int8_t* w = p.w + blockIdx.x * stride + s0 * kI8Bytes;
+    const long long jump = gridDim.x * stride;
+    __amdgpu_buffer_rsrc_t rw = i8_rsrc(w, n * kI8Bytes);
 #pragma unroll
-    for (int g = 0; g < G; ++g) a[g] = p.a + (long long)min(row0 + 16 * g + (lane & 15), p.M - 1) * p.a_ld;
-    const int k0 = 16 * (lane >> 4), kmax = p.K - 16;
-    i32x4 acc[C][G] = {};
-    for (int s = s0; s < s1; s += U) {
-        u32x4 wv[U][C], av[U][G];
+    for (int i = 0; i < U; ++i) wv[i] = i8_load<kI8Stream>(rw, 16 * lane + i * kI8Bytes);
+    const float as = p.a_scale[min(row, p.M - 1)];
+    int turn = 0, half = 0;  // the wave that stores the tile's outputs, and its place in LDS
+    for (int tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
+        w += jump;
+        const __amdgpu_buffer_rsrc_t next = i8_rsrc(w, tile + (int)gridDim.x < p.tiles ? n * kI8Bytes : 0);
+        const int c = tile * 16 + 4 * quarter;
+        float ws[4], bias[4];
+        if (wave == turn) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int t = min(s + u, s1 - 1);
-#pragma unroll
-            for (int c = 0; c < C; ++c) wv[u][c] = __builtin_nontemporal_load((const u32x4*)(w[c] + (long long)t * kI8Bytes));
-#pragma unroll
-            for (int g = 0; g < G; ++g) av[u][g] = *(const u32x4*)(a[g] + min(t * kI8Step + k0, kmax));
+            for (int r = 0; r < 4; ++r) {
+                ws[r] = p.w_scale[min(c + r, p.N - 1)];
+                bias[r] = p.bias ? p.bias[min(c + r, p.N - 1)] : 0.f;
+            }
         }
+        i32x4 acc = {};
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (s + u >= s1) break;
-#pragma unroll
-            for (int c = 0; c < C; ++c)
-#pragma unroll
-                for (int g = 0; g < G; ++g)
-                    acc[c][g] = __builtin_amdgcn_mfma_i32_16x16x64_i8((i32x4)wv[u][c], (i32x4)av[u][g], acc[c][g], 0, 0, 0);
+        for (int i = 0; i < NP; ++i) {
+            acc = __builtin_amdgcn_mfma_i32_16x16x64_i8((i32x4)wv[i % U], (i32x4)av[i], acc, 0, 0, 0);
+            wv[i % U] = i8_load<kI8Stream>(i + U < NP ? rw : next, 16 * lane + (i + U) % NP * kI8Bytes);
         }
-    }
-    if (waves > 1) {
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-#pragma unroll
-            for (int g = 0; g < G; ++g) sums[((wave * C + c) * G + g) * 64 + lane] = acc[c][g];
-        __syncthreads();
-        for (int i = wave; i < C * G; i += waves) {
-            i32x4 all = sums[i * 64 + lane];
-            for (int v = 1; v < waves; ++v) all += sums[(v * C * G + i) * 64 + lane];
-            i8_store<BF16>(p, row0 + 16 * (i % G) + (lane & 15), (tile0 + i / G) * 16 + 4 * (lane >> 4), all);
+        rw = next;
+        sums[(half * waves + wave) * 64 + lane] = acc;
+        // (no fence, which would wait for the weights in flight)
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        if (wave == turn) {
+            i32x4 all = sums[half * waves * 64 + lane];
+            for (int v = 1; v < waves; ++v) all += sums[(half * waves + v) * 64 + lane];
+            i8_store_scaled<BF16>(p, row, c, all, as, ws, bias);
         }
-    } else {
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-#pragma unroll
-            for (int g = 0; g < G; ++g) i8_store<BF16>(p, row0 + 16 * g + (lane & 15), (tile0 + c) * 16 + 4 * (lane >> 4), acc[c][g]);
+        turn = turn + 1 == waves ? 0 : turn + 1;
+        half ^= 1;
     }
 }
+
+template <int NP, int U>
+static int launch_stream(const I8Args& p, bool bf16, int waves, hipStream_t s) {
+    // As many workgroups as the device holds at once, or one for each tile.
+    const int room = device_cus() * (16 / waves);
+    const dim3 grid((unsigned)(p.tiles < room ? p.tiles : room)), block(64 * waves);
+    const size_t lds = (size_t)2 * waves * 64 * sizeof(i32x4);
+    if (bf16)
+        hipLaunchKernelGGL((int8_stream_kernel<NP, U, true>), grid, block, lds, s, p);
+    else
+        hipLaunchKernelGGL((int8_stream_kernel<NP, U, false>), grid, block, lds, s, p);
+    NVFP4_HIP(hipGetLastError());
+    return NVFP4_OK;
+}
+
+// Steps a wave, at most.
+constexpr int kI8MaxSteps = 20;
+static bool int8_streams(int M, int K) { return M <= kI8StreamRows && i8_steps(K) <= kI8MaxSplit * kI8MaxSteps; }
 
 }  // namespace nvfp4
 
@@ -187,7 +161,7 @@ int nvfp4_int8_unpack(const int8_t* packed_dev, int K, int N, int8_t* codes_dev,
 
 size_t nvfp4_int8_gemm_workspace_bytes(int M, int K, int N) {
     if (M < 1 || !i8_shape(K, N)) return 0;
-    return 0;
+    return int8_streams(M, K) ? 0 : int8_tile_ws(M, K, N);
 }
 
 int nvfp4_int8_gemm(const int8_t* a_dev, int64_t a_ld, const float* a_scale_dev, const int8_t* w_packed_dev,
@@ -198,7 +172,8 @@ int nvfp4_int8_gemm(const int8_t* a_dev, int64_t a_ld, const float* a_scale_dev,
     if (K < 16 || K % 16 || K > NVFP4_INT8_MAX_K) return set_error(NVFP4_EINVAL, "K: %d is not a multiple of 16 in [16, %d]", K, NVFP4_INT8_MAX_K);
     if (N < 1) return set_error(NVFP4_EINVAL, "N: %d < 1", N);
     if (out_dtype != NVFP4_OUT_F32 && out_dtype != NVFP4_OUT_BF16) return set_error(NVFP4_EINVAL, "out_dtype: %d", out_dtype);
-    if (a_ld < K || a_ld % 16) return set_error(NVFP4_EINVAL, "a_ld: %lld is not a multiple of 16 of at least K = %d", (long long)a_ld, K);
+    if (M > (1 << 22)) return set_error(NVFP4_EINVAL, "M: %d > 2^22", M);
+    if (a_ld < K || a_ld % 16 || a_ld > (1 << 22)) return set_error(NVFP4_EINVAL, "a_ld: %lld is not a multiple of 16 in [K = %d, 2^22]", (long long)a_ld, K);
     if (out_ld < N) return set_error(NVFP4_EINVAL, "out_ld: %lld < N = %d", (long long)out_ld, N);
     if (M == 0) return NVFP4_OK;
     const bool bf16 = out_dtype == NVFP4_OUT_BF16;
@@ -226,25 +201,20 @@ int nvfp4_int8_gemm(const int8_t* a_dev, int64_t a_ld, const float* a_scale_dev,
     p.steps = i8_steps(K);
     p.tiles = i8_tiles(N);
     p.vec = ((uintptr_t)out_dev & (bf16 ? 7 : 15)) == 0 && out_ld % 4 == 0;
+    p.wide = ((uintptr_t)out_dev & 15) == 0 && out_ld % (bf16 ? 8 : 4) == 0;
     const hipStream_t s = (hipStream_t)stream;
-    const int g = M <= 16 ? 1 : M <= 32 ? 2 : 4, c = g;
-    const int groups = (p.tiles + c - 1) / c, rows = (M + 16 * g - 1) / (16 * g);
+    if (!int8_streams(M, K)) return launch_int8_tile(p, bf16, workspace_dev, s);
+    // Four to eight steps a wave, where 16 waves are enough for that: 8 x 5120 x 152064 takes 121 us
+    // with 16 waves of 5 steps, 127 with 4 of 20; 8 x 1024 x 100000 18.4 with 4 of 4, 32 with 16 of 1. And
+    // waves for every compute unit, where there are few tiles.
     int waves = 4;
-    while (waves < kI8MaxSplit && (long long)groups * waves < 4096 && p.steps >= 8 * waves && waves * c * g < 64) waves *= 2;
+    while (waves < kI8MaxSplit && (p.steps > 8 * waves || ((long long)p.tiles * waves < 4096 && p.steps >= 8 * waves))) waves *= 2;
     if (waves > p.steps) waves = p.steps;
-    const dim3 grid((unsigned)groups, (unsigned)rows), block(64 * waves);
-    const size_t lds = (size_t)waves * c * g * 1024;
-#define NVFP4_STREAM(G, B)                                                                            \
-    if (g == G && bf16 == B) hipLaunchKernelGGL((int8_stream_kernel<G, G, B>), grid, block, lds, s, p);
-    NVFP4_STREAM(1, false)
-    NVFP4_STREAM(1, true)
-    NVFP4_STREAM(2, false)
-    NVFP4_STREAM(2, true)
-    NVFP4_STREAM(4, false)
-    NVFP4_STREAM(4, true)
-#undef NVFP4_STREAM
-    NVFP4_HIP(hipGetLastError());
-    return NVFP4_OK;
+    const int most = (p.steps + waves - 1) / waves;
+    if (most <= 4) return launch_stream<4, 4>(p, bf16, waves, s);
+    if (most <= 8) return launch_stream<8, 8>(p, bf16, waves, s);
+    if (most <= 12) return launch_stream<12, 4>(p, bf16, waves, s);
+    return launch_stream<20, 4>(p, bf16, waves, s);
 }
 
 }  // extern "C"

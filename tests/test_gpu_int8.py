@@ -38,7 +38,7 @@ def test_pack_is_a_bijection(nv, K, N):
     back = torch.zeros((N, K), dtype=torch.int8, device="cuda")
     nv.nvfp4_int8_unpack(p.packed, K, N, back)
     assert np.array_equal(host(back), w)
-    tiles, steps = -(-N // 16), -(-K // 64)
+    tiles, steps = -(-N // 16), 2 * -(-K // 128)
     whole = np.zeros((tiles * 16, steps * 64), np.int8)
     whole[:N, :K] = w
     want = whole.reshape(tiles, 16, steps, 4, 16).transpose(0, 2, 3, 1, 4)

@@ -77,7 +77,7 @@ def test_quantize_refuses(nv, bad, word):
 
 
 @pytest.mark.parametrize("bad,word", [
-    (dict(M=-1), "M"), (dict(K=0), "K"), (dict(K=24), "K"), (dict(K=131072), "K"), (dict(N=0), "N"), (dict(out_dtype=2), "out_dtype"),
+    (dict(M=-1), "M"), (dict(M=(1 << 22) + 1), "M"), (dict(a_ld=(1 << 22) + 16), "a_ld"), (dict(K=0), "K"), (dict(K=24), "K"), (dict(K=131072), "K"), (dict(N=0), "N"), (dict(out_dtype=2), "out_dtype"),
     (dict(a_ld=48), "a_ld"), (dict(a_ld=72), "a_ld"), (dict(out_ld=15), "out_ld"), (dict(a=None), "a"), (dict(a=P + 8), "a"),
     (dict(a_scale=None), "a_scale"), (dict(w_packed=P + 8), "w_packed"), (dict(w_scale=None), "w_scale"), (dict(bias=P + 1), "bias"),
     (dict(out=None), "out"), (dict(out=P + 1), "out"), (dict(out_dtype=0, out=P + 2), "out")], ids=str)
@@ -98,7 +98,7 @@ def test_logprobs_refuses(nv, bad, word):
 
 @pytest.mark.parametrize("K,N", [(16, 1), (64, 16), (80, 17), (5120, 152064)])
 def test_packed_sizes(nv, K, N):
-    assert nv.nvfp4_int8_packed_bytes(K, N) == -(-K // 64) * 64 * -(-N // 16) * 16
+    assert nv.nvfp4_int8_packed_bytes(K, N) == -(-K // 128) * 128 * -(-N // 16) * 16
 
 
 @pytest.mark.parametrize("K,N", [(0, 16), (8, 16), (24, 16), (16, 0), (-16, 4), (131072, 16)])
@@ -129,7 +129,7 @@ def test_workspace_sizes(nv):
     assert nv.nvfp4_logprobs_workspace_bytes(2, 4089, 0) == 2 * 16  # one unit, whatever the row's offset from 16 bytes
     assert nv.nvfp4_logprobs_workspace_bytes(2, 4090, 1) == 2 * 2 * (16 + 32)
     assert nv.nvfp4_int8_gemm_workspace_bytes(0, 64, 16) == 0 and nv.nvfp4_int8_gemm_workspace_bytes(4, 24, 16) == 0
-    for M in (1, 8, 64):
+    for M in (1, 8, 16):
         assert nv.nvfp4_int8_gemm_workspace_bytes(M, 5120, 152064) == 0
 
 
