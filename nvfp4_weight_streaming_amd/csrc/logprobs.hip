@@ -24,6 +24,7 @@ constexpr int kLpUnit = 4096;           // logits of a wave
 constexpr int kLpGroup = 512;
 constexpr int kLpGroups = kLpUnit / kLpGroup;
 constexpr int kLpThreads = 256;
+constexpr int kLpFew = 256;             // rows that the second kernel gives 1024 threads each
 constexpr int kLpList = 1024;           // keys the second kernel ranks at once
 constexpr float kLog2e = 1.44269504088896340736f;
 
@@ -129,50 +130,83 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_scan_kernel(LpArgs a) {
         v = fmaxf(v, __shfl_xor(v, 32));
         if (lane < kLpGroups) a.groups[((long long)row * a.units + unit) * kLpGroups + lane] = v;
     }
-    const float use = m == -__builtin_inff() ? 0.f : m, c = a.scale * kLog2e;
+    const float use = m == -__builtin_inff() ? 0.f : m, c = a.scale * kLog2e, mc = use * c;
     float s[4] = {0.f, 0.f, 0.f, 0.f}, t[4] = {0.f, 0.f, 0.f, 0.f};
+    // exp(scale (x - m)) as 2^(x c - m c), the product m c rounded: what that loses is the same for every term and
+    // put right once.  (The vector units bind here, with 40 cycles a logit of bf16: a difference and a product
+    // are one more of 4.)  Large maxima, or scales, take the difference first.
+    float sum, moment;
+    if (fabsf(mc) < 0x1p20f && c > 0x1p-60f && c < 0x1p60f) {
+        const float lost = __builtin_fmaf(use, c, -mc);
 #pragma unroll
-    for (int j = 0; j < J; ++j)
+        for (int j = 0; j < J; ++j)
 #pragma unroll
-        for (int e = 0; e < W; ++e) {
-            // (the difference is rounded before it is scaled; a NaN stays in s)
-            const float d = x[j][e] - use, p = __builtin_amdgcn_exp2f(d * c);
-            s[e % 4] += p;
-            t[e % 4] = __builtin_fmaf(p, fmaxf(d, -3e38f), t[e % 4]);
-        }
-    const float sum = wave_sum((s[0] + s[1]) + (s[2] + s[3])), moment = wave_sum((t[0] + t[1]) + (t[2] + t[3]));
+            for (int e = 0; e < W; ++e) {
+                const float z = __builtin_fmaf(x[j][e], c, -mc), p = __builtin_amdgcn_exp2f(z);
+                s[e % 4] += p;  // (a NaN stays in it)
+                t[e % 4] = __builtin_fmaf(p, fmaxf(z, -3e38f), t[e % 4]);
+            }
+        const float back = __builtin_amdgcn_exp2f(-lost);
+        sum = wave_sum((s[0] + s[1]) + (s[2] + s[3])) * back;
+        moment = (wave_sum((t[0] + t[1]) + (t[2] + t[3])) * back - lost * sum) / c;
+    } else {
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                const float d = x[j][e] - use, p = __builtin_amdgcn_exp2f(d * c);
+                s[e % 4] += p;
+                t[e % 4] = __builtin_fmaf(p, fmaxf(d, -3e38f), t[e % 4]);
+            }
+        sum = wave_sum((s[0] + s[1]) + (s[2] + s[3]));
+        moment = wave_sum((t[0] + t[1]) + (t[2] + t[3]));
+    }
     if (lane == 0) a.part[(long long)row * a.units + unit] = make_float4(m, sum, moment, 0.f);
 }
 
-// fp64 sum over the workgroup's four waves, in all threads; `lds` is used once.
-__device__ __forceinline__ double lp_sum(double v, double* lds) {
-#pragma unroll
-    for (int i = 1; i < 64; i <<= 1) v += __shfl_xor(v, i);
-    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+// The workgroup's sums of two fp64 values, in all threads.
+template <int WAVES>
+__device__ __forceinline__ void lp_sums(double& s, double& t, double (*lds)[WAVES]) {
+    s = wave_sumd(s);
+    t = wave_sumd(t);
+    if ((threadIdx.x & 63) == 0) {
+        lds[0][threadIdx.x >> 6] = s;
+        lds[1][threadIdx.x >> 6] = t;
+    }
     __syncthreads();
-    return (lds[0] + lds[1]) + (lds[2] + lds[3]);
+    s = lds[0][0];
+    t = lds[1][0];
+#pragma unroll
+    for (int i = 1; i < WAVES; ++i) {
+        s += lds[0][i];
+        t += lds[1][i];
+    }
 }
 
-template <bool BF16, bool TOP>
-__global__ __launch_bounds__(kLpThreads) void logprobs_finish_kernel(LpArgs a) {
-    constexpr int kWaves = kLpThreads / 64;
+// THREADS: 1024 for few rows, whose groups are then read by 16 waves at once; 256 for many.
+template <bool BF16, bool TOP, int THREADS>
+__global__ __launch_bounds__(THREADS) void logprobs_finish_kernel(LpArgs a) {
+    constexpr int kWaves = THREADS / 64;
     constexpr int W = BF16 ? 8 : 4;
-    static_assert(kWaves == 4, "lp_sum");
     __shared__ float row_m[kWaves];
     __shared__ double sums[2][kWaves];
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), lane = threadIdx.x & 63;
     const int row = blockIdx.x;
     const float4* part = a.part + (long long)row * a.units;
+    const int shift = lp_shift<BF16>(a, row), n = (int)(((long long)a.V + shift + kLpGroup - 1) / kLpGroup);
+    const float* groups = a.groups + (long long)row * a.units * kLpGroups;
 
     // The row's maximum, then its sums about it.
     float m = -__builtin_inff();
-    for (int i = threadIdx.x; i < a.units; i += kLpThreads) m = fmaxf(m, part[i].x);
+    for (int i = threadIdx.x; i < a.units; i += THREADS) m = fmaxf(m, part[i].x);
     m = wave_max(m);
     if (lane == 0) row_m[wave] = m;
     __syncthreads();
-    m = fmaxf(fmaxf(row_m[0], row_m[1]), fmaxf(row_m[2], row_m[3]));
+    m = row_m[0];
+#pragma unroll
+    for (int i = 1; i < kWaves; ++i) m = fmaxf(m, row_m[i]);
     double s = 0.0, t = 0.0;
-    for (int i = threadIdx.x; i < a.units; i += kLpThreads) {
+    for (int i = threadIdx.x; i < a.units; i += THREADS) {
         const float4 p = part[i];
         if (p.x == -__builtin_inff()) {
             s += p.y;  // 0, or NaN
@@ -182,8 +216,8 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_finish_kernel(LpArgs a) {
             if (f > 0) t += f * (p.z + d * p.y);
         }
     }
-    s = lp_sum(s, sums[0]);
-    t = lp_sum(t, sums[1]) * a.scale;
+    lp_sums<kWaves>(s, t, sums);
+    t *= a.scale;
     const double z = log(s);
     const bool none = s == 0.0;  // every logit is -inf
     auto logprob = [&](float x) -> float {
@@ -191,7 +225,7 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_finish_kernel(LpArgs a) {
         return (float)((double)a.scale * ((double)x - (double)m) - z);
     };
     if (threadIdx.x == 0 && a.entropy) a.entropy[row] = none ? 0.f : (float)(z - t / s);
-    for (int i = threadIdx.x; i < a.n_tokens; i += kLpThreads) {
+    for (int i = threadIdx.x; i < a.n_tokens; i += THREADS) {
         const long long at = (long long)row * a.n_tokens + i;
         const int token = a.tokens[at];
         a.logprob[at] = token >= 0 && token < a.V ? logprob(lp_at<BF16>(a, row, token)) : -__builtin_inff();
@@ -202,29 +236,38 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_finish_kernel(LpArgs a) {
     __shared__ u64 best[64], tops[64], bar;
     __shared__ int counts[2];
     if (threadIdx.x < 2) counts[threadIdx.x] = 0;
-    const int shift = lp_shift<BF16>(a, row), n = (int)(((long long)a.V + shift + kLpGroup - 1) / kLpGroup);
-    const float* groups = a.groups + (long long)row * a.units * kLpGroups;
-    auto group_key = [&](int i) -> u64 { return i < n ? topk_key(groups[i], max(0, i * kLpGroup - shift)) : 0; };
+    auto group_key = [&](int i) -> u64 {
+        return i < n ? topk_key(groups[i], max(0, i * kLpGroup - shift)) : 0;
+    };
 
     // The k best groups: what passes a bar that at least k pass is ranked.  The bar is
-    // the k-th largest of 64 maxima, each over the groups of four threads; threads 4
+    // the k-th largest of 64 maxima, each over the groups of `kPer` threads; threads kPer
     // apart take neighbouring groups, as the best of a row may lie together.
-    const int sub = threadIdx.x >> 2, mine = (threadIdx.x & 3) * 64 + sub;
+    constexpr int kPer = THREADS / 64;
+    const int sub = threadIdx.x / kPer, mine = threadIdx.x % kPer * 64 + sub;
     u64 head = 0;
-    for (int i = mine; i < n; i += kLpThreads) head = max64(head, group_key(i));
+    for (int i = mine; i < n; i += THREADS) head = max64(head, group_key(i));
     head = max64(head, dpp64<0xB1>(head));
     head = max64(head, dpp64<0x4E>(head));
-    if ((lane & 3) == 0) tops[sub] = head;
+    if (kPer == 16) {
+        head = max64(head, dpp64<0x141>(head));
+        head = max64(head, dpp64<0x140>(head));
+    }
+    if (lane % kPer == 0) tops[sub] = head;
     if (threadIdx.x == 0) bar = 1;  // fewer than k: all
     __syncthreads();
     int above = 0;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) above += tops[16 * (lane & 3) + j] > head ? 1 : 0;
+    for (int j = 0; j < 64 / kPer; ++j) above += tops[64 / kPer * (lane % kPer) + j] > head ? 1 : 0;
     above += dppi<0xB1>(above);
     above += dppi<0x4E>(above);
-    if (above == a.k - 1 && head) bar = head;  // (distinct keys: one quad)
+    if (kPer == 16) {
+        above += dppi<0x141>(above);
+        above += dppi<0x140>(above);
+    }
+    if (above == a.k - 1 && head) bar = head;  // (distinct keys: one sub)
     __syncthreads();
-    for (int i0 = 0; i0 < n; i0 += kLpThreads) {
+    for (int i0 = 0; i0 < n; i0 += THREADS) {
         const u64 key = group_key(i0 + mine);
         append_keys<kLpList>(key, key && key >= bar, list, &counts[0], lane);
     }
@@ -241,12 +284,12 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_finish_kernel(LpArgs a) {
         __syncthreads();
     };
     if (counts[0] <= kLpList) {
-        rank_keys<kLpThreads>(list, counts[0], a.k, best);
+        rank_keys<THREADS>(list, counts[0], a.k, best);
         __syncthreads();
     } else {  // too many pass (over half a million logits): the waves insert them one by one
         __syncthreads();
         u64 kept = 0;
-        for (int i0 = 0; i0 < n; i0 += kLpThreads) {
+        for (int i0 = 0; i0 < n; i0 += THREADS) {
             const u64 key = group_key(i0 + threadIdx.x);
             kept = wave_insert(kept, key, key != 0, a.k, lane);
         }
@@ -257,18 +300,29 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_finish_kernel(LpArgs a) {
     const u64 last = best[a.k - 1];
     const u64 floor = last ? ((last >> 32) << 32) | (unsigned int)((unsigned int)last - (kLpGroup - 1)) : 1;
     auto for_candidates = [&](auto&& f) {
-        for (int q = wave; q < a.k && best[q]; q += kWaves) {
-            const int group = ((int)~(unsigned int)best[q] + shift) / kLpGroup;
+        // (two groups of a wave at a time, read before either is looked at)
+        for (int q = wave; q < a.k; q += 2 * kWaves) {
+            constexpr int kV = kLpGroup / 64 / W;
+            float x[2][kV][W];
+            int first[2];
 #pragma unroll
-            for (int j = 0; j < kLpGroup / 64 / W; ++j) {
-                float x[W];
-                const int p = group * kLpGroup + (j * 64 + lane) * W;
-                lp_vector<BF16>(a, row, shift, p, x);
+            for (int g = 0; g < 2; ++g) {
+                const u64 key = q + g * kWaves < a.k ? best[q + g * kWaves] : 0;
+                first[g] = key ? ((int)~(unsigned int)key + shift) / kLpGroup * kLpGroup : -1;
+                if (first[g] >= 0)
 #pragma unroll
-                for (int e = 0; e < W; ++e) {
-                    const int token = p - shift + e;
-                    f(token >= 0 && token < a.V ? topk_key(x[e], token) : 0);
-                }
+                    for (int j = 0; j < kV; ++j) lp_vector<BF16>(a, row, shift, first[g] + (j * 64 + lane) * W, x[g][j]);
+            }
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                if (first[g] < 0) continue;
+#pragma unroll
+                for (int j = 0; j < kV; ++j)
+#pragma unroll
+                    for (int e = 0; e < W; ++e) {
+                        const int token = first[g] + (j * 64 + lane) * W - shift + e;
+                        f(token >= 0 && token < a.V ? topk_key(x[g][j][e], token) : 0);
+                    }
             }
         }
     };
@@ -276,7 +330,7 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_finish_kernel(LpArgs a) {
     __syncthreads();
     if (counts[1] <= kLpList) {
         __shared__ u64 winners[64];
-        rank_keys<kLpThreads>(list, counts[1], a.k, winners);
+        rank_keys<THREADS>(list, counts[1], a.k, winners);
         __syncthreads();
         if (threadIdx.x < 64) best[threadIdx.x] = winners[threadIdx.x];
         __syncthreads();
@@ -290,9 +344,10 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_finish_kernel(LpArgs a) {
         const u64 key = best[threadIdx.x];
         // (a NaN among the logits can leave a place empty: token 0)
         const int token = key ? (int)~(unsigned int)key : 0;
+        const unsigned int o = (unsigned int)(key >> 32);
         const long long at = (long long)row * a.k + threadIdx.x;
         a.top_token[at] = token;
-        a.top_logprob[at] = logprob(lp_at<BF16>(a, row, token));
+        a.top_logprob[at] = logprob(__uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o));
     }
 }
 
@@ -356,11 +411,15 @@ int nvfp4_logprobs(const void* logits_dev, int logits_dtype, int64_t ld, int row
     a.top_token = top_token_dev;
     a.top_logprob = top_logprob_dev;
     const hipStream_t s = (hipStream_t)stream;
+    const bool wide = rows <= kLpFew;
 #define NVFP4_LOGPROBS(B, T)                                                                                          \
     if (bf16 == B && (k > 0) == T) {                                                                                  \
         hipLaunchKernelGGL((logprobs_scan_kernel<B, T>), dim3((unsigned)(rows * blocks)), dim3(kLpThreads), 0, s, a); \
         NVFP4_HIP(hipGetLastError());                                                                                 \
-        hipLaunchKernelGGL((logprobs_finish_kernel<B, T>), dim3((unsigned)rows), dim3(kLpThreads), 0, s, a);          \
+        if (wide)                                                                                                     \
+            hipLaunchKernelGGL((logprobs_finish_kernel<B, T, 1024>), dim3((unsigned)rows), dim3(1024), 0, s, a);      \
+        else                                                                                                          \
+            hipLaunchKernelGGL((logprobs_finish_kernel<B, T, 256>), dim3((unsigned)rows), dim3(256), 0, s, a);        \
     }
     NVFP4_LOGPROBS(false, false)
     NVFP4_LOGPROBS(false, true)

@@ -29,6 +29,20 @@ __device__ __forceinline__ float wave_sum(float v) {
     v += dppf<0x140>(v);
     return (lanef(v, 0) + lanef(v, 16)) + (lanef(v, 32) + lanef(v, 48));
 }
+template <int CTRL>
+__device__ __forceinline__ double dppd(double v) {
+    return __longlong_as_double((long long)dpp64<CTRL>((u64)__double_as_longlong(v)));
+}
+__device__ __forceinline__ double laned(double v, int lane) {
+    return __longlong_as_double((long long)lane64((u64)__double_as_longlong(v), lane));
+}
+__device__ __forceinline__ double wave_sumd(double v) {
+    v += dppd<0xB1>(v);
+    v += dppd<0x4E>(v);
+    v += dppd<0x141>(v);
+    v += dppd<0x140>(v);
+    return (laned(v, 0) + laned(v, 16)) + (laned(v, 32) + laned(v, 48));
+}
 // exp(x - m): the difference is rounded before it is scaled, so that terms near
 // the maximum, which make up the sum, are off by 2^-22 or less.
 __device__ __forceinline__ float exp_diff(float x, float m) {

@@ -23,8 +23,8 @@ def _dev(x, bf16, ld, skip):
 
 def _check(nv, x, tokens, k, scale, bf16, pad=0, skip=0, what=""):
     """Every term of S is off by 2^-23 (the exponential) and by |z - max| 2^-23 (its argument: a product
-    and a rounded constant), and 24 additions in fp32 by 2^-24 each: eps = (26 + 2 E) 2^-24 of S, E the
-    mean of |z - max|.  So is a log probability, with its own rounding; and the entropy's mean, E, by eps E,
+    and a rounded constant), and 24 additions in fp32 by 2^-24 each; taking a unit's reference back is
+    another exponential and product, 3 2^-24: eps = (29 + 2 E) 2^-24 of S, E the mean of |z - max|.  So is a log probability, with its own rounding; and the entropy's mean, E, by eps E,
     by E2 2^-23 (E2 the mean square) and by eps E once more for its division by S."""
     import torch
     rows, V = x.shape
@@ -33,7 +33,7 @@ def _check(nv, x, tokens, k, scale, bf16, pad=0, skip=0, what=""):
     torch.cuda.synchronize()
     glp, gH, gtop, gtop_lp = (host(t).astype(np.float64) for t in got)
     assert np.array_equal(gtop, top), (what, np.argwhere(gtop != top)[:3], gtop[gtop != top][:3], top[gtop != top][:3])
-    eps = (26 + 2 * E) * 2.0 ** -24
+    eps = (29 + 2 * E) * 2.0 ** -24
 
     def near(a, b, tol, name):
         b = np.where(b < -3.4028235677973366e38, -np.inf, b)  # rounds to -inf: half a step past the largest fp32

@@ -174,3 +174,76 @@ def test_many_rows(nv):
     _same(codes, q, "codes")
     y, _ = oracle.rms_norm(x, np.ones(24), 1e-6)
     _same(nv.rms_norm(_dev(x, "bf16"), torch.ones(24, device="cuda"), 1e-6), oracle.bf16(y), "norm")
+
+
+def test_swiglu_of_extreme_gates(nv):
+    """Exponentials past fp32 either way, rows of nothing but such values, tiny and huge rows."""
+    rng = np.random.default_rng(11)
+    K = 1032
+    rows = []
+    for scale, up in ((30, 1), (100, 1), (300, 1), (1e4, 1e3), (1, 1e-25), (1e-25, 1), (1, 1e25), (60, 1e18), (120, 1e30), (3e37, 1), (1e-38, 1e-3)):
+        rows.append(np.concatenate([rng.standard_normal(K) * scale, rng.standard_normal(K) * up]))
+    rows.append(np.concatenate([np.full(K, -90.0), rng.standard_normal(K)]))      # every value below fp32's least
+    rows.append(np.concatenate([np.full(K, -88.0), rng.standard_normal(K) * 1e30]))
+    rows.append(np.concatenate([np.full(K, -300.0), rng.standard_normal(K) * 1e38]))
+    rows.append(np.concatenate([-np.abs(rng.standard_normal(K)) * 40, rng.standard_normal(K)]))
+    for name in ("f32", "bf16"):
+        with np.errstate(over="ignore"):
+            x = oracle.to_type(np.stack(rows), name)
+        q, s = oracle.codes(oracle.swiglu(x))
+        codes, scale = nv.int8_quantize(_dev(x, name), swiglu=True)
+        _same(scale, s, name)
+        _same(codes, q, name)
+
+
+def test_norm_of_extreme_rows(nv):
+    """Tiny and huge values and weights beside ordinary ones, to every type."""
+    import torch
+    rng = np.random.default_rng(12)
+    K = 520
+    x = rng.standard_normal((7, K))
+    x[0] *= 1e-38
+    x[1] *= 1e37
+    x[2, ::3] *= 1e-36
+    x[3, ::5] *= 1e-30
+    x[4] = 0
+    x[4, 7] = 1e-40
+    x[5, ::2] = 0
+    x[6, 1:] *= 1e-12
+    for w in (rng.standard_normal(K), np.zeros(K), rng.standard_normal(K) * 1e30, np.where(rng.random(K) < 0.5, 0, 1e-20), rng.standard_normal(K) * 2.0 ** 45):
+        for name in ("f32", "bf16"):
+            v, wv = oracle.to_type(x, name), oracle.to_type(w, "f32")
+            for eps in (0.0, 1e-6, 1e36):
+                y, _ = oracle.rms_norm(v, wv, eps)
+                wd = torch.from_numpy(wv.astype(np.float32)).cuda()
+                for t in ("bf16", "f32"):
+                    _same(nv.rms_norm(_dev(v, name), wd, eps, dtype=_types()[t]), oracle.to_type(y, t), (name, eps, t))
+                q, s = oracle.codes(y)
+                codes, scale = nv.rms_norm(_dev(v, name), wd, eps, dtype=torch.int8)
+                _same(scale, s, (name, eps))
+                _same(codes, q, (name, eps))
+
+
+def test_codes_of_many_draws(nv):
+    """Millions of values, tens of thousands of them next to a border of fp32's error."""
+    import torch
+    for seed in range(3):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        x = torch.randn((256, 8192), generator=g, device="cuda").to(torch.bfloat16)
+        for swiglu in (False, True):
+            y = x.double()
+            if swiglu:
+                y = y[:, :4096] * y[:, 4096:] / (1 + torch.exp(-y[:, :4096]))
+            s = (y.abs().amax(1) / 127).float()
+            codes, scale = nv.int8_quantize(x, swiglu=swiglu)
+            assert torch.equal(scale, s) and torch.equal(codes, torch.round(y / s.double()[:, None]).to(torch.int8))
+        h = x.double()
+        w = torch.randn(8192, generator=g, device="cuda").to(torch.bfloat16)
+        y = h * (h.square().mean(1, keepdim=True) + float(np.float32(1e-6))).rsqrt() * w.double()
+        s = (y.abs().amax(1) / 127).float()
+        codes, scale = nv.rms_norm(x, w, 1e-6, dtype=torch.int8)
+        assert torch.equal(scale, s) and torch.equal(codes, torch.round(y / s.double()[:, None]).to(torch.int8))
+        out = nv.rms_norm(x, w, 1e-6).double()
+        low = torch.nextafter(out.to(torch.bfloat16), torch.full_like(x, -float("inf"))).double()
+        high = torch.nextafter(out.to(torch.bfloat16), torch.full_like(x, float("inf"))).double()
+        assert ((y - out).abs() <= torch.minimum((y - low).abs(), (y - high).abs())).all()
