@@ -171,7 +171,7 @@ def lib():
         L.nvfp4_beam_workspace_bytes.restype = sz
         L.nvfp4_beam_select.argtypes = [vp, i, i64, i, i, i, vp, vp, i, i, vp, vp, vp, vp, vp, sz,
                                         vp]
-        L.nvfp4_rms_norm.argtypes = [c.POINTER(Norm), i, i, vp]
+        L.nvfp4_rms_norm.argtypes = [vp, i, i, vp]  # an nvfp4_norm
         L.nvfp4_int8_quantize.argtypes = [vp, i, i64, i, i, i, vp, i64, vp, vp]
         L.nvfp4_int8_packed_bytes.argtypes = [i, i]
         L.nvfp4_int8_packed_bytes.restype = sz
@@ -448,19 +448,50 @@ def nvfp4_logprobs(logits, logits_dtype, ld, rows, V, scale, tokens, n_tokens, k
                                 _stream(stream)))
 
 
-def _matrix(x, name, gpu, codes=(OUT_F32, OUT_BF16)):
-    """(rows, columns, row stride, type code) of a matrix of contiguous rows on a GPU; the stride of a
-    single row is never used, and is its columns."""
-    import torch
-    if not x.dim() == 2 or x.get_device() < 0 or x.get_device() != gpu:
+class _Torch:
+    """torch's types and calls that the functions below use, looked up once."""
+    known = None
+
+    def __init__(self):
+        import struct
+
+        import torch
+        self.f32, self.bf16, self.i8, self.i32, self.u8 = (torch.float32, torch.bfloat16, torch.int8, torch.int32,
+                                                           torch.uint8)
+        self.floats = {torch.float32: OUT_F32, torch.bfloat16: OUT_BF16}
+        self.outs = {None: OUT_BF16, **self.floats}
+        self.normed = {**self.outs, torch.int8: OUT_INT8}
+        self.empty, self.like = torch.empty, torch.empty_like
+        here = torch.cuda.is_available()
+        self.stream = torch._C._cuda_getCurrentRawStream if here else lambda gpu: 0
+        self.device = torch._C._cuda_getDevice if here else lambda: 0
+        self.on_device = torch.cuda.device
+        self.norm = struct.Struct("PiqPPiqPiffPiqP").pack  # an nvfp4_norm
+
+
+def _torch():
+    if _Torch.known is None:
+        _Torch.known = _Torch()
+    return _Torch.known
+
+
+def _bad_matrix(x, name, gpu, types):
+    """Names what is wrong with a matrix."""
+    if x.dim() != 2 or x.get_device() < 0 or x.get_device() != gpu:
         _refuse("%s: not a matrix on %s GPU" % (name, "a" if gpu < 0 else "the call's"))
-    code = {torch.float32: OUT_F32, torch.bfloat16: OUT_BF16, torch.int8: OUT_INT8}.get(x.dtype)
-    if code not in codes:
+    if x.dtype not in types:
         _refuse("%s: of type %s" % (name, x.dtype))
-    (rows, cols), (ld, inner) = x.shape, x.stride()
-    if inner != 1 and cols > 1:
+    if x.stride(1) != 1 and x.shape[1] > 1:
         _refuse("%s: rows are not contiguous" % name)
-    return rows, cols, ld if rows > 1 else cols, code
+
+
+def _matrix(x, name, gpu, types):
+    """(shape, row stride) of a matrix of contiguous rows on a GPU; the stride of a single row is never
+    used, and is its columns."""
+    if x.dim() != 2 or gpu < 0 or x.get_device() != gpu or x.dtype not in types or (x.stride(1) != 1 and x.shape[1] > 1):
+        _bad_matrix(x, name, gpu, types)
+    shape = x.shape
+    return shape, x.stride(0) if shape[0] > 1 else shape[1]
 
 
 def _vector(x, n, dtype, name, gpu):
@@ -477,71 +508,82 @@ def rms_norm(x, weight, eps, residual=None, dtype=None, weight_offset=0.0, out=N
     int8; and the new residual stream as a last value if ``residual`` is given (``residual_out`` may be
     ``residual`` itself).  A stream that is given is torch's current one during the call, so outputs belong
     to it."""
-    import torch
     if stream is not None and x.is_cuda:
         with _on(stream, x.device):
             return rms_norm(x, weight, eps, residual, dtype, weight_offset, out, residual_out)
-    gpu = x.get_device()
-    rows, K, x_ld, x_type = _matrix(x, "x", gpu)
-    wanted = {None: OUT_BF16, torch.bfloat16: OUT_BF16, torch.float32: OUT_F32, torch.int8: OUT_INT8}.get(dtype)
+    T, L, gpu = _Torch.known or _torch(), _lib or lib(), x.get_device()
+    if gpu != T.device() and gpu >= 0:  # launches go to the current device
+        with T.on_device(gpu):
+            return rms_norm(x, weight, eps, residual, dtype, weight_offset, out, residual_out)
+    shape, x_ld = _matrix(x, "x", gpu, T.floats)
+    rows, K = shape
+    wanted = T.normed.get(dtype)
     if wanted is None:
         _refuse("dtype: %s" % dtype)
-    if weight.dtype not in (torch.float32, torch.bfloat16):
+    w_type = T.floats.get(weight.dtype)
+    if w_type is None:
         _refuse("weight: of type %s" % weight.dtype)
     _vector(weight, K, weight.dtype, "weight", gpu)
     if out is None:
-        out = torch.empty((rows, K), dtype=dtype or torch.bfloat16, device=x.device)
-    out_rows, cols, out_ld, _ = _matrix(out, "out", gpu, (wanted,))
-    if out_rows != rows or cols != K:
-        _refuse("out: shape %s, not %s" % (tuple(out.shape), (rows, K)))
-    n = Norm(x.data_ptr(), x_type, x_ld, None, None, 0, 0, weight.data_ptr(),
-             OUT_BF16 if weight.dtype is torch.bfloat16 else OUT_F32, weight_offset, eps, out.data_ptr(), wanted, out_ld, None)
+        # (empty_like takes 0.9 us, new_empty 1.1, empty 1.5)
+        dtype = dtype or T.bf16
+        out = T.like(x) if x.dtype is dtype and x_ld == K else x.new_empty(shape, dtype=dtype)
+        out_ld = K
+    else:
+        out_shape, out_ld = _matrix(out, "out", gpu, (dtype or T.bf16,))
+        if out_shape != shape:
+            _refuse("out: shape %s, not %s" % (tuple(out.shape), (rows, K)))
+    scale = None
+    if wanted == OUT_INT8:
+        scale = T.empty(rows, dtype=T.f32, device=x.device)
+    r = r_out = r_type = r_ld = 0
     if residual is not None:
-        shape = _matrix(residual, "residual", gpu)
-        if shape[:2] != (rows, K):
+        r_shape, r_ld = _matrix(residual, "residual", gpu, T.floats)
+        if r_shape != shape:
             _refuse("residual: shape %s, not %s" % (tuple(residual.shape), (rows, K)))
+        r_type = T.floats[residual.dtype]
         if residual_out is None:
-            residual_out = torch.empty_strided(residual.shape, residual.stride(), dtype=residual.dtype, device=x.device)
-        if _matrix(residual_out, "residual_out", gpu) != shape:
+            residual_out = T.like(residual) if r_ld == K else residual.new_empty((rows, r_ld))[:, :K]
+        elif _matrix(residual_out, "residual_out", gpu, (residual.dtype,)) != (shape, r_ld):
             _refuse("residual_out: not of the residual's shape, type and stride")
-        n.residual_dev, n.residual_out_dev = residual.data_ptr(), residual_out.data_ptr()
-        n.residual_dtype, n.residual_ld = shape[3], shape[2]
+        r, r_out = residual.data_ptr(), residual_out.data_ptr()
     elif residual_out is not None:
         _refuse("residual_out: without a residual")
-    got = [out]
-    if wanted == OUT_INT8:
-        got.append(torch.empty(rows, dtype=torch.float32, device=x.device))
-        n.scale_dev = got[1].data_ptr()
-    st = (_lib or lib()).nvfp4_rms_norm(ctypes.byref(n), rows, K, _current(x.device))
+    st = L.nvfp4_rms_norm(T.norm(x.data_ptr(), T.floats[x.dtype], x_ld, r, r_out, r_type, r_ld, weight.data_ptr(), w_type,
+                                 weight_offset, eps, out.data_ptr(), wanted, out_ld,
+                                 0 if scale is None else scale.data_ptr()), rows, K, T.stream(gpu))
     if st:
         _check(st)
-    if residual is not None:
-        got.append(residual_out)
-    return tuple(got) if len(got) > 1 else out
+    if scale is None:
+        return out if residual is None else (out, residual_out)
+    return (out, scale) if residual is None else (out, scale, residual_out)
 
 
 def int8_quantize(x, swiglu=False, codes=None, stream=None):
     """(codes int8 [rows][K], scale fp32 [rows]) of a device fp32 or bf16 matrix [rows][K], or, with
     ``swiglu``, of silu(gate) * up of one [rows][gate | up] of 2 K columns.  A stream that is given is
     torch's current one during the call, so outputs belong to it."""
-    import torch
     if stream is not None and x.is_cuda:
         with _on(stream, x.device):
             return int8_quantize(x, swiglu, codes)
-    gpu = x.get_device()
-    rows, K, x_ld, x_type = _matrix(x, "x", gpu)
+    T, L, gpu = _Torch.known or _torch(), _lib or lib(), x.get_device()
+    if gpu != T.device() and gpu >= 0:  # launches go to the current device
+        with T.on_device(gpu):
+            return int8_quantize(x, swiglu, codes)
+    (rows, K), x_ld = _matrix(x, "x", gpu, T.floats)
     if swiglu:
         if K % 2:
             _refuse("x: %d columns are not two halves" % K)
         K //= 2
     if codes is None:
-        codes = torch.empty((rows, K), dtype=torch.int8, device=x.device)
-    code_rows, cols, codes_ld, _ = _matrix(codes, "codes", gpu, (OUT_INT8,))
-    if code_rows != rows or cols != K:
-        _refuse("codes: shape %s, not %s" % (tuple(codes.shape), (rows, K)))
-    scale = torch.empty(rows, dtype=torch.float32, device=x.device)
-    st = (_lib or lib()).nvfp4_int8_quantize(x.data_ptr(), x_type, x_ld, rows, K, 1 if swiglu else 0, codes.data_ptr(), codes_ld,
-                                             scale.data_ptr(), _current(x.device))
+        codes, codes_ld = T.empty((rows, K), dtype=T.i8, device=x.device), K
+    else:
+        shape, codes_ld = _matrix(codes, "codes", gpu, (T.i8,))
+        if shape != (rows, K):
+            _refuse("codes: shape %s, not %s" % (tuple(shape), (rows, K)))
+    scale = T.empty(rows, dtype=T.f32, device=x.device)
+    st = L.nvfp4_int8_quantize(x.data_ptr(), T.floats[x.dtype], x_ld, rows, K, 1 if swiglu else 0, codes.data_ptr(),
+                               codes_ld, scale.data_ptr(), T.stream(gpu))
     if st:
         _check(st)
     return codes, scale
@@ -556,17 +598,19 @@ class Int8Weight:
     @classmethod
     def from_canonical(cls, codes, scale, stream=None):
         """Pack a device int8 matrix [N][K] with its channels' fp32 scales [N]."""
-        import torch
         if stream is not None and codes.is_cuda:
             with _on(stream, codes.device):
                 return cls.from_canonical(codes, scale)
-        gpu = codes.get_device()
-        N, K, ld, _ = _matrix(codes, "codes", gpu, (OUT_INT8,))
+        T, gpu = _torch(), codes.get_device()
+        if gpu != T.device() and gpu >= 0:
+            with T.on_device(gpu):
+                return cls.from_canonical(codes, scale)
+        (N, K), ld = _matrix(codes, "codes", gpu, (T.i8,))
         if ld != K:
             _refuse("codes: rows are not next to each other")
-        _vector(scale, N, torch.float32, "scale", gpu)
-        packed = torch.empty(nvfp4_int8_packed_bytes(K, N), dtype=torch.int8, device=codes.device)
-        st = lib().nvfp4_int8_pack(codes.data_ptr(), K, N, packed.data_ptr(), _current(codes.device))
+        _vector(scale, N, T.f32, "scale", gpu)
+        packed = T.empty(nvfp4_int8_packed_bytes(K, N), dtype=T.i8, device=codes.device)
+        st = lib().nvfp4_int8_pack(codes.data_ptr(), K, N, packed.data_ptr(), T.stream(gpu))
         if st:
             _check(st)
         return cls(packed, scale, K, N)
@@ -584,31 +628,35 @@ def int8_gemm(codes, scale, weight, dtype=None, bias=None, out=None, stream=None
     """[M][N] product, bfloat16 (as by default) or float32, of a device int8 matrix [M][K] with its rows'
     fp32 scales [M] and an ``Int8Weight``, plus ``bias`` (fp32 [N]).  A stream that is given is torch's
     current one during the call, so outputs belong to it."""
-    import torch
     if stream is not None and codes.is_cuda:
         with _on(stream, codes.device):
             return int8_gemm(codes, scale, weight, dtype, bias, out)
-    L, gpu, K, N = _lib or lib(), codes.get_device(), weight.K, weight.N
-    M, cols, ld, _ = _matrix(codes, "codes", gpu, (OUT_INT8,))
+    T, L, gpu, K, N = _Torch.known or _torch(), _lib or lib(), codes.get_device(), weight.K, weight.N
+    if gpu != T.device() and gpu >= 0:  # launches go to the current device
+        with T.on_device(gpu):
+            return int8_gemm(codes, scale, weight, dtype, bias, out)
+    (M, cols), ld = _matrix(codes, "codes", gpu, (T.i8,))
     if cols != K:
         _refuse("codes: %d columns, not the weight's K = %d" % (cols, K))
-    _vector(scale, M, torch.float32, "scale", gpu)
+    _vector(scale, M, T.f32, "scale", gpu)
     if weight.packed.get_device() != gpu or weight.scale.get_device() != gpu:
         _refuse("weight: not on the call's GPU")
     if bias is not None:
-        _vector(bias, N, torch.float32, "bias", gpu)
-    wanted = OUT_BF16 if dtype in (None, torch.bfloat16) else OUT_F32 if dtype is torch.float32 else _refuse("dtype: %s" % dtype)
+        _vector(bias, N, T.f32, "bias", gpu)
+    wanted = T.outs.get(dtype)
+    if wanted is None:
+        _refuse("dtype: %s" % dtype)
     if out is None:
-        out, out_ld = torch.empty((M, N), dtype=dtype or torch.bfloat16, device=codes.device), N
+        out, out_ld = T.empty((M, N), dtype=dtype or T.bf16, device=codes.device), N
     else:
-        rows, cols, out_ld, _ = _matrix(out, "out", gpu, (wanted,))
-        if rows != M or cols != N:
-            _refuse("out: shape %s, not %s" % (tuple(out.shape), (M, N)))
+        shape, out_ld = _matrix(out, "out", gpu, (dtype or T.bf16,))
+        if shape != (M, N):
+            _refuse("out: shape %s, not %s" % (tuple(shape), (M, N)))
     wsb = L.nvfp4_int8_gemm_workspace_bytes(M, K, N)
-    ws = torch.empty(wsb, dtype=torch.uint8, device=codes.device) if wsb else None
+    ws = T.empty(wsb, dtype=T.u8, device=codes.device) if wsb else None
     st = L.nvfp4_int8_gemm(codes.data_ptr(), ld, scale.data_ptr(), weight.packed.data_ptr(), weight.scale.data_ptr(),
                            None if bias is None else bias.data_ptr(), M, K, N, out.data_ptr(), wanted, out_ld,
-                           None if ws is None else ws.data_ptr(), wsb, _current(codes.device))
+                           None if ws is None else ws.data_ptr(), wsb, T.stream(gpu))
     if st:
         _check(st)
     return out
@@ -616,27 +664,32 @@ def int8_gemm(codes, scale, weight, dtype=None, bias=None, out=None, stream=None
 
 def logprobs(logits, tokens, k=0, scale=1.0, stream=None):
     """(logprob fp32 of the tokens' shape, entropy fp32 [rows], top_token int32 [rows][k], top_logprob fp32
-    [rows][k]) of a device fp32 or bf16 logits matrix [rows][V], times ``scale`` (an inverse temperature),
-    and int32 ``tokens`` [rows] or [rows][n].  A stream that is given is torch's current one during the
-    call, so outputs belong to it."""
-    import torch
+    [rows][k]; the last two None for k = 0) of a device fp32 or bf16 logits matrix [rows][V], times
+    ``scale`` (an inverse temperature), and int32 ``tokens`` [rows] or [rows][n].  A stream that is given is
+    torch's current one during the call, so outputs belong to it."""
     if stream is not None and logits.is_cuda:
         with _on(stream, logits.device):
             return logprobs(logits, tokens, k, scale)
-    L, gpu, dev = _lib or lib(), logits.get_device(), logits.device
-    rows, V, ld, dtype = _matrix(logits, "logits", gpu)
-    if tokens.dim() not in (1, 2) or tokens.shape[0] != rows:
-        _refuse("tokens: shape %s does not go with %d rows" % (tuple(tokens.shape), rows))
-    n = tokens.shape[1] if tokens.dim() == 2 else 1
-    _vector(tokens, rows * n, torch.int32, "tokens", gpu)
-    logprob = torch.empty(tokens.shape, dtype=torch.float32, device=dev)
-    entropy = torch.empty(rows, dtype=torch.float32, device=dev)
-    top_token = torch.empty((rows, max(k, 0)), dtype=torch.int32, device=dev)
-    top = torch.empty((rows, max(k, 0)), dtype=torch.float32, device=dev)
+    T, L, gpu, dev = _Torch.known or _torch(), _lib or lib(), logits.get_device(), logits.device
+    if gpu != T.device() and gpu >= 0:  # launches go to the current device
+        with T.on_device(gpu):
+            return logprobs(logits, tokens, k, scale)
+    (rows, V), ld = _matrix(logits, "logits", gpu, T.floats)
+    asked = tokens.shape
+    if len(asked) not in (1, 2) or asked[0] != rows:
+        _refuse("tokens: shape %s does not go with %d rows" % (tuple(asked), rows))
+    n = asked[1] if len(asked) == 2 else 1
+    _vector(tokens, rows * n, T.i32, "tokens", gpu)
+    logprob = T.empty(asked, dtype=T.f32, device=dev)
+    entropy = logprob.new_empty(rows)
+    top_token = top = None
+    if k > 0:
+        top_token, top = tokens.new_empty((rows, k)), logprob.new_empty((rows, k))
     wsb = L.nvfp4_logprobs_workspace_bytes(rows, V, k)
-    ws = torch.empty(wsb, dtype=torch.uint8, device=dev)
-    st = L.nvfp4_logprobs(logits.data_ptr(), dtype, ld, rows, V, scale, tokens.data_ptr(), n, k, logprob.data_ptr(),
-                          entropy.data_ptr(), top_token.data_ptr(), top.data_ptr(), ws.data_ptr(), wsb, _current(dev))
+    ws = logprob.new_empty(wsb // 4)
+    st = L.nvfp4_logprobs(logits.data_ptr(), T.floats[logits.dtype], ld, rows, V, scale, tokens.data_ptr(), n, k,
+                          logprob.data_ptr(), entropy.data_ptr(), None if top is None else top_token.data_ptr(),
+                          None if top is None else top.data_ptr(), ws.data_ptr(), wsb, T.stream(gpu))
     if st:
         _check(st)
     return logprob, entropy, top_token, top
