@@ -4,7 +4,7 @@
 // the rows and 32 TJ of the outputs, as TI x TJ products of v_mfma_i32_32x32x32_i8 for each 32 k.
 //
 // Rows go through LDS, as the four waves share them: a ring of four stages, copied directly, three
-// stages ahead.  Each wave reads its own weights straight into registers, one stage ahead, in
+// stages ahead.  Each wave reads its own weights straight into registers, one or two stages ahead, in
 // the packed order, where a product's operand is two runs of 512 bytes.  Through LDS as well they
 // would double what its port carries and halve the workgroups that fit: 128 x 256 outputs (TI = 4, TJ = 2) take 67 KiB
 // and half the registers of a compute unit, so that two workgroups share it, and the one's
@@ -39,6 +39,17 @@ __device__ __forceinline__ void t_barrier() {
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 }
+
+struct TileNo {
+    static constexpr bool value = false;
+};
+struct TileYes {
+    static constexpr bool value = true;
+};
+
+// Stages of weights that a wave reads ahead: two where registers are left for them (64 x 5120 x 7168 in 32 x 128
+// tiles: 11.9 us, 13.4 one ahead; 64 x 128 tiles gain 1 to 4%).
+constexpr int t_ahead(int ti, int tj) { return ti * tj <= 2 ? 2 : 1; }
 
 // Stages u0 .. u1 - 1 of the tile at (m0, n0), added to acc.
 template <int TI, int TJ>
@@ -92,41 +103,52 @@ __device__ __forceinline__ void tile_sum(i32x16 (&acc)[TI][TJ], int8_t* lds, con
             for (int j = 0; j < TJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(w[j], a[i], acc[i][j], 0, 0, 0);
         __builtin_amdgcn_s_setprio(0);
     };
-    i32x4 w0[4][TJ], w1[4][TJ], a0[TI], a1[TI];
+    constexpr int kAhead = t_ahead(TI, TJ);
+    i32x4 w[kAhead + 1][4][TJ], a0[TI], a1[TI];
+    // (in the order in which stages would have issued them, which the waits below count on)
     copy(u0);
-    load(w0, u0);
+    __builtin_amdgcn_sched_barrier(0);
+    load(w[0], u0);
+    __builtin_amdgcn_sched_barrier(0);
     copy(u0 + 1);
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (kAhead == 2) load(w[1], u0 + 1);
+    __builtin_amdgcn_sched_barrier(0);
     copy(u0 + 2);
-    t_wait<2 * TI>();
+    __builtin_amdgcn_sched_barrier(0);
+    t_wait<2 * TI + 4 * TJ * (kAhead - 1)>();
     t_barrier();
     read(a0, u0, 0);
 
     // The barrier stands in the middle of a stage, so that no wave begins a stage with its operands
     // still to be read.  Behind it, stage u + 1 has landed for every wave, and all have left stage
     // u - 1, whose place the copy of stage u + 3 takes.
-    auto stage = [&](int u, const i32x4 (&w)[4][TJ], i32x4 (&next)[4][TJ]) {
-        load(next, u + 1);
+    auto stage = [&](int u, const i32x4 (&now)[4][TJ], i32x4 (&later)[4][TJ], auto last) {
+        load(later, u + kAhead);
         read(a1, u, 1);
-        multiply(w[0], a0);
+        multiply(now[0], a0);
         read(a0, u, 2);
-        multiply(w[1], a1);
+        multiply(now[1], a1);
         __builtin_amdgcn_sched_barrier(0);
-        // (what was issued after that copy, the next one and the weights above, may be in flight)
-        t_wait<TI + 4 * TJ>();
+        // What was issued after that copy may be in flight: the next one, the weights above and, two ahead, those
+        // before.  In the last stages the weights above are nobody's, and no load: only the next copy is counted on.
+        t_wait<TI + (last.value ? 0 : 4 * TJ * kAhead)>();
         t_barrier();
         copy(u + 3);
         __builtin_amdgcn_sched_barrier(0);
         read(a1, u, 3);
-        multiply(w[2], a0);
+        multiply(now[2], a0);
         read(a0, u + 1, 0);
-        multiply(w[3], a1);
+        multiply(now[3], a1);
     };
     int u = u0;
-    for (; u + 1 < u1; u += 2) {
-        stage(u, w0, w1);
-        stage(u + 1, w1, w0);
+    for (; u + kAhead < u1; u += kAhead + 1) {
+#pragma unroll
+        for (int i = 0; i <= kAhead; ++i) stage(u + i, w[i], w[(i + kAhead) % (kAhead + 1)], TileNo{});
     }
-    if (u < u1) stage(u, w0, w1);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        if (u + i < u1) stage(u + i, w[i], w[(i + kAhead) % (kAhead + 1)], TileYes{});
     // (no copy may land after the workgroup has left its LDS, or in what the outputs are turned in)
     t_wait<0>();
     t_barrier();
@@ -281,7 +303,7 @@ __global__ __launch_bounds__(256) void int8_join_kernel(I8Args p, TilePlan g) {
 // 50 choices on average, 8% at most:
 //   2048 x 5120 x 34816   322 us in 128 x 256 tiles, 389 in 128 x 128
 //   2048 x 5120 x 5120    60.0 in 128 x 128, 72.5 in 64 x 128
-//   256 x 5120 x 7168     16.2 in 64 x 128, 19.8 in 32 x 128, 21.4 in 128 x 128
+//   256 x 5120 x 7168     15.8 in 64 x 128, 18.9 in 32 x 128, 20.9 in 128 x 128
 //   128 x 17408 x 5120    27.0 in 6 pieces of 128 x 128, 79.6 in one
 struct TileChoice {
     int ti, tj, splits;
@@ -290,7 +312,7 @@ struct TileCost {
     int ti, tj;
     float alone, beside;
 };
-constexpr TileCost kTileCosts[] = {{4, 2, 0.80f, 0.84f}, {4, 1, 0.47f, 0.47f}, {2, 1, 0.33f, 0.34f}, {1, 1, 0.29f, 0.25f}};
+constexpr TileCost kTileCosts[] = {{4, 2, 0.80f, 0.84f}, {4, 1, 0.47f, 0.47f}, {2, 1, 0.33f, 0.34f}, {1, 1, 0.26f, 0.25f}};
 constexpr int kTMaxSplits = 12, kTMinStages = 4;  // of a piece
 
 static TileChoice choose_tile(int M, int K, int N) {

@@ -64,6 +64,18 @@ def test_product(nv, M):
             _check(out, y, s, bf16, (M, K, N, bf16))
 
 
+@pytest.mark.parametrize("M", [20, 70, 130, 300])
+def test_every_number_of_stages(nv, M):
+    """K in stages of 128, from one to more than the pieces of a long sum have; the last one whole or begun."""
+    import torch
+    for stages in list(range(1, 27)) + [40, 47, 62, 97, 136, 203]:
+        K, N = 128 * stages - 16 * (stages % 3), 300
+        a, sa, w, sw, _ = _case(M * 1000 + stages, M, K, N)
+        y, s = oracle.int8_gemm(a, sa, w, sw, None)
+        out = nv.int8_gemm(dev(a), dev(sa), nv.Int8Weight.from_canonical(dev(w), dev(sw)), dtype=torch.float32)
+        _check(out, y, s, False, (M, K, N))
+
+
 # The round's matrices and the head's width, by sampled columns; prefill chunks with ragged ends.
 @pytest.mark.parametrize("M,K,N", [(8, 5120, 7168), (3, 6144, 5120), (64, 17408, 5120), (8, 5120, 152064), (24, 5120, 34816),
                                    (2048, 5120, 7168), (2048, 6144, 5120), (1000, 17408, 5120), (333, 5136, 6001), (2048, 5120, 17408)])
