@@ -2,7 +2,7 @@
 //
 // For a row of logits x, z = scale * x:
 //     logprob(t) = z_t - log sum exp z,   entropy = log sum exp z - sum p z.
-// With d = x - m for a maximum m, S = sum exp(scale d) and T = sum exp(scale d) d carry
+// With d = scale (x - m) for a maximum m, S = sum exp d and T = sum d exp(d) / ln 2 carry
 // both over any part of a row, and two parts' join by the difference of their maxima.
 //
 // The first kernel reads the logits once, a wave 4096 of them (all loads in flight at
@@ -27,6 +27,7 @@ constexpr int kLpThreads = 256;
 constexpr int kLpFew = 256;             // rows that the second kernel gives 1024 threads each
 constexpr int kLpList = 1024;           // keys the second kernel ranks at once
 constexpr float kLog2e = 1.44269504088896340736f;
+constexpr double kLn2 = 0.69314718055994530942;
 
 struct LpArgs {
     const void* logits;
@@ -134,7 +135,8 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_scan_kernel(LpArgs a) {
     float s[4] = {0.f, 0.f, 0.f, 0.f}, t[4] = {0.f, 0.f, 0.f, 0.f};
     // exp(scale (x - m)) as 2^(x c - m c), the product m c rounded: what that loses is the same for every term and
     // put right once.  (The vector units bind here, with 40 cycles a logit of bf16: a difference and a product
-    // are one more of 4.)  Large maxima, or scales, take the difference first.
+    // are one more of 4.)  Large maxima, or scales, take the difference first, of halves: that of two fp32 values may
+    // pass fp32.  And they scale it before the constant, whose product with the largest scales is infinite.
     float sum, moment;
     if (fabsf(mc) < 0x1p20f && c > 0x1p-60f && c < 0x1p60f) {
         const float lost = __builtin_fmaf(use, c, -mc);
@@ -148,15 +150,15 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_scan_kernel(LpArgs a) {
             }
         const float back = __builtin_amdgcn_exp2f(-lost);
         sum = wave_sum((s[0] + s[1]) + (s[2] + s[3])) * back;
-        moment = (wave_sum((t[0] + t[1]) + (t[2] + t[3])) * back - lost * sum) / c;
+        moment = wave_sum((t[0] + t[1]) + (t[2] + t[3])) * back - lost * sum;
     } else {
 #pragma unroll
         for (int j = 0; j < J; ++j)
 #pragma unroll
             for (int e = 0; e < W; ++e) {
-                const float d = x[j][e] - use, p = __builtin_amdgcn_exp2f(d * c);
+                const float z = (0.5f * x[j][e] - 0.5f * use) * a.scale * (2.f * kLog2e), p = __builtin_amdgcn_exp2f(z);
                 s[e % 4] += p;
-                t[e % 4] = __builtin_fmaf(p, fmaxf(d, -3e38f), t[e % 4]);
+                t[e % 4] = __builtin_fmaf(p, fmaxf(z, -3e38f), t[e % 4]);
             }
         sum = wave_sum((s[0] + s[1]) + (s[2] + s[3]));
         moment = wave_sum((t[0] + t[1]) + (t[2] + t[3]));
@@ -211,13 +213,12 @@ __global__ __launch_bounds__(THREADS) void logprobs_finish_kernel(LpArgs a) {
         if (p.x == -__builtin_inff()) {
             s += p.y;  // 0, or NaN
         } else {
-            const double d = (double)p.x - (double)m, f = exp(a.scale * d);
+            const double d = a.scale * ((double)p.x - (double)m), f = exp(d);
             s += f * p.y;
-            if (f > 0) t += f * (p.z + d * p.y);
+            if (f > 0) t += f * (kLn2 * p.z + d * p.y);
         }
     }
     lp_sums<kWaves>(s, t, sums);
-    t *= a.scale;
     const double z = log(s);
     const bool none = s == 0.0;  // every logit is -inf
     auto logprob = [&](float x) -> float {

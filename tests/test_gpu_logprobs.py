@@ -121,3 +121,16 @@ def test_wide_rows(nv):
     x = np.stack([rng.standard_normal(V), np.zeros(V), np.arange(V) / 65536.0])
     _check(nv, oracle.to_type(x, "f32"), rng.integers(0, V, (3, 2)), 64, 1.0, False)
     _check(nv, oracle.to_type(x, "bf16"), rng.integers(0, V, (3, 2)), 5, 1.0, True, 1, 1)
+
+
+def test_scales_at_the_ends_of_their_range(nv):
+    """From the smallest fp32 to the largest: the best logits (several alike) against all others, and nearly
+    uniform rows with masked places."""
+    rng = np.random.default_rng(4)
+    apart = 2.0 * rng.integers(-2, 3, (4, 5000))
+    for scale in (1e18, 1e25, 3.4e38):
+        _check(nv, apart, rng.integers(0, 5000, (4, 3)), 12, scale, False, what=scale)
+    for scale, spread in ((1e-45, 1e38), (1e-40, 1e36), (2.0 ** -70, 2.0 ** 58)):
+        x = spread * rng.standard_normal((4, 5000))
+        x[:, ::7] = -np.inf
+        _check(nv, oracle.to_type(x, "f32"), rng.integers(0, 5000, (4, 3)), 12, scale, False, what=scale)
