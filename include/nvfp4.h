@@ -401,7 +401,7 @@ int nvfp4_int8_quantize(const void* x_dev, int x_dtype, int64_t x_ld, int rows, 
                         int8_t* codes_dev, int64_t codes_ld, float* scale_dev, void* stream);
 
 /* Bytes of a packed K x N matrix of codes: K padded to a multiple of 128 and N to one
- * of 16, with zeros.  0 for invalid K or N (K % 16 != 0, K < 16, K > NVFP4_INT8_MAX_K, N < 1). */
+ * of 16, with zeros.  0 for invalid K or N (K % 16 != 0, K < 16, K > NVFP4_INT8_MAX_K, N < 1, N > 2^30). */
 size_t nvfp4_int8_packed_bytes(int K, int N);
 /* Permute codes [N][K] into the packed layout, 16-byte aligned, and back. */
 int nvfp4_int8_pack(const int8_t* codes_dev, int K, int N, int8_t* packed_dev, void* stream);

@@ -137,7 +137,7 @@ static int int8_repack(const int8_t* from, const char* from_name, int8_t* to, co
                        void* stream) {
     clear_error();
     if (K < 16 || K % 16 || K > NVFP4_INT8_MAX_K) return set_error(NVFP4_EINVAL, "K: %d is not a multiple of 16 in [16, %d]", K, NVFP4_INT8_MAX_K);
-    if (N < 1) return set_error(NVFP4_EINVAL, "N: %d < 1", N);
+    if (N < 1 || N > (1 << 30)) return set_error(NVFP4_EINVAL, "N: %d outside [1, 2^30]", N);
     if (!from || ((uintptr_t)from & 15)) return set_error(NVFP4_EINVAL, "%s: NULL or not 16-byte aligned", from_name);
     if (!to || ((uintptr_t)to & 15)) return set_error(NVFP4_EINVAL, "%s: NULL or not 16-byte aligned", to_name);
     const int steps = i8_steps(K);
@@ -170,7 +170,7 @@ int nvfp4_int8_gemm(const int8_t* a_dev, int64_t a_ld, const float* a_scale_dev,
     clear_error();
     if (M < 0) return set_error(NVFP4_EINVAL, "M: %d < 0", M);
     if (K < 16 || K % 16 || K > NVFP4_INT8_MAX_K) return set_error(NVFP4_EINVAL, "K: %d is not a multiple of 16 in [16, %d]", K, NVFP4_INT8_MAX_K);
-    if (N < 1) return set_error(NVFP4_EINVAL, "N: %d < 1", N);
+    if (N < 1 || N > (1 << 30)) return set_error(NVFP4_EINVAL, "N: %d outside [1, 2^30]", N);
     if (out_dtype != NVFP4_OUT_F32 && out_dtype != NVFP4_OUT_BF16) return set_error(NVFP4_EINVAL, "out_dtype: %d", out_dtype);
     if (M > (1 << 22)) return set_error(NVFP4_EINVAL, "M: %d > 2^22", M);
     if (a_ld < K || a_ld % 16 || a_ld > (1 << 22)) return set_error(NVFP4_EINVAL, "a_ld: %lld is not a multiple of 16 in [K = %d, 2^22]", (long long)a_ld, K);

@@ -16,7 +16,7 @@ constexpr int kI8Bytes = 16 * kI8Step;  // bytes of an operand
 
 inline int i8_steps(int K) { return 2 * ((K + 127) / 128); }
 inline int i8_tiles(int N) { return (N + 15) / 16; }
-inline bool i8_shape(int K, int N) { return K >= 16 && K % 16 == 0 && K <= NVFP4_INT8_MAX_K && N >= 1; }
+inline bool i8_shape(int K, int N) { return K >= 16 && K % 16 == 0 && K <= NVFP4_INT8_MAX_K && N >= 1 && N <= (1 << 30); }
 
 struct I8Args {
     const int8_t* a;

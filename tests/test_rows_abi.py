@@ -146,3 +146,13 @@ def test_structure_matches_the_header(nv):
         subprocess.check_call(["gcc", "-I", os.path.join(root, "include"), "-o", os.path.join(d, "t"), os.path.join(d, "t.c")])
         got = [int(v) for v in subprocess.check_output([os.path.join(d, "t")]).split()]
     assert got == [getattr(nv.Norm, n).offset for n in names] + [ctypes.sizeof(nv.Norm)]
+
+
+def test_more_columns_than_an_index_holds(nv):
+    """Tiles' ends stay within 32 bits."""
+    big = (1 << 30) + 1
+    _refused(nv, "N", lambda: _gemm(nv, N=big, out_ld=big))
+    _refused(nv, "N", lambda: _gemm(nv, M=64, N=2 ** 31 - 1, out_ld=2 ** 31))
+    _refused(nv, "N", lambda: nv.nvfp4_int8_pack(P, 64, big, P, stream=0))
+    assert nv.nvfp4_int8_packed_bytes(64, big) == 0 and nv.nvfp4_int8_gemm_workspace_bytes(64, 64, big) == 0
+    assert nv.nvfp4_int8_packed_bytes(16, 1 << 30) == 128 << 30
