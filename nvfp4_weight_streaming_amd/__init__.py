@@ -448,6 +448,9 @@ def nvfp4_logprobs(logits, logits_dtype, ld, rows, V, scale, tokens, n_tokens, k
                                 _stream(stream)))
 
 
+_INT_MAX = 2 ** 31 - 1
+
+
 class _Torch:
     """torch's types and calls that the functions below use, looked up once."""
     known = None
@@ -491,6 +494,8 @@ def _matrix(x, name, gpu, types):
     if x.dim() != 2 or gpu < 0 or x.get_device() != gpu or x.dtype not in types or (x.stride(1) != 1 and x.shape[1] > 1):
         _bad_matrix(x, name, gpu, types)
     shape = x.shape
+    if shape[0] > _INT_MAX or shape[1] > _INT_MAX:  # what a C int would cut off
+        _refuse("%s: shape %s" % (name, tuple(shape)))
     return shape, x.stride(0) if shape[0] > 1 else shape[1]
 
 
@@ -593,6 +598,13 @@ class Int8Weight:
     """A K x N matrix of 8-bit integers with one scale for each output channel, packed on the GPU."""
 
     def __init__(self, packed, scale, K: int, N: int):
+        T, size = _torch(), nvfp4_int8_packed_bytes(K, N)
+        if not size:
+            _refuse("K, N: %d x %d cannot be packed" % (K, N))
+        if packed.dtype is not T.i8 or packed.numel() < size or not packed.is_contiguous():
+            _refuse("packed: not %d contiguous int8 values, or more" % size)
+        if scale.dtype is not T.f32 or scale.numel() != N or not scale.is_contiguous():
+            _refuse("scale: not %d contiguous float32 values" % N)
         self.packed, self.scale, self.K, self.N = packed, scale, K, N
 
     @classmethod
@@ -679,6 +691,10 @@ def logprobs(logits, tokens, k=0, scale=1.0, stream=None):
     if len(asked) not in (1, 2) or asked[0] != rows:
         _refuse("tokens: shape %s does not go with %d rows" % (tuple(asked), rows))
     n = asked[1] if len(asked) == 2 else 1
+    if n > 1024:
+        _refuse("tokens: %d of a row, more than 1024" % n)
+    if k > V:
+        _refuse("k: %d > V = %d" % (k, V))
     _vector(tokens, rows * n, T.i32, "tokens", gpu)
     logprob = T.empty(asked, dtype=T.f32, device=dev)
     entropy = logprob.new_empty(rows)

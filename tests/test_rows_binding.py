@@ -174,3 +174,39 @@ def test_the_tensors_device_is_made_current(nv, monkeypatch):
         seen.clear()
         f(**args)
         assert state == dict(device=1, entered=[0]) and len(seen) == 1, name
+
+
+def test_a_weight_of_other_sizes_is_refused(nv):
+    import torch
+    packed, scale = torch.zeros(64 * 128, dtype=torch.int8), torch.zeros(48)
+    nv.Int8Weight(packed[:48 * 128], scale, 64, 48)
+    nv.Int8Weight(packed, scale, 64, 48)
+    for bad, word in (((packed[:47 * 128], scale, 64, 48), "packed"), ((packed[:48 * 128], scale, 144, 48), "packed"),
+                      ((packed[:48 * 128].view(torch.uint8), scale, 64, 48), "packed"), ((packed[::2][:48 * 128], scale, 64, 48), "packed"),
+                      ((packed[:48 * 128], scale[:47], 64, 48), "scale"), ((packed[:48 * 128], scale.double(), 64, 48), "scale"),
+                      ((packed[:48 * 128], torch.zeros((48, 2))[:, 0], 64, 48), "scale"), ((packed, scale, 24, 48), "K, N"), ((packed, scale, 64, 0), "K, N")):
+        with pytest.raises(nv.Nvfp4Error, match="^.*" + word):
+            nv.Int8Weight(*bad)
+
+
+def test_sizes_past_a_c_integer_are_refused(nv, monkeypatch):
+    """Shapes alone: storage of one value, told to be larger."""
+    import torch
+    OnGpu = _gpu_class()
+    seen = _recorded(nv, monkeypatch)
+    tall = lambda t: torch.zeros(1, dtype=t).as_strided((2 ** 32 + 1, 1), (0, 1)).as_subclass(OnGpu)  # noqa: E731
+    wide = lambda t: torch.zeros(1, dtype=t).as_strided((1, 2 ** 32 + 16), (0, 0)).as_subclass(OnGpu)  # noqa: E731
+    put = lambda x: x.as_subclass(OnGpu)  # noqa: E731
+    one = put(torch.zeros(1))
+    w = nv.Int8Weight(put(torch.zeros(16 * 128, dtype=torch.int8)), one, 16, 1)
+    tokens = put(torch.zeros((1, 1), dtype=torch.int32))
+    for f in (lambda: nv.rms_norm(tall(torch.float32), one, 1e-6), lambda: nv.int8_quantize(tall(torch.bfloat16)),
+              lambda: nv.int8_gemm(tall(torch.int8), one, w), lambda: nv.logprobs(tall(torch.float32), tokens),
+              lambda: nv.Int8Weight.from_canonical(tall(torch.int8), one),
+              lambda: nv.logprobs(put(torch.zeros((1, 100))), torch.zeros(1, dtype=torch.int32).as_strided((1, 2 ** 32 + 1), (0, 0)).as_subclass(OnGpu)),
+              lambda: nv.logprobs(put(torch.zeros((1, 100))), tokens, k=2 ** 32 + 4)):
+        with pytest.raises(nv.Nvfp4Error):
+            f()
+    with pytest.raises(nv.Nvfp4Error):
+        nv.int8_quantize(wide(torch.float32))
+    assert not seen
