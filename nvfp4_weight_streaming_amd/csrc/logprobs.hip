@@ -198,9 +198,23 @@ __global__ __launch_bounds__(THREADS) void logprobs_finish_kernel(LpArgs a) {
     const int shift = lp_shift<BF16>(a, row), n = (int)(((long long)a.V + shift + kLpGroup - 1) / kLpGroup);
     const float* groups = a.groups + (long long)row * a.units * kLpGroups;
 
+    // What waits for nothing is read first, all at once: a token and its logit, the first unit and the first groups
+    // of each thread.
+    constexpr int kPer = THREADS / 64, kHeld = 2;
+    const int sub = threadIdx.x / kPer, mine = threadIdx.x % kPer * 64 + sub;
+    const float4 nothing = make_float4(-__builtin_inff(), 0.f, 0.f, 0.f);
+    const long long token_at = (long long)row * a.n_tokens + threadIdx.x;
+    const int token0 = (int)threadIdx.x < a.n_tokens ? a.tokens[token_at] : -1;
+    const float4 part0 = (int)threadIdx.x < a.units ? part[threadIdx.x] : nothing;
+    float held[kHeld];
+    if (TOP)
+#pragma unroll
+        for (int c = 0; c < kHeld; ++c) held[c] = mine + c * THREADS < n ? groups[mine + c * THREADS] : 0.f;
+    const float logit0 = token0 >= 0 && token0 < a.V ? lp_at<BF16>(a, row, token0) : -__builtin_inff();
+
     // The row's maximum, then its sums about it.
-    float m = -__builtin_inff();
-    for (int i = threadIdx.x; i < a.units; i += THREADS) m = fmaxf(m, part[i].x);
+    float m = part0.x;
+    for (int i = threadIdx.x + THREADS; i < a.units; i += THREADS) m = fmaxf(m, part[i].x);
     m = wave_max(m);
     if (lane == 0) row_m[wave] = m;
     __syncthreads();
@@ -209,7 +223,7 @@ __global__ __launch_bounds__(THREADS) void logprobs_finish_kernel(LpArgs a) {
     for (int i = 1; i < kWaves; ++i) m = fmaxf(m, row_m[i]);
     double s = 0.0, t = 0.0;
     for (int i = threadIdx.x; i < a.units; i += THREADS) {
-        const float4 p = part[i];
+        const float4 p = i < THREADS ? part0 : part[i];
         if (p.x == -__builtin_inff()) {
             s += p.y;  // 0, or NaN
         } else {
@@ -228,8 +242,9 @@ __global__ __launch_bounds__(THREADS) void logprobs_finish_kernel(LpArgs a) {
     if (threadIdx.x == 0 && a.entropy) a.entropy[row] = none ? 0.f : (float)(z - t / s);
     for (int i = threadIdx.x; i < a.n_tokens; i += THREADS) {
         const long long at = (long long)row * a.n_tokens + i;
-        const int token = a.tokens[at];
-        a.logprob[at] = token >= 0 && token < a.V ? logprob(lp_at<BF16>(a, row, token)) : -__builtin_inff();
+        const int token = i < THREADS ? token0 : a.tokens[at];
+        const bool real = token >= 0 && token < a.V;
+        a.logprob[at] = real ? logprob(i < THREADS ? logit0 : lp_at<BF16>(a, row, token)) : -__builtin_inff();
     }
     if (!TOP) return;
 
@@ -237,17 +252,16 @@ __global__ __launch_bounds__(THREADS) void logprobs_finish_kernel(LpArgs a) {
     __shared__ u64 best[64], tops[64], bar;
     __shared__ int counts[2];
     if (threadIdx.x < 2) counts[threadIdx.x] = 0;
-    auto group_key = [&](int i) -> u64 {
-        return i < n ? topk_key(groups[i], max(0, i * kLpGroup - shift)) : 0;
-    };
+    auto key_of = [&](int i, float v) -> u64 { return i < n ? topk_key(v, max(0, i * kLpGroup - shift)) : 0; };
+    auto group_key = [&](int i) -> u64 { return i < n ? key_of(i, groups[i]) : 0; };
 
     // The k best groups: what passes a bar that at least k pass is ranked.  The bar is
     // the k-th largest of 64 maxima, each over the groups of `kPer` threads; threads kPer
     // apart take neighbouring groups, as the best of a row may lie together.
-    constexpr int kPer = THREADS / 64;
-    const int sub = threadIdx.x / kPer, mine = threadIdx.x % kPer * 64 + sub;
     u64 head = 0;
-    for (int i = mine; i < n; i += THREADS) head = max64(head, group_key(i));
+#pragma unroll
+    for (int c = 0; c < kHeld; ++c) head = max64(head, key_of(mine + c * THREADS, held[c]));
+    for (int i = mine + kHeld * THREADS; i < n; i += THREADS) head = max64(head, group_key(i));
     head = max64(head, dpp64<0xB1>(head));
     head = max64(head, dpp64<0x4E>(head));
     if (kPer == 16) {
@@ -268,7 +282,12 @@ __global__ __launch_bounds__(THREADS) void logprobs_finish_kernel(LpArgs a) {
     }
     if (above == a.k - 1 && head) bar = head;  // (distinct keys: one sub)
     __syncthreads();
-    for (int i0 = 0; i0 < n; i0 += THREADS) {
+#pragma unroll
+    for (int c = 0; c < kHeld; ++c) {
+        const u64 key = key_of(mine + c * THREADS, held[c]);
+        append_keys<kLpList>(key, key && key >= bar, list, &counts[0], lane);
+    }
+    for (int i0 = kHeld * THREADS; i0 < n; i0 += THREADS) {
         const u64 key = group_key(i0 + mine);
         append_keys<kLpList>(key, key && key >= bar, list, &counts[0], lane);
     }
