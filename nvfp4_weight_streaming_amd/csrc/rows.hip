@@ -13,7 +13,10 @@
 // (All of it in fp64, the SwiGLU of 2048 x 17408 took 124 us, and its exponentials and divisions were what it waited for.)
 //
 // A row is read once: 64, 256 or 1024 threads hold up to 3 vectors of 8 values each (1536, 6144, 24576 values);
-// longer rows are read again for each step.  Few rows take 1024 threads each, for less work one after the other.
+// longer rows are read again for each step.  From 4097 to 8192 values 1024 threads hold a vector each: always above
+// 6144, where three would leave a compute unit fewer rows (codes of 1024 SwiGLU rows of 8192: 15.4 us, 20.1 so; of 8: 5.4 and 6.5),
+// and below it for few rows, for less work one after the other (codes of 64 rows of 5120: 4.4 us, 6.3 with 256 threads;
+// 512 rows 6.4 and 6.8, 1024 rows 10.7 and 9.6; 8 rows of 2048 would take 4.3 and 3.7).
 #include "select_device.h"
 #include "swiglu_device.h"
 
@@ -22,7 +25,7 @@ namespace nvfp4 {
 enum { kRowNorm = 0, kRowPlain = 1, kRowSwiglu = 2 };
 enum { kRowNone = -1 };  // a type: there is no such operand
 constexpr int kRowMaxRows = (1 << 22) - 1;  // a launch has fewer than 2^32 threads
-constexpr int kRowFew = 512;  // rows that take 1024 threads each
+constexpr int kRowFew = 512;
 constexpr int kRowVecs = 3;  // vectors of 8 values a thread holds
 
 struct RowArgs {
@@ -466,16 +469,15 @@ __global__ __launch_bounds__(T < 256 ? 256 : T, T == 1024 && B16 && MODE != kRow
 
 template <int MODE, int OUT>
 int launch_rows(const RowArgs& a, bool vec, hipStream_t s) {
-    // Few rows: 1024 threads and one vector each.
-    const bool few = vec && a.rows <= kRowFew && a.K > 512 && a.K <= 8192;
-    const int t = few ? 1024 : a.K <= 64 * kRowVecs * 8 ? 64 : a.K <= 256 * kRowVecs * 8 ? 256 : 1024;
+    const bool single = vec && a.K > 4096 && a.K <= 8192 && (a.rows <= kRowFew || a.K > 256 * kRowVecs * 8);
+    const int t = single ? 1024 : a.K <= 64 * kRowVecs * 8 ? 64 : a.K <= 256 * kRowVecs * 8 ? 256 : 1024;
     // (unaligned rows of 1024 threads would not fit the registers)
     const bool held = a.K <= t * kRowVecs * 8 && (vec || t < 1024);
     const unsigned grid = t == 64 ? (unsigned)((a.rows + 3) / 4) : (unsigned)a.rows;
     const bool b16 = vec && a.x_type == NVFP4_OUT_BF16 && (!a.residual || a.residual_type == NVFP4_OUT_BF16) &&
                      (MODE != kRowNorm || a.weight_type == NVFP4_OUT_BF16);
 #define NVFP4_ROWS(T, R, V, H, B)                                                                             \
-    if (t == T && few == (R == 1) && vec == V && held == H && b16 == B)                                       \
+    if (t == T && single == (R == 1) && vec == V && held == H && b16 == B)                                       \
         hipLaunchKernelGGL((rows_kernel<T, R, MODE, OUT, V, H, B>), dim3(grid), dim3(T < 256 ? 256 : T), 0, s, a);
     NVFP4_ROWS(1024, 1, true, true, true)
     NVFP4_ROWS(1024, 1, true, true, false)
