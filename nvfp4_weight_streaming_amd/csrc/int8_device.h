@@ -89,18 +89,6 @@ __device__ __forceinline__ void i8_store_scaled(const I8Args& p, int m, int n, i
             }
     }
 }
-template <bool BF16>
-__device__ __forceinline__ void i8_store(const I8Args& p, int m, int n, i32x4 acc) {
-    if (m >= p.M || n >= p.N) return;
-    float ws[4], bias[4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const int c = min(n + r, p.N - 1);
-        ws[r] = p.w_scale[c];
-        bias[r] = p.bias ? p.bias[c] : 0.f;
-    }
-    i8_store_scaled<BF16>(p, m, n, acc, p.a_scale[m], ws, bias);
-}
 
 // Launchers (no validation).
 int launch_int8_tile(const I8Args& p, bool bf16, void* ws, hipStream_t s);

@@ -20,6 +20,8 @@ typedef int i32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kTK = 128;           // k of a stage
 constexpr int kTRing = 4;          // stages in LDS
+constexpr int kTMaxSplits = 12;    // pieces along K
+constexpr int kTMinStages = 4;     // stages of a piece
 constexpr int t_stage_bytes(int ti) { return 32 * ti * kTK; }
 
 __device__ __forceinline__ int t_key(int row) { return (row >> 1) & 7; }
@@ -280,20 +282,30 @@ __global__ __launch_bounds__(256, 2) void int8_tile_kernel(I8Args p, TilePlan g)
                 part[((i * TJ + j) * 4 + q) * 64] = i32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
 }
 
-// The pieces' sums and the outputs, four a thread.
+// The pieces' sums and the outputs, four a thread, all pieces in flight at once (those past the last read zero).
 template <int TI, int TJ, bool BF16>
 __global__ __launch_bounds__(256) void int8_join_kernel(I8Args p, TilePlan g) {
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-    constexpr int kTile = TI * TJ * 1024;  // groups of four
-    const int t = (int)(i / kTile), at = (int)(i % kTile);
+    constexpr int kTile = TI * TJ * 1024, kBlocks = kTile / 256;  // groups of four; workgroups of a tile
+    const int t = blockIdx.x / kBlocks, at = blockIdx.x % kBlocks * 256 + threadIdx.x;
     const int lane = at & 63, q = at >> 6 & 3, j = at / 256 % TJ, k = at / (256 * TJ) % TI, wave = at / (256 * TI * TJ);
     const int m = t % g.mblocks * 32 * TI + 32 * k + (lane & 31);
     const int n = t / g.mblocks * 128 * TJ + wave * 32 * TJ + 32 * j + 8 * q + 4 * (lane >> 5);
     if (m >= p.M || n >= p.N) return;
-    const i32x4* from = g.part + (long long)t * g.splits * kTile + at;
-    i32x4 sum = from[0];
-    for (int s = 1; s < g.splits; ++s) sum += from[(long long)s * kTile];
-    i8_store<BF16>(p, m, n, sum);
+    const __amdgpu_buffer_rsrc_t from = i8_rsrc(g.part + (long long)t * g.splits * kTile, (long long)g.splits * kTile * 16);
+    u32x4 piece[kTMaxSplits];
+#pragma unroll
+    for (int s = 0; s < kTMaxSplits; ++s) piece[s] = i8_load<0>(from, (s * kTile + at) * 16);
+    float ws[4], bias[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int c = min(n + r, p.N - 1);
+        ws[r] = p.w_scale[c];
+        bias[r] = p.bias ? p.bias[c] : 0.f;
+    }
+    i32x4 sum = (i32x4)piece[0];
+#pragma unroll
+    for (int s = 1; s < kTMaxSplits; ++s) sum += (i32x4)piece[s];
+    i8_store_scaled<BF16>(p, m, n, sum, p.a_scale[m], ws, bias);
 }
 
 // Which tiles, and in how many pieces along K: the fewest microseconds by what was measured. A stage of one tile
@@ -313,7 +325,6 @@ struct TileCost {
     float alone, beside;
 };
 constexpr TileCost kTileCosts[] = {{4, 2, 0.80f, 0.84f}, {4, 1, 0.47f, 0.47f}, {2, 1, 0.33f, 0.34f}, {1, 1, 0.26f, 0.25f}};
-constexpr int kTMaxSplits = 12, kTMinStages = 4;  // of a piece
 
 static TileChoice choose_tile(int M, int K, int N) {
     const int cus = device_cus(), stages = i8_steps(K) / 2;
