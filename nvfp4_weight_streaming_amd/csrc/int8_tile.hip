@@ -156,18 +156,24 @@ __device__ __forceinline__ void tile_sum(i32x16 (&acc)[TI][TJ], int8_t* lds, con
     t_barrier();
 }
 
-// The scales and bias of the tile at (m0, n0), after the ring in LDS.
+// The scales and bias of the tile at (m0, n0), after the ring in LDS; thread i's of them, in flight while the
+// sums are made.
 struct TileScales {
     float row[128], channel[256], bias[256];
 };
-template <int TI, int TJ>
-__device__ __forceinline__ void tile_scales_load(TileScales& s, const I8Args& p, int m0, int n0) {
+struct TileScale {
+    float row, channel, bias;
+};
+__device__ __forceinline__ TileScale tile_scale_load(const I8Args& p, int m0, int n0) {
     const int i = threadIdx.x, n = min(n0 + i, p.N - 1);
-    if (i < 32 * TI) s.row[i] = p.a_scale[min(m0 + i, p.M - 1)];
-    if (i < 128 * TJ) {
-        s.channel[i] = p.w_scale[n];
-        s.bias[i] = p.bias ? p.bias[n] : 0.f;
-    }
+    return {p.a_scale[min(m0 + i, p.M - 1)], p.w_scale[n], p.bias ? p.bias[n] : 0.f};
+}
+template <int TI, int TJ>
+__device__ __forceinline__ void tile_scale_put(TileScales& s, const TileScale& mine) {
+    const int i = threadIdx.x;
+    if (i < 32 * TI) s.row[i] = mine.row;
+    if (i < 128 * TJ) s.channel[i] = mine.channel, s.bias[i] = mine.bias;
+    __syncthreads();
 }
 
 // The tile's outputs.  A lane has four consecutive ones of a row in each quarter of a product, lanes
@@ -266,9 +272,10 @@ __global__ __launch_bounds__(256, 2) void int8_tile_kernel(I8Args p, TilePlan g)
     for (int i = 0; i < TI; ++i)
 #pragma unroll
         for (int j = 0; j < TJ; ++j) acc[i][j] = i32x16{};
-    if (g.splits == 1) tile_scales_load<TI, TJ>(scales, p, m0, n0);
+    const TileScale mine = tile_scale_load(p, m0, n0);
     tile_sum<TI, TJ>(acc, lds, p, m0, n0, u0, u1);
     if (g.splits == 1) {
+        tile_scale_put<TI, TJ>(scales, mine);
         tile_store<TI, TJ, BF16>(acc, lds, kRing / 4, scales, p, m0, n0);
         return;
     }
@@ -312,11 +319,12 @@ __global__ __launch_bounds__(256) void int8_join_kernel(I8Args p, TilePlan g) {
 // takes `alone` where a compute unit has one of them, and `beside` in each unit's time where it has
 // several; pieces cost a second kernel and their sums' way through memory.
 // Over 25 shapes (64 < M <= 2048, 512 <= K <= 17408, 256 <= N <= 34816) this comes within 1.6% of the best of
-// 50 choices on average, 8% at most:
+// 50 choices on average, 8% at most (below 64 rows, where memory bounds all of them, 13%: 64 x 5120 x 34816 takes
+// 50.6 us in the 32 x 128 tiles chosen, 45 in 128 x 256):
 //   2048 x 5120 x 34816   322 us in 128 x 256 tiles, 389 in 128 x 128
 //   2048 x 5120 x 5120    60.0 in 128 x 128, 72.5 in 64 x 128
-//   256 x 5120 x 7168     15.8 in 64 x 128, 18.9 in 32 x 128, 20.9 in 128 x 128
-//   128 x 17408 x 5120    27.0 in 6 pieces of 128 x 128, 79.6 in one
+//   256 x 5120 x 7168     15.3 in 64 x 128, 18.9 in 32 x 128, 20.9 in 128 x 128
+//   128 x 17408 x 5120    27.3 in 6 pieces of 128 x 128, 79.6 in one
 struct TileChoice {
     int ti, tj, splits;
 };
