@@ -11,7 +11,7 @@
 // past K and N.  What is read of a row past K (the next row, or zeros past the last) meets a zero.
 //
 // Up to 16 rows the weights are streamed (here); above, tiles run on the matrix cores
-// (int8_tile.hip): 64 rows of 17408 x 5120 take 23 us there.  16 of them take 23.7 here and 21.6 there, 16 of
+// (int8_tile.hip): 64 rows of 17408 x 5120 take 21.4 us there.  16 of them take 23.7 here and 20.7 there, 16 of
 // 5120 x 152064 129 and 140, 8 of 5120 x 34816 28.8 and 41.
 #include "int8_device.h"
 
