@@ -10,7 +10,7 @@
 // Packed weights lie one 1 KiB operand after the other as a wave reads them, zeros
 // past K and N.  What is read of a row past K (the next row, or zeros past the last) meets a zero.
 //
-// Up to 16 rows the weights are streamed (here); above, tiles run on the matrix cores
+// Up to 16 rows, and some widths up to 32, the weights are streamed (here); above, tiles run on the matrix cores
 // (int8_tile.hip): 64 rows of 17408 x 5120 take 21.4 us there.  16 of them take 23.7 here and 20.7 there, 16 of
 // 5120 x 152064 129 and 140, 8 of 5120 x 34816 28.8 and 41.
 #include "int8_device.h"
@@ -18,7 +18,6 @@
 namespace nvfp4 {
 
 constexpr int kI8MaxSplit = 16;    // waves over K
-constexpr int kI8StreamRows = 16;  // most rows of the streaming kernel
 
 // One 16-byte piece a thread; UNPACK: the other way, and no padding.
 template <bool UNPACK>
@@ -39,17 +38,17 @@ __global__ __launch_bounds__(256) void int8_pack_kernel(const int8_t* __restrict
     }
 }
 
-// Up to 16 rows: the weights are streamed once.  The waves of a workgroup split K, and each holds the
+// G groups of 16 rows: the weights are streamed once.  The waves of a workgroup split K, and each holds the
 // rows' part of its own steps (NP at most) in registers for all of the column tiles that the workgroup takes, one after
 // the other; the waves' sums meet in LDS.  A wave has U steps of weights in flight, those of the
 // next tile behind those of this one.
 //
 // (Read anew for each tile, rows cost as much of the vector cache's time as weights: 8 rows of 5120 x 34816 took
 // 35.0 us, and 29.2 with one load of them.)
-template <int NP, int U, bool BF16>
+template <int NP, int U, int G, bool BF16>
 __global__ __launch_bounds__(1024) void int8_stream_kernel(I8Args p) {
     static_assert(NP % U == 0, "a step of any tile has one place");
-    extern __shared__ i32x4 sums[];  // [2][wave][lane]
+    extern __shared__ i32x4 sums[];  // [2][wave][G][lane]
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), lane = threadIdx.x & 63;
     const int waves = blockDim.x >> 6;
     const int s0 = p.steps * wave / waves, n = p.steps * (wave + 1) / waves - s0;
@@ -57,70 +56,87 @@ __global__ __launch_bounds__(1024) void int8_stream_kernel(I8Args p) {
     // Steps past the wave's last one are read past the end of what their resource covers: zeros, with no
     // branch and no traffic.
     const __amdgpu_buffer_rsrc_t ra = i8_rsrc(p.a, (long long)(p.M - 1) * p.a_ld + p.K);
-    const int arow = min(row, p.M - 1) * (int)p.a_ld + s0 * kI8Step + 16 * quarter;
-    u32x4 av[NP], wv[U];
+    u32x4 av[G][NP], wv[U];
 #pragma unroll
-    for (int i = 0; i < NP; ++i) av[i] = i8_load<0>(ra, i < n ? arow + i * kI8Step : 0x7FFFFFFF);
+    for (int g = 0; g < G; ++g) {
+        const int at = min(16 * g + row, p.M - 1) * (int)p.a_ld + s0 * kI8Step + 16 * quarter;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) av[g][i] = i8_load<0>(ra, i < n ? at + i * kI8Step : 0x7FFFFFFF);
+    }
     const long long stride = (long long)p.steps * kI8Bytes;
     const int8_t* w = p.w + blockIdx.x * stride + s0 * kI8Bytes;
     const long long jump = gridDim.x * stride;
     __amdgpu_buffer_rsrc_t rw = i8_rsrc(w, n * kI8Bytes);
 #pragma unroll
     for (int i = 0; i < U; ++i) wv[i] = i8_load<kI8Stream>(rw, 16 * lane + i * kI8Bytes);
-    const float as = p.a_scale[min(row, p.M - 1)];
-    int turn = 0, half = 0;  // the wave that stores the tile's outputs, and its place in LDS
+    int turn = 0, half = 0;  // the first wave that stores the tile's outputs (each a group of rows), and their place in LDS
     for (int tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
         w += jump;
         const __amdgpu_buffer_rsrc_t next = i8_rsrc(w, tile + (int)gridDim.x < p.tiles ? n * kI8Bytes : 0);
         const int c = tile * 16 + 4 * quarter;
-        float ws[4], bias[4];
-        if (wave == turn) {
+        const int mine = wave < turn ? wave - turn + waves : wave - turn;
+        float ws[4], bias[4], as = 0.f;
+        if (mine < G) {
+            as = p.a_scale[min(16 * mine + row, p.M - 1)];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 ws[r] = p.w_scale[min(c + r, p.N - 1)];
                 bias[r] = p.bias ? p.bias[min(c + r, p.N - 1)] : 0.f;
             }
         }
-        i32x4 acc = {};
+        i32x4 acc[G] = {};
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-            acc = __builtin_amdgcn_mfma_i32_16x16x64_i8((i32x4)wv[i % U], (i32x4)av[i], acc, 0, 0, 0);
+#pragma unroll
+            for (int g = 0; g < G; ++g) acc[g] = __builtin_amdgcn_mfma_i32_16x16x64_i8((i32x4)wv[i % U], (i32x4)av[g][i], acc[g], 0, 0, 0);
             wv[i % U] = i8_load<kI8Stream>(i + U < NP ? rw : next, 16 * lane + (i + U) % NP * kI8Bytes);
         }
         rw = next;
-        sums[(half * waves + wave) * 64 + lane] = acc;
+#pragma unroll
+        for (int g = 0; g < G; ++g) sums[((half * waves + wave) * G + g) * 64 + lane] = acc[g];
         // (no fence, which would wait for the weights in flight)
         __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
         asm volatile("" ::: "memory");
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
-        if (wave == turn) {
-            i32x4 all = sums[half * waves * 64 + lane];
-            for (int v = 1; v < waves; ++v) all += sums[(half * waves + v) * 64 + lane];
-            i8_store_scaled<BF16>(p, row, c, all, as, ws, bias);
+        if (mine < G) {
+            const i32x4* from = sums + (half * waves * G + mine) * 64 + lane;
+            i32x4 all = from[0];
+            for (int v = 1; v < waves; ++v) all += from[v * G * 64];
+            i8_store_scaled<BF16>(p, 16 * mine + row, c, all, as, ws, bias);
         }
-        turn = turn + 1 == waves ? 0 : turn + 1;
+        turn += G;
+        if (turn >= waves) turn -= waves;
         half ^= 1;
     }
 }
 
-template <int NP, int U>
+template <int NP, int U, int G>
 static int launch_stream(const I8Args& p, bool bf16, int waves, hipStream_t s) {
     // As many workgroups as the device holds at once, or one for each tile.
     const int room = device_cus() * (16 / waves);
     const dim3 grid((unsigned)(p.tiles < room ? p.tiles : room)), block(64 * waves);
-    const size_t lds = (size_t)2 * waves * 64 * sizeof(i32x4);
+    const size_t lds = (size_t)2 * waves * G * 64 * sizeof(i32x4);
     if (bf16)
-        hipLaunchKernelGGL((int8_stream_kernel<NP, U, true>), grid, block, lds, s, p);
+        hipLaunchKernelGGL((int8_stream_kernel<NP, U, G, true>), grid, block, lds, s, p);
     else
-        hipLaunchKernelGGL((int8_stream_kernel<NP, U, false>), grid, block, lds, s, p);
+        hipLaunchKernelGGL((int8_stream_kernel<NP, U, G, false>), grid, block, lds, s, p);
     NVFP4_HIP(hipGetLastError());
     return NVFP4_OK;
 }
 
 // Steps a wave, at most.
 constexpr int kI8MaxSteps = 20;
-static bool int8_streams(int M, int K) { return M <= kI8StreamRows && i8_steps(K) <= kI8MaxSplit * kI8MaxSteps; }
+// 17 to 32 rows are streamed where a wave has 5 to 8 steps of them and each workgroup two tiles or more: 32 rows of
+// 5120 x 34816 take 34.0 us here and 44.9 as tiles, of 8192 x 100000 139 and 161, 20 of 5120 x 12288 14.3 and 18.9; 32 of
+// 5120 x 65536 58.5 and 57.3. With fewer tiles or steps they would be slower: 32 of 5120 x 5120 11.9 and 10.2, of
+// 2048 x 17408 13.1 and 8.3. (64 rows, four groups of 5 steps: 64 x 5120 x 34816 42 and 51, x 17408 26.5 and 24.3,
+// 1024 x 32000 14.8 and 8.7.)
+static bool int8_streams(int M, int K, int N) {
+    const int steps = i8_steps(K);
+    if (M <= 16) return steps <= kI8MaxSplit * kI8MaxSteps;
+    return M <= 32 && steps > 4 * kI8MaxSplit && steps <= 8 * kI8MaxSplit && i8_tiles(N) >= 2 * device_cus();
+}
 
 }  // namespace nvfp4
 
@@ -161,7 +177,7 @@ int nvfp4_int8_unpack(const int8_t* packed_dev, int K, int N, int8_t* codes_dev,
 
 size_t nvfp4_int8_gemm_workspace_bytes(int M, int K, int N) {
     if (M < 1 || !i8_shape(K, N)) return 0;
-    return int8_streams(M, K) ? 0 : int8_tile_ws(M, K, N);
+    return int8_streams(M, K, N) ? 0 : int8_tile_ws(M, K, N);
 }
 
 int nvfp4_int8_gemm(const int8_t* a_dev, int64_t a_ld, const float* a_scale_dev, const int8_t* w_packed_dev,
@@ -203,7 +219,7 @@ int nvfp4_int8_gemm(const int8_t* a_dev, int64_t a_ld, const float* a_scale_dev,
     p.vec = ((uintptr_t)out_dev & (bf16 ? 7 : 15)) == 0 && out_ld % 4 == 0;
     p.wide = ((uintptr_t)out_dev & 15) == 0 && out_ld % (bf16 ? 8 : 4) == 0;
     const hipStream_t s = (hipStream_t)stream;
-    if (!int8_streams(M, K)) return launch_int8_tile(p, bf16, workspace_dev, s);
+    if (!int8_streams(M, K, N)) return launch_int8_tile(p, bf16, workspace_dev, s);
     // Four to eight steps a wave, where 16 waves are enough for that: 8 x 5120 x 152064 takes 121 us
     // with 16 waves of 5 steps, 127 with 4 of 20; 8 x 1024 x 100000 18.4 with 4 of 4, 32 with 16 of 1. And
     // waves for every compute unit, where there are few tiles.
@@ -211,10 +227,11 @@ int nvfp4_int8_gemm(const int8_t* a_dev, int64_t a_ld, const float* a_scale_dev,
     while (waves < kI8MaxSplit && (p.steps > 8 * waves || ((long long)p.tiles * waves < 4096 && p.steps >= 8 * waves))) waves *= 2;
     if (waves > p.steps) waves = p.steps;
     const int most = (p.steps + waves - 1) / waves;
-    if (most <= 4) return launch_stream<4, 4>(p, bf16, waves, s);
-    if (most <= 8) return launch_stream<8, 8>(p, bf16, waves, s);
-    if (most <= 12) return launch_stream<12, 4>(p, bf16, waves, s);
-    return launch_stream<20, 4>(p, bf16, waves, s);
+    if (M > 16) return launch_stream<8, 8, 2>(p, bf16, waves, s);
+    if (most <= 4) return launch_stream<4, 4, 1>(p, bf16, waves, s);
+    if (most <= 8) return launch_stream<8, 8, 1>(p, bf16, waves, s);
+    if (most <= 12) return launch_stream<12, 4, 1>(p, bf16, waves, s);
+    return launch_stream<20, 4, 1>(p, bf16, waves, s);
 }
 
 }  // extern "C"

@@ -76,6 +76,26 @@ def test_every_number_of_stages(nv, M):
         _check(out, y, s, False, (M, K, N))
 
 
+@pytest.mark.parametrize("M", [17, 24, 31, 32, 33])
+@pytest.mark.parametrize("K,N", [(4112, 8192), (5120, 8200), (6000, 12289), (8192, 8192), (8208, 8192)])
+def test_streamed_groups_of_rows(nv, M, K, N):
+    """Widths that are streamed in two groups of rows, and their neighbours that are not; wide matrices by sampled columns."""
+    import torch
+    a, sa, w, sw, bias = _case(M + K + N, M, K, N)
+    weight = nv.Int8Weight.from_canonical(dev(w), dev(sw))
+    at = np.unique(np.concatenate([np.arange(24), np.arange(N - 40, N), np.random.default_rng(M).integers(0, N, 200)]))
+    y, s = oracle.int8_gemm(a, sa, w[at], sw[at], bias[at])
+    for bf16 in (False, True):
+        out, canary = canary_out(M, N, torch.bfloat16 if bf16 else torch.float32)
+        nv.int8_gemm(dev(a), dev(sa), weight, dtype=out.dtype, bias=dev(bias), out=out)
+        torch.cuda.synchronize()
+        canary((M, K, N))
+        _check(out[:, torch.from_numpy(at).cuda()], y, s, bf16, (M, K, N, bf16))
+        if not bf16:
+            part = nv.int8_gemm(dev(a[:9]), dev(sa[:9]), weight, dtype=torch.float32, bias=dev(bias))
+            assert torch.equal(part, out[:9])
+
+
 # The round's matrices and the head's width, by sampled columns; prefill chunks with ragged ends.
 @pytest.mark.parametrize("M,K,N", [(8, 5120, 7168), (3, 6144, 5120), (64, 17408, 5120), (8, 5120, 152064), (24, 5120, 34816),
                                    (2048, 5120, 7168), (2048, 6144, 5120), (1000, 17408, 5120), (333, 5136, 6001), (2048, 5120, 17408)])
