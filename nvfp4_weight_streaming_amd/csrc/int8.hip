@@ -11,8 +11,8 @@
 // past K and N.  What is read of a row past K (the next row, or zeros past the last) meets a zero.
 //
 // Up to 16 rows, and some widths up to 32, the weights are streamed (here); above, tiles run on the matrix cores
-// (int8_tile.hip): 64 rows of 17408 x 5120 take 21.4 us there.  16 of them take 23.7 here and 20.7 there, 16 of
-// 5120 x 152064 129 and 140, 8 of 5120 x 34816 28.8 and 41.
+// (int8_tile.hip): 16 rows of 5120 x 152064 take 129 us here and 140 there, 8 of 5120 x 34816 28.8 and 41, 1 of 5120 x 7168 8.8
+// and 10.4.
 #include "int8_device.h"
 
 namespace nvfp4 {
@@ -127,6 +127,10 @@ static int launch_stream(const I8Args& p, bool bf16, int waves, hipStream_t s) {
 
 // Steps a wave, at most.
 constexpr int kI8MaxSteps = 20;
+// Of 5 to 16 rows, those of more than 12 steps a wave are streamed where workgroups have more than 1.25 tiles on average: with
+// few, a wave first waits for its rows and then, 4 steps at a time, for its one tile. 16 rows of 17408 x 5120 take 23.5 us
+// here and 20.5 as tiles, of 20480 x 2048 18.3 and 11.8, 8 of 17408 x 2048 13.3 and 10.7; 16 of 17408 x 7168 25.3 and 26.5, 1 of 17408 x
+// 5120 19.6 and 20.5, 8 of 12288 x 2048 9.3 and 9.8.
 // 17 to 32 rows are streamed where a wave has 5 to 8 steps of them and each workgroup two tiles or more: 32 rows of
 // 5120 x 34816 take 34.0 us here and 44.9 as tiles, of 8192 x 100000 139 and 161, 20 of 5120 x 12288 14.3 and 18.9; 32 of
 // 5120 x 65536 58.5 and 57.3. With fewer tiles or steps they would be slower: 32 of 5120 x 5120 11.9 and 10.2, of
@@ -134,8 +138,8 @@ constexpr int kI8MaxSteps = 20;
 // 1024 x 32000 14.8 and 8.7.)
 static bool int8_streams(int M, int K, int N) {
     const int steps = i8_steps(K);
-    if (M <= 16) return steps <= kI8MaxSplit * kI8MaxSteps;
-    return M <= 32 && steps > 4 * kI8MaxSplit && steps <= 8 * kI8MaxSplit && i8_tiles(N) >= 2 * device_cus();
+    if (M <= 16 && (M <= 4 || steps <= 12 * kI8MaxSplit || 4ll * i8_tiles(N) > 5ll * device_cus())) return steps <= kI8MaxSplit * kI8MaxSteps;
+    return M > 16 && M <= 32 && steps > 4 * kI8MaxSplit && steps <= 8 * kI8MaxSplit && i8_tiles(N) >= 2 * device_cus();
 }
 
 }  // namespace nvfp4

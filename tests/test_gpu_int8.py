@@ -96,6 +96,18 @@ def test_streamed_groups_of_rows(nv, M, K, N):
             assert torch.equal(part, out[:9])
 
 
+@pytest.mark.parametrize("M", [1, 4, 5, 9, 16])
+@pytest.mark.parametrize("K,N", [(12288, 100), (12304, 100), (17408, 2048), (17408, 6400), (20480, 33), (20496, 33)])
+def test_long_rows(nv, M, K, N):
+    """Sums of more than 12 steps a wave, streamed or as tiles."""
+    import torch
+    a, sa, w, sw, bias = _case(M + K + N, M, K, N)
+    out = nv.int8_gemm(dev(a), dev(sa), nv.Int8Weight.from_canonical(dev(w), dev(sw)), dtype=torch.float32, bias=dev(bias))
+    at = np.unique(np.concatenate([np.arange(min(N, 24)), np.arange(max(0, N - 40), N)]))
+    y, s = oracle.int8_gemm(a, sa, w[at], sw[at], bias[at])
+    _check(out[:, torch.from_numpy(at).cuda()], y, s, False, (M, K, N))
+
+
 # The round's matrices and the head's width, by sampled columns; prefill chunks with ragged ends.
 @pytest.mark.parametrize("M,K,N", [(8, 5120, 7168), (3, 6144, 5120), (64, 17408, 5120), (8, 5120, 152064), (24, 5120, 34816),
                                    (2048, 5120, 7168), (2048, 6144, 5120), (1000, 17408, 5120), (333, 5136, 6001), (2048, 5120, 17408)])
