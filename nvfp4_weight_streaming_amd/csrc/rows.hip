@@ -14,9 +14,9 @@
 //
 // A row is read once: 64, 256 or 1024 threads hold up to 3 vectors of 8 values each (1536, 6144, 24576 values);
 // longer rows are read again for each step.  From 4097 to 8192 values 1024 threads hold a vector each: always above
-// 6144, where three would leave a compute unit fewer rows (codes of 1024 SwiGLU rows of 8192: 15.4 us, 20.1 so; of 8: 5.4 and 6.5),
-// and below it for few rows, for less work one after the other (codes of 64 rows of 5120: 4.4 us, 6.3 with 256 threads;
-// 512 rows 6.4 and 6.8, 1024 rows 10.7 and 9.6; 8 rows of 2048 would take 4.3 and 3.7).
+// 6144 (codes of 1026 rows of 6400: 11.5 us, 12.4 with room for three), and below it for few rows, for less work one after the
+// other (codes of 65 rows of 5120: 5.1 us, 7.1 with 256 threads; 513 rows 6.5 and 7.4, 1025 rows 10.8 and 9.0; 8 rows of 2048
+// would take 4.3 and 3.7).
 #include "select_device.h"
 #include "swiglu_device.h"
 
@@ -310,6 +310,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T, T == 1024 && B16 && MODE != kRow
             if (!HELD) load(c, false);
 #pragma unroll
             for (int j = 0; j < R; ++j) {
+                if (row_at<T, VEC>(c * R + j, t, 0) >= K) continue;
                 float y[8];
                 uint32_t open = 0;  // elements that may round either way
 #pragma unroll
@@ -321,7 +322,6 @@ __global__ __launch_bounds__(T < 256 ? 256 : T, T == 1024 && B16 && MODE != kRow
                     const bool sound = fabsf(h[j][e] * f32) >= kRowLeast && fabsf(y[e]) >= kRowLeast && fabsf(y[e]) <= kRowMost;
                     open |= (sound && far) || (h[j][e] == 0.f && y[e] == 0.f) ? 0u : 1u << e;
                 }
-                if (row_at<T, VEC>(c * R + j, t, 0) >= K) open = 0;
                 while (open) {
                     const int at = __ffs(open) - 1, i = row_at<T, VEC>(c * R + j, t, at);
                     open &= open - 1;
@@ -345,6 +345,10 @@ __global__ __launch_bounds__(T < 256 ? 256 : T, T == 1024 && B16 && MODE != kRow
             for (int j = 0; j < R; ++j) {
                 float side = 0.f;
                 peak[j] = 0;
+                eps[j] = 0.f;
+                fine[j] = true;
+                // (a vector past the row's end, as most waves' third of 17408 values: with them 2048 such SwiGLU rows took 49 us, and take 44)
+                if (row_at<T, VEC>(c * R + j, t, 0) >= K) continue;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     // (past the row's end x is 0, and so is y, or NaN as the row's others)
@@ -354,7 +358,6 @@ __global__ __launch_bounds__(T < 256 ? 256 : T, T == 1024 && B16 && MODE != kRow
                     if (MODE == kRowSwiglu) side = fmaxf(side, -h[j][e]);
                 }
                 fine[j] = peak[j] <= __float_as_uint(kRowMost);
-                eps[j] = 0.f;
                 if (MODE == kRowNorm) {
                     // Four roundings, the factor's, the sum's and two products'; a first product below fp32's range
                     // makes no value that matters.
