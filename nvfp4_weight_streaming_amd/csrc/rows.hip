@@ -208,8 +208,10 @@ constexpr float row_floor() {
 }
 
 // One row per T threads, R vectors a thread.  HELD: the row lies in registers between the steps.
+// (Two rows of 1024 threads a compute unit where rows are held; rows read again need more registers than that leaves: 1024 SwiGLU rows
+// of 32768 took 153 us so, and take 85.)
 template <int T, int R, int MODE, int OUT, bool VEC, bool HELD, bool B16>
-__global__ __launch_bounds__(T < 256 ? 256 : T, T == 1024 && B16 && MODE != kRowNorm ? 8 : 1) void rows_kernel(RowArgs a) {
+__global__ __launch_bounds__(T < 256 ? 256 : T, T == 1024 && B16 && HELD && MODE != kRowNorm ? 8 : 1) void rows_kernel(RowArgs a) {
     constexpr int kPer = T < 256 ? 256 / T : 1;  // rows per workgroup
     __shared__ u64 lds[2][T / 64];
     __shared__ u64 top;
