@@ -349,7 +349,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T, T == 1024 && B16 && HELD && MODE
                 peak[j] = 0;
                 eps[j] = 0.f;
                 fine[j] = true;
-                // (a vector past the row's end, as most waves' third of 17408 values: with them 2048 such SwiGLU rows took 49 us, and take 44)
+                // (a vector past the row's end, as most waves' third of 17408 values: with them 2048 such SwiGLU rows took 49 us, and take 44 to 46)
                 if (row_at<T, VEC>(c * R + j, t, 0) >= K) continue;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
