@@ -94,7 +94,9 @@ __global__ __launch_bounds__(1024) void int8_stream_kernel(I8Args p) {
         rw = next;
 #pragma unroll
         for (int g = 0; g < G; ++g) sums[((half * waves + wave) * G + g) * 64 + lane] = acc[g];
-        // (no fence, which would wait for the weights in flight)
+        // (no fence, which would wait for the weights in flight; the wait stands between two points that no access to
+        // memory is moved across, as its counter is of the sums above)
+        asm volatile("" ::: "memory");
         __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
         asm volatile("" ::: "memory");
         __builtin_amdgcn_s_barrier();
