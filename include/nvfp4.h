@@ -415,7 +415,7 @@ int nvfp4_int8_unpack(const int8_t* packed_dev, int K, int N, int8_t* codes_dev,
  *   w_packed_dev  : packed codes (nvfp4_int8_pack), 16-byte aligned
  *   out_dev       : fp32 or bf16 [M][out_ld], out_ld >= N
  *   workspace_dev : nvfp4_int8_gemm_workspace_bytes(M, K, N) bytes (16-byte aligned; may be 0),
- *                   any content; owned by the call while it runs.
+ *                   any content; owned by the call while it runs (0 bytes for sizes that the call refuses).
  * Few rows stream the weights once; more run tiles on the matrix cores, cut along K where they are few.  Results do
  * not depend on M, and repeat to the bit.  M = 0 launches nothing.  Asynchronous on `stream`. */
 size_t nvfp4_int8_gemm_workspace_bytes(int M, int K, int N);

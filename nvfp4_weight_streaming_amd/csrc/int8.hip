@@ -18,6 +18,7 @@
 namespace nvfp4 {
 
 constexpr int kI8MaxSplit = 16;    // waves over K
+constexpr int kI8MaxRows = 1 << 22;
 
 // One 16-byte piece a thread; UNPACK: the other way, and no padding.
 template <bool UNPACK>
@@ -182,7 +183,7 @@ int nvfp4_int8_unpack(const int8_t* packed_dev, int K, int N, int8_t* codes_dev,
 }
 
 size_t nvfp4_int8_gemm_workspace_bytes(int M, int K, int N) {
-    if (M < 1 || !i8_shape(K, N)) return 0;
+    if (M < 1 || M > kI8MaxRows || !i8_shape(K, N)) return 0;
     return int8_streams(M, K, N) ? 0 : int8_tile_ws(M, K, N);
 }
 
@@ -194,7 +195,7 @@ int nvfp4_int8_gemm(const int8_t* a_dev, int64_t a_ld, const float* a_scale_dev,
     if (K < 16 || K % 16 || K > NVFP4_INT8_MAX_K) return set_error(NVFP4_EINVAL, "K: %d is not a multiple of 16 in [16, %d]", K, NVFP4_INT8_MAX_K);
     if (N < 1 || N > (1 << 30)) return set_error(NVFP4_EINVAL, "N: %d outside [1, 2^30]", N);
     if (out_dtype != NVFP4_OUT_F32 && out_dtype != NVFP4_OUT_BF16) return set_error(NVFP4_EINVAL, "out_dtype: %d", out_dtype);
-    if (M > (1 << 22)) return set_error(NVFP4_EINVAL, "M: %d > 2^22", M);
+    if (M > kI8MaxRows) return set_error(NVFP4_EINVAL, "M: %d > 2^22", M);
     if (a_ld < K || a_ld % 16 || a_ld > (1 << 22)) return set_error(NVFP4_EINVAL, "a_ld: %lld is not a multiple of 16 in [K = %d, 2^22]", (long long)a_ld, K);
     if (out_ld < N) return set_error(NVFP4_EINVAL, "out_ld: %lld < N = %d", (long long)out_ld, N);
     if (M == 0) return NVFP4_OK;
