@@ -609,7 +609,8 @@ class Int8Weight:
 
     @classmethod
     def from_canonical(cls, codes, scale, stream=None):
-        """Pack a device int8 matrix [N][K] with its channels' fp32 scales [N]."""
+        """Pack a device int8 matrix [N][K] with its channels' fp32 scales [N].  Both are copied: the weight does not
+        change with the tensors that it was made of."""
         if stream is not None and codes.is_cuda:
             with _on(stream, codes.device):
                 return cls.from_canonical(codes, scale)
@@ -625,7 +626,7 @@ class Int8Weight:
         st = lib().nvfp4_int8_pack(codes.data_ptr(), K, N, packed.data_ptr(), T.stream(gpu))
         if st:
             _check(st)
-        return cls(packed, scale, K, N)
+        return cls(packed, scale.clone(), K, N)
 
     @classmethod
     def quantize(cls, w, stream=None):

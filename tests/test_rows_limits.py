@@ -18,3 +18,19 @@ def nv():
 @pytest.mark.parametrize("K,N", [(64, 64), (5120, 7168), (131056, 16), (131056, 1 << 30)])
 def test_workspace_of_more_rows_than_a_product_takes(nv, M, K, N):
     assert nv.nvfp4_int8_gemm_workspace_bytes(M, K, N) == 0
+
+
+def test_a_weight_keeps_nothing_of_the_callers(nv, monkeypatch):
+    """What the caller writes into the scales' buffer afterwards is not the weight's."""
+    import torch
+
+    from tests.test_rows_binding import _gpu_class, _recorded
+    OnGpu = _gpu_class()
+    seen = _recorded(nv, monkeypatch)
+    codes, scale = torch.zeros((48, 64), dtype=torch.int8).as_subclass(OnGpu), torch.arange(48.0).as_subclass(OnGpu)
+    w = nv.Int8Weight.from_canonical(codes, scale)
+    scale.zero_()
+    assert torch.equal(w.scale, torch.arange(48.0)) and w.scale.get_device() == 0
+    w.packed = w.packed.as_subclass(OnGpu)
+    nv.int8_gemm(codes[:3], scale[:3], w)
+    assert seen["nvfp4_int8_gemm"][4] == w.scale.data_ptr() != scale.data_ptr()
