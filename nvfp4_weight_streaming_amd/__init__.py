@@ -511,7 +511,7 @@ def rms_norm(x, weight, eps, residual=None, dtype=None, weight_offset=0.0, out=N
     added to, times ``weight + weight_offset`` ([K], fp32 or bf16).  ``dtype``: the output's, bfloat16 (as
     by default), float32, or int8 for codes with a scale each row.  Returns ``out``; ``(codes, scale)`` for
     int8; and the new residual stream as a last value if ``residual`` is given (``residual_out`` may be
-    ``residual`` itself).  A stream that is given is torch's current one during the call, so outputs belong
+    ``residual`` itself; by default it has the residual's stride, or, if that is more than 2 K, none between rows).  A stream that is given is torch's current one during the call, so outputs belong
     to it."""
     if stream is not None and x.is_cuda:
         with _on(stream, x.device):
@@ -548,7 +548,12 @@ def rms_norm(x, weight, eps, residual=None, dtype=None, weight_offset=0.0, out=N
             _refuse("residual: shape %s, not %s" % (tuple(residual.shape), (rows, K)))
         r_type = T.floats[residual.dtype]
         if residual_out is None:
-            residual_out = T.like(residual) if r_ld == K else residual.new_empty((rows, r_ld))[:, :K]
+            if r_ld > 2 * K:
+                # (both streams have one stride: a few columns of a wide buffer would take as much memory as it has)
+                residual, r_ld = residual.contiguous(), K
+                residual_out = residual
+            else:
+                residual_out = T.like(residual) if r_ld == K else residual.new_empty((rows, r_ld))[:, :K]
         elif _matrix(residual_out, "residual_out", gpu, (residual.dtype,)) != (shape, r_ld):
             _refuse("residual_out: not of the residual's shape, type and stride")
         r, r_out = residual.data_ptr(), residual_out.data_ptr()

@@ -34,3 +34,25 @@ def test_a_weight_keeps_nothing_of_the_callers(nv, monkeypatch):
     w.packed = w.packed.as_subclass(OnGpu)
     nv.int8_gemm(codes[:3], scale[:3], w)
     assert seen["nvfp4_int8_gemm"][4] == w.scale.data_ptr() != scale.data_ptr()
+
+
+@pytest.mark.parametrize("rows,ld,alike", [(3, 64, True), (3, 128, True), (3, 129, False), (3, 100000, False), (1, 100000, False)])
+def test_the_new_stream_takes_memory_for_its_rows(nv, monkeypatch, rows, ld, alike):
+    """A residual of a few columns of a wide buffer: the new one is not as wide."""
+    import struct
+
+    import torch
+
+    from tests.test_rows_binding import _gpu_class, _recorded
+    OnGpu = _gpu_class()
+    seen = _recorded(nv, monkeypatch)
+    r = torch.arange(rows * ld, dtype=torch.float32).view(rows, ld).as_subclass(OnGpu)[:, :64]
+    was = r.clone()
+    _, stream = nv.rms_norm(torch.zeros(rows, 64).as_subclass(OnGpu), torch.zeros(64).as_subclass(OnGpu), 1e-6, residual=r)
+    d = struct.unpack("PiqPPiqPiffPiqP", seen["nvfp4_rms_norm"][0])
+    assert stream.shape == r.shape and stream.untyped_storage().nbytes() <= 2 * rows * 64 * 4
+    assert d[4] == stream.data_ptr() != r.data_ptr() and d[6] == (ld if alike else 64)
+    assert (d[3] == r.data_ptr()) == (alike or rows == 1)
+    if d[3] == d[4]:
+        assert torch.equal(stream, was)  # what the call reads is the residual's values
+    assert torch.equal(r, was)
