@@ -10,9 +10,9 @@
 // Packed weights lie one 1 KiB operand after the other as a wave reads them, zeros
 // past K and N.  What is read of a row past K (the next row, or zeros past the last) meets a zero.
 //
-// Up to 16 rows, and some widths up to 32, the weights are streamed (here); above, tiles run on the matrix cores
-// (int8_tile.hip): 16 rows of 5120 x 152064 take 129 us here and 140 there, 8 of 5120 x 34816 28.8 and 41, 1 of 5120 x 7168 8.8
-// and 10.4.
+// Up to 16 rows, and up to 32 of some K and N, the weights are streamed (here): 16 rows of 5120 x 152064 take 129 us here and 140 as
+// tiles on the matrix cores (int8_tile.hip), 8 of 5120 x 34816 28.8 and 41, 1 of 5120 x 7168 8.8 and 10.4.  Tiles take all else:
+// more rows, 5 to 16 rows of a long K with few columns, and any number of rows of a K above 20480, whose part a wave could not hold.
 #include "int8_device.h"
 
 namespace nvfp4 {
@@ -135,8 +135,8 @@ constexpr int kI8MaxSteps = 20;
 // here and 20.5 as tiles, of 20480 x 2048 18.3 and 11.8, 8 of 17408 x 2048 13.3 and 10.7; 16 of 17408 x 7168 25.3 and 26.5, 1 of 17408 x
 // 5120 19.6 and 20.5, 8 of 12288 x 2048 9.3 and 9.8.
 // 17 to 32 rows are streamed where a wave has 5 to 8 steps of them and each workgroup two tiles or more: 32 rows of
-// 5120 x 34816 take 34.0 us here and 44.9 as tiles, of 8192 x 100000 139 and 161, 20 of 5120 x 12288 14.3 and 18.9; 32 of
-// 5120 x 65536 58.5 and 57.3. With fewer tiles or steps they would be slower: 32 of 5120 x 5120 11.9 and 10.2, of
+// 5120 x 34816 take 34.0 us here and 44.9 as tiles, of 8192 x 100000 139 and 161, 20 of 5120 x 12288 14.3 and 18.9; inside the rule
+// 32 of 5120 x 65536 lose 2%, 58.5 and 57.3. With fewer tiles or steps they would be slower: 32 of 5120 x 5120 11.9 and 10.2, of
 // 2048 x 17408 13.1 and 8.3. (64 rows, four groups of 5 steps: 64 x 5120 x 34816 42 and 51, x 17408 26.5 and 24.3,
 // 1024 x 32000 14.8 and 8.7.)
 static bool int8_streams(int M, int K, int N) {

@@ -1,4 +1,5 @@
-// The 8-bit product for more than 16 rows: tiles on the matrix cores.
+// The 8-bit product in tiles on the matrix cores: of more than 16 rows but for those that are streamed, of 5 to 16 rows of a long
+// K with few columns, and of any K above 20480.
 //
 // A workgroup of four waves takes 32 TI rows x 128 TJ outputs, K in stages of 128; each wave has
 // the rows and 32 TJ of the outputs, as TI x TJ products of v_mfma_i32_32x32x32_i8 for each 32 k.

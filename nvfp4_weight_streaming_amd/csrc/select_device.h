@@ -82,7 +82,7 @@ __device__ __forceinline__ u64 wave_insert(u64 kept, u64 key, bool take, int k, 
     return kept;
 }
 
-// Appends the wave's keys that are at least `bar` to a list in LDS (in no
+// Appends the wave's keys that have `take` to a list in LDS (in no
 // particular order); *count goes on past the end of its LIST places.
 template <int LIST>
 __device__ __forceinline__ void append_keys(u64 key, bool take, u64* list, int* count, int lane) {
