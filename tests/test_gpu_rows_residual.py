@@ -41,3 +41,33 @@ def test_a_stream_of_a_wide_buffer(nv, K, width, at):
         graph.replay()
         check(*out)
         assert torch.equal(wide, before)
+
+
+@pytest.mark.parametrize("K", [40, 1001, 1536, 5120, 7001, 17408, 24584, 30001])
+@pytest.mark.parametrize("name", ["bf16", "f32"])
+def test_streams_in_place(nv, K, name):
+    """The new stream in place of x, of the residual, and of both where they are one; the norm in place of x."""
+    import torch
+    rng = np.random.default_rng(K)
+    types = {"bf16": torch.bfloat16, "f32": torch.float32, "int8": torch.int8}
+    x, r = (oracle.to_type(rng.standard_normal((5, K)) * 3, name) for _ in range(2))
+    w = oracle.to_type(rng.standard_normal(K), "bf16")
+    put = lambda v, t: torch.from_numpy(v.astype(np.float32)).cuda().to(types[t])  # noqa: E731
+    wd = put(w, "bf16")
+    for out in ("bf16", "f32", "int8"):
+        for place in ("x", "residual", "one"):
+            xd = put(x, name)
+            rd = xd if place == "one" else put(r, name)
+            y, h = oracle.rms_norm(x, w, 1e-6, 0.0, x if place == "one" else r, name)
+            got = nv.rms_norm(xd, wd, 1e-6, residual=rd, residual_out=rd if place == "residual" else xd, dtype=types[out])
+            assert got[-1].data_ptr() == (rd if place == "residual" else xd).data_ptr()
+            assert np.array_equal(host(got[-1].float()), h), (K, out, place)
+            if out == "int8":
+                q, s = oracle.codes(y)
+                assert np.array_equal(host(got[1]), s) and np.array_equal(host(got[0]), q), (K, out, place)
+            else:
+                assert np.array_equal(host(got[0].float()), oracle.to_type(y, out)), (K, out, place)
+    xd = put(x, name)
+    y, _ = oracle.rms_norm(x, w, 1e-6)
+    nv.rms_norm(xd, wd, 1e-6, dtype=types[name], out=xd)
+    assert np.array_equal(host(xd.float()), oracle.to_type(y, name)), K

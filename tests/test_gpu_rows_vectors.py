@@ -87,3 +87,23 @@ def test_quantize(nv, rows, K, swiglu):
         got, scale = nv.int8_quantize(_dev(x, rows, name, pad), swiglu=swiglu)
         _same(scale, s, (rows, K, name, "scale"))
         _same(got, q, (rows, K, name, "codes"))
+
+
+@pytest.mark.parametrize("K", [1536, 4096, 5121])
+def test_rows_at_the_top_of_the_range(nv, K):
+    """Rows whose root mean square's inverse is below fp32's normal numbers, and keeps fewer bits there."""
+    import torch
+    rng = np.random.default_rng(K)
+    for name in ("bf16", "f32"):
+        x = (1 + 0.98 * rng.random((64, K))) * 2.0 ** 127 * rng.choice([-1, 1], (64, K))
+        x[1::2, ::3] *= 2.0 ** -rng.integers(0, 40, x[1::2, ::3].shape)
+        x, w = oracle.to_type(x, name), oracle.to_type(rng.standard_normal(K), "bf16")
+        assert np.isfinite(x).all() and (1 / np.sqrt((x * x).mean(axis=1)) < 2.0 ** -126).all()
+        y, _ = oracle.rms_norm(x, w, 0.0)
+        xd, wd = (torch.from_numpy(v.astype(np.float32)).cuda().to(_types()[t]) for v, t in ((x, name), (w, "bf16")))
+        for out in ("bf16", "f32"):
+            got = nv.rms_norm(xd, wd, 0.0, dtype=_types()[out])
+            assert np.array_equal(got.double().cpu().numpy(), oracle.to_type(y, out)), (K, name, out)
+        q, s = oracle.codes(y)
+        codes, scale = nv.rms_norm(xd, wd, 0.0, dtype=torch.int8)
+        assert np.array_equal(scale.cpu().numpy(), s) and np.array_equal(codes.cpu().numpy(), q), (K, name)
